@@ -179,6 +179,69 @@ int regtile_gemm_f16_ex(int algo, int trans_a, int trans_b, int M, int N, int K,
                         const uint16_t *A, int lda, const uint16_t *B, int ldb, float beta,
                         float *C, int ldc, void *stream);
 
+/*
+ * Block-scaled (MX) matrices: 4 or 8 bits an element and one power-of-two scale for each group of
+ * 32 consecutive columns of a row, as the OCP Microscaling Formats specification (v1.0) lays them
+ * out. A matrix of rows x cols values is two arrays of bytes:
+ *   Q, ldq   the codes, row r at Q + r * ldq. REGTILE_MX_FP4 holds E2M1 floats (sign, 2 exponent
+ *            bits, 1 mantissa bit: 0, .5, 1, 1.5, 2, 3, 4, 6), two to a byte with the even column in
+ *            the low half: (cols + 1) / 2 bytes a row. REGTILE_MX_INT8 holds signed 8-bit integers q
+ *            that stand for q / 64: cols bytes a row.
+ *   S, lds   the scales, row r at S + r * lds: one byte E for each 32 columns (the last group may be
+ *            short), (cols + 31) / 32 bytes a row. E stands for 2^(E - 127), 255 for NaN.
+ * ldq and lds are in bytes and at least those sizes (and 1); neither array needs any alignment. Bytes of a row
+ * past its size are neither read nor written. The second half of an odd row's last fp4 byte is
+ * written as 0 and never used.
+ */
+enum regtile_mx_format {
+    REGTILE_MX_FP4 = 0,  /* E2M1 elements: weights in 4.25 bits */
+    REGTILE_MX_INT8 = 1  /* 8-bit integer elements: activations in 8.25 bits */
+};
+enum regtile_mx_dtype { REGTILE_MX_F32 = 0, REGTILE_MX_BF16 = 1, REGTILE_MX_F16 = 2 };
+
+/*
+ * regtile_quantize_mx -- X (rows x cols, row-major, of `dtype`) to a block-scaled matrix. With a the
+ * largest magnitude of a group: E = floor(log2 a) + 127 - t, clamped to 0 .. 254 (t = 2 for fp4, 0 for
+ * int8; E = 0 for a = 0). fp4 elements are x / 2^(E - 127) rounded to the nearest E2M1 value, ties to
+ * the even code, saturating at 6; int8 elements 64 x / 2^(E - 127) rounded to the nearest integer,
+ * ties to even, saturating at +-127. A group with a NaN or an infinity gets E = 255 and zero codes.
+ *   format, dtype (args 1-2), rows, cols (3-4, >= 0), X, ldx (5-6, device, ldx >= max(1, cols)
+ *   elements, X aligned to its element), Q, ldq (7-8), S, lds (9-10), stream (11)
+ * regtile_dequantize_mx -- the values of a block-scaled matrix, rounded to the nearest value of
+ * `dtype` (fp32 and bf16 hold them exactly; fp16 overflows to infinity past 65504).
+ *   format, dtype (args 1-2), rows, cols (3-4), Q, ldq (5-6), S, lds (7-8), X, ldx (9-10),
+ *   stream (11)
+ * Returns and conventions as everywhere above; rows == 0 or cols == 0 launches nothing. X must not
+ * overlap Q or S.
+ */
+int regtile_quantize_mx(int format, int dtype, int rows, int cols, const void *X, int ldx,
+                        uint8_t *Q, int ldq, uint8_t *S, int lds, void *stream);
+int regtile_dequantize_mx(int format, int dtype, int rows, int cols, const uint8_t *Q, int ldq,
+                          const uint8_t *S, int lds, void *X, int ldx, void *stream);
+
+/*
+ * regtile_gemm_bf16_mx / regtile_gemm_f16_mx -- C = alpha*op(A)*op(B) + beta*C with a bf16 / fp16 A,
+ * a block-scaled B and fp32 accumulation on MFMA fragments. B's values are taken in A's type: bf16
+ * holds each of them exactly, fp16 those within its range (smaller ones round to nearest, larger
+ * ones are infinite), so the products are exact. The three products of a linear layer
+ * y = x W^T whose weights (N_out x N_in) or input (tokens x N_in) are block-scaled:
+ *   y  = x W^T    trans_a 0, trans_b 1, B = W (stored N x K);
+ *   dx = dy W     trans_a 0, trans_b 0, B = W (stored K x N);
+ *   dW = dy^T x   trans_a 1, trans_b 0, B = x (stored K x N), beta 1 to accumulate.
+ *   format   (arg 1) a regtile_mx_format value
+ *   trans_a  (arg 2) as in regtile_gemm_bf16_ex;  trans_b (arg 3) 0: B stored K x N, groups along N;
+ *            1: B stored N x K, groups along K
+ *   M, N, K, alpha, A, lda (args 4-9), Q, ldq, S, lds (10-13), beta, C, ldc (14-16), stream (17)
+ *   as above: 0 sizes, alpha == 0 and beta == 0 as for gemm_bf16.
+ * Every output is summed in a fixed order: repeated calls give identical bits.
+ */
+int regtile_gemm_bf16_mx(int format, int trans_a, int trans_b, int M, int N, int K, float alpha,
+                         const uint16_t *A, int lda, const uint8_t *Q, int ldq, const uint8_t *S,
+                         int lds, float beta, float *C, int ldc, void *stream);
+int regtile_gemm_f16_mx(int format, int trans_a, int trans_b, int M, int N, int K, float alpha,
+                        const uint16_t *A, int lda, const uint8_t *Q, int ldq, const uint8_t *S,
+                        int lds, float beta, float *C, int ldc, void *stream);
+
 /* Name of the kernel the calling thread launched last ("none" before the first launch,
  * "quick-return" when nothing was launched). Static storage; do not free. */
 const char *regtile_last_kernel(void);

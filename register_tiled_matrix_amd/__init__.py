@@ -16,6 +16,13 @@ Entry points (same names as the C ABI):
   views and passes the layout to the ``regtile_gemm_*_ex`` entry points.
 * ``gemm_f16(A, B, C=None, alpha=1.0, beta=0.0, algo=ALGO_BF16_AUTO)`` the same with
   float16 A and B (IEEE binary16); the algorithm values are the bf16 ones.
+* ``gemm_bf16_mx(A, B, C=None, alpha=1.0, beta=0.0)`` / ``gemm_f16_mx`` the same products with a
+  block-scaled B (``MXMatrix``: 4 or 8 bits an element, one power-of-two scale per group of 32 along
+  its rows). For a linear layer with weights ``W`` held as an MXMatrix (out x in):
+  ``y = gemm_bf16_mx(x, W.t())`` and ``dx = gemm_bf16_mx(dy, W)``; for an input ``X`` kept as an MXMatrix
+  (tokens x in): ``dW = gemm_bf16_mx(dy.t(), X)``.
+* ``quantize_mx(X, format)`` -> MXMatrix and ``dequantize_mx(Q, dtype=torch.bfloat16)``; ``MX_FP4`` holds
+  weights in 4.25 bits, ``MX_INT8`` activations (a checkpoint for the backward pass) in 8.25.
 * ``gemm_f32_raw`` / ``gemm_bf16_raw`` / ``gemm_f16_raw`` take the C arguments verbatim
   (integers for pointers).
 * ``last_kernel()``, ``last_kernel_info()`` (registers, LDS, scratch and occupancy of that
@@ -38,16 +45,22 @@ __all__ = [
     "gemm_f32", "gemm_bf16", "gemm_f16", "gemm_f32_raw", "gemm_bf16_raw", "gemm_f16_raw",
     "regtile_gemm_f32_algo", "regtile_gemm_bf16_algo", "regtile_gemm_f16_algo",
     "regtile_gemm_f32_ex", "regtile_gemm_bf16_ex", "regtile_gemm_f16_ex",
+    "MX_FP4", "MX_INT8", "MX_GROUP", "MXMatrix", "quantize_mx", "dequantize_mx", "gemm_bf16_mx", "gemm_f16_mx",
+    "regtile_quantize_mx", "regtile_dequantize_mx", "regtile_gemm_bf16_mx", "regtile_gemm_f16_mx",
     "last_kernel", "last_kernel_info", "strerror", "version", "EXPORTED_SYMBOLS",
 ]
 
 ALGO_F32_AUTO, ALGO_F32_NAIVE, ALGO_F32_LDS, ALGO_F32_REGTILE, ALGO_F32_SPLITK = 0, 1, 2, 3, 4
 ALGO_F32_REGTILE_SMALL = 5
 ALGO_BF16_AUTO, ALGO_BF16_NAIVE, ALGO_BF16_MFMA, ALGO_BF16_MFMA_16X16, ALGO_BF16_MFMA_SPLITK = 0, 1, 2, 3, 4
+MX_FP4, MX_INT8 = 0, 1  # regtile_mx_format
+MX_GROUP = 32  # columns that share a scale
 
 EXPORTED_SYMBOLS = ("gemm_f32", "gemm_bf16", "gemm_f16", "regtile_gemm_f32_algo",
                     "regtile_gemm_bf16_algo", "regtile_gemm_f16_algo", "regtile_gemm_f32_ex",
                     "regtile_gemm_bf16_ex", "regtile_gemm_f16_ex",
+                    "regtile_quantize_mx", "regtile_dequantize_mx", "regtile_gemm_bf16_mx",
+                    "regtile_gemm_f16_mx",
                     "regtile_last_kernel", "regtile_last_kernel_info", "regtile_strerror",
                     "regtile_version")
 
@@ -90,7 +103,11 @@ def load():
         lib = ctypes.CDLL(_LIB_PATH)
         I, F, P = ctypes.c_int, ctypes.c_float, ctypes.c_void_p
         gemm = [I, I, I, F, P, I, P, I, F, P, I, P]
-        for name, args in (("gemm_f32", gemm), ("gemm_bf16", gemm), ("gemm_f16", gemm),
+        gemm_mx = [I, I, I, I, I, I, F, P, I, P, I, P, I, F, P, I, P]
+        convert_mx = [I, I, I, I, P, I, P, I, P, I, P]
+        for name, args in (("regtile_gemm_bf16_mx", gemm_mx), ("regtile_gemm_f16_mx", gemm_mx),
+                           ("regtile_quantize_mx", convert_mx), ("regtile_dequantize_mx", convert_mx),
+                           ("gemm_f32", gemm), ("gemm_bf16", gemm), ("gemm_f16", gemm),
                            ("regtile_gemm_f16_algo", [I] + gemm),
                            ("regtile_gemm_f32_ex", [I, I, I] + gemm),
                            ("regtile_gemm_bf16_ex", [I, I, I] + gemm),
@@ -180,6 +197,26 @@ def regtile_gemm_f16_ex(algo, trans_a, trans_b, M, N, K, alpha, A, lda, B, ldb, 
 def regtile_gemm_bf16_algo(algo, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, stream=0) -> int:
     return load().regtile_gemm_bf16_algo(algo, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc,
                                          stream)
+
+
+def regtile_gemm_bf16_mx(format, trans_a, trans_b, M, N, K, alpha, A, lda, Q, ldq, S, lds, beta, C, ldc,
+                         stream=0) -> int:
+    return load().regtile_gemm_bf16_mx(format, trans_a, trans_b, M, N, K, alpha, A, lda, Q, ldq, S, lds,
+                                       beta, C, ldc, stream)
+
+
+def regtile_gemm_f16_mx(format, trans_a, trans_b, M, N, K, alpha, A, lda, Q, ldq, S, lds, beta, C, ldc,
+                        stream=0) -> int:
+    return load().regtile_gemm_f16_mx(format, trans_a, trans_b, M, N, K, alpha, A, lda, Q, ldq, S, lds,
+                                      beta, C, ldc, stream)
+
+
+def regtile_quantize_mx(format, dtype, rows, cols, X, ldx, Q, ldq, S, lds, stream=0) -> int:
+    return load().regtile_quantize_mx(format, dtype, rows, cols, X, ldx, Q, ldq, S, lds, stream)
+
+
+def regtile_dequantize_mx(format, dtype, rows, cols, Q, ldq, S, lds, X, ldx, stream=0) -> int:
+    return load().regtile_dequantize_mx(format, dtype, rows, cols, Q, ldq, S, lds, X, ldx, stream)
 
 
 # ---- tensor entry points -------------------------------------------------------------------
@@ -272,3 +309,208 @@ def gemm_f16(A, B, C=None, alpha=1.0, beta=0.0, algo=ALGO_BF16_AUTO, stream=None
 
     return _gemm(regtile_gemm_f16_ex, torch.float16, "gemm_f16", A, B, C, alpha, beta, algo,
                  stream)
+
+
+# ---- block-scaled (MX) operands --------------------------------------------------------------
+_INT_MAX = 2**31 - 1
+
+
+def _row_bytes(format, cols):
+    return (cols + 1) // 2 if format == MX_FP4 else cols
+
+
+def _check_format(format):
+    if format != MX_FP4 and format != MX_INT8:
+        raise ValueError(f"unknown block-scaled format {format!r}")
+
+
+class MXMatrix:
+    """A block-scaled matrix of ``rows`` x ``cols`` values (include/regtile.h states the layout).
+
+    ``codes``: uint8, rows x (cols + 1) // 2 bytes (``MX_FP4``) or rows x cols (``MX_INT8``, int8 is
+    taken too); ``scales``: uint8, rows x ceil(cols / 32). Both have unit column stride (their row
+    strides may exceed the width) and live on one device. ``t()`` is the transposed view: the same
+    bytes, taken as cols x rows. The tensors are kept, not copied.
+    """
+
+    __slots__ = ("format", "codes", "scales", "transposed", "_rows", "_cols", "_ldq", "_lds")
+
+    def __init__(self, format, codes, scales, cols, transposed=False):
+        import torch
+
+        _check_format(format)
+        cols = int(cols)
+        if codes.dtype != torch.uint8 and not (codes.dtype == torch.int8 and format == MX_INT8):
+            raise ValueError("codes must be uint8 (int8 is taken for MX_INT8)")
+        if scales.dtype != torch.uint8:
+            raise ValueError("scales must be uint8")
+        self._ldq, self._lds = _row_major_ld(codes, "codes"), _row_major_ld(scales, "scales")
+        rows = codes.shape[0]
+        if cols < 0 or codes.shape[1] != _row_bytes(format, cols):
+            raise ValueError(f"codes must be {_row_bytes(format, cols)} bytes wide for {cols} columns, not {codes.shape[1]}")
+        if tuple(scales.shape) != (rows, -(-cols // MX_GROUP)):
+            raise ValueError(f"scales must be {(rows, -(-cols // MX_GROUP))}, not {tuple(scales.shape)}")
+        if codes.device != scales.device:
+            raise ValueError("codes and scales are on different devices")
+        self.format, self.codes, self.scales = format, codes, scales
+        self.transposed = bool(transposed)
+        self._rows, self._cols = rows, cols
+
+    @property
+    def shape(self):
+        return (self._cols, self._rows) if self.transposed else (self._rows, self._cols)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def t(self):
+        v = object.__new__(MXMatrix)
+        for name in MXMatrix.__slots__:
+            setattr(v, name, getattr(self, name))
+        v.transposed = not self.transposed
+        return v
+
+    def __repr__(self):
+        name = "MX_FP4" if self.format == MX_FP4 else "MX_INT8"
+        return f"MXMatrix({name}, {self.shape[0]} x {self.shape[1]}{', transposed' if self.transposed else ''})"
+
+
+class _Launch:
+    """Makes `device` the current device and, for what is allocated inside, `stream` the current
+    stream (so that the allocator knows where the memory is used); `handle` is the stream to
+    launch on. Nothing is switched where both are current already."""
+
+    __slots__ = ("handle", "_contexts")
+
+    def __init__(self, device, stream):
+        import torch
+
+        self._contexts = []
+        if torch.cuda.current_device() != device.index:
+            self._contexts.append(torch.cuda.device(device))
+        if stream is None:
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+            return
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the operands on {device}")
+        self._contexts.append(torch.cuda.stream(stream))
+        self.handle = stream.cuda_stream
+
+    def __enter__(self):
+        for c in self._contexts:
+            c.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        for c in reversed(self._contexts):
+            c.__exit__(*exc)
+
+
+def _ints(*values):
+    for v in values:
+        if v > _INT_MAX:
+            raise ValueError(f"sizes and leading dimensions go up to 2**31 - 1, not {v}")
+
+
+def _mx_dtype(dtype, name):
+    import torch
+
+    try:
+        return {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}[dtype]
+    except KeyError:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, not {dtype}") from None
+
+
+def quantize_mx(X, format=MX_INT8, out=None, stream=None):
+    """The block-scaled form of a row-major device tensor X (float32, bfloat16 or float16); groups
+    run along its rows. Writes into ``out`` (an MXMatrix of X's shape and the format) or a new
+    MXMatrix, and returns it."""
+    import torch
+
+    _check_format(format)
+    dt = _mx_dtype(X.dtype, "X")
+    if not X.is_cuda:
+        raise ValueError("quantize_mx takes a device tensor")
+    ldx = _row_major_ld(X, "X")
+    rows, cols = X.shape
+    with _Launch(X.device, stream) as handle:
+        if out is None:
+            out = MXMatrix(format, torch.empty((rows, _row_bytes(format, cols)), dtype=torch.uint8, device=X.device),
+                           torch.empty((rows, -(-cols // MX_GROUP)), dtype=torch.uint8, device=X.device), cols)
+        elif out.format != format or out.transposed or out.shape != (rows, cols) or out.device != X.device:
+            raise ValueError(f"out must be an untransposed MXMatrix of format {format}, shape {(rows, cols)} on {X.device}")
+        _ints(rows, cols, ldx, out._ldq, out._lds)
+        _check(regtile_quantize_mx(format, dt, rows, cols, X.data_ptr(), ldx, out.codes.data_ptr(), out._ldq,
+                                   out.scales.data_ptr(), out._lds, handle))
+    return out
+
+
+def dequantize_mx(Q, dtype=None, out=None, stream=None):
+    """The values of an MXMatrix as a row-major tensor of its shape (of a transposed one: the
+    transposed view of a row-major tensor), rounded to ``dtype`` (bfloat16 when neither it nor ``out``
+    is given). Writes into ``out`` or a new tensor, and returns it."""
+    import torch
+
+    if not Q.codes.is_cuda:
+        raise ValueError("dequantize_mx takes an MXMatrix of device tensors")
+    if dtype is None:
+        dtype = torch.bfloat16 if out is None else out.dtype
+    dt = _mx_dtype(dtype, "dtype")
+    rows, cols = Q._rows, Q._cols
+    with _Launch(Q.device, stream) as handle:
+        if out is None:
+            X = torch.empty((rows, cols), dtype=dtype, device=Q.device)
+        else:
+            if out.dtype != dtype or tuple(out.shape) != Q.shape or out.device != Q.device:
+                raise ValueError(f"out must be {dtype} of shape {Q.shape} on {Q.device}")
+            X = out.t() if Q.transposed else out
+        ldx = _row_major_ld(X, "out")
+        _ints(rows, cols, ldx, Q._ldq, Q._lds)
+        _check(regtile_dequantize_mx(Q.format, dt, rows, cols, Q.codes.data_ptr(), Q._ldq, Q.scales.data_ptr(),
+                                     Q._lds, X.data_ptr(), ldx, handle))
+    if out is not None:
+        return out
+    return X.t() if Q.transposed else X
+
+
+def _gemm_mx(fn, want, label, A, B, C, alpha, beta, stream):
+    if A.dtype != want:
+        raise ValueError(f"{label} takes {want} A")
+    if not isinstance(B, MXMatrix):
+        raise ValueError(f"{label} takes an MXMatrix B")
+    device = A.device
+    if not A.is_cuda or B.codes.device != device or (C is not None and C.device != device):
+        raise ValueError(f"{label} takes device tensors, all on one device")
+    ta, lda = _layout(A, "A")
+    M, K = A.shape
+    K2, N = B.shape
+    if K != K2:
+        raise ValueError(f"inner dimensions differ: {K} vs {K2}")
+    if C is None and beta != 0.0:
+        raise ValueError("beta != 0 needs C")
+    with _Launch(device, stream) as handle:
+        C = _out(C, M, N, A)
+        ldc = _row_major_ld(C, "C")
+        _ints(M, N, K, lda, B._ldq, B._lds, ldc)
+        _check(fn(B.format, ta, int(B.transposed), M, N, K, float(alpha), A.data_ptr(), lda, B.codes.data_ptr(),
+                  B._ldq, B.scales.data_ptr(), B._lds, float(beta), C.data_ptr(), ldc, handle))
+    return C
+
+
+def gemm_bf16_mx(A, B, C=None, alpha=1.0, beta=0.0, stream=None):
+    """C = alpha*A@B + beta*C; bf16 A (M x K), row-major or a transposed view, times a block-scaled B
+    (an MXMatrix, K x N; ``W.t()`` for weights stored N x K), fp32 C row-major; returns C (allocated
+    when None)."""
+    import torch
+
+    return _gemm_mx(regtile_gemm_bf16_mx, torch.bfloat16, "gemm_bf16_mx", A, B, C, alpha, beta, stream)
+
+
+def gemm_f16_mx(A, B, C=None, alpha=1.0, beta=0.0, stream=None):
+    """As gemm_bf16_mx with a float16 A; B's values are taken in float16."""
+    import torch
+
+    return _gemm_mx(regtile_gemm_f16_mx, torch.float16, "gemm_f16_mx", A, B, C, alpha, beta, stream)

@@ -5,6 +5,7 @@
 
 #include <math.h>
 
+#include "mx_common.h"
 #include "regtile_internal.h"
 
 namespace {
@@ -154,6 +155,105 @@ int run_16b(bool f16, int shift, int algo, bool ta, bool tb, int M, int N, int K
     return finish(err, name);
 }
 
+bool bad_format(int f) { return f != REGTILE_MX_FP4 && f != REGTILE_MX_INT8; }
+
+// The product with a block-scaled B. Positions as in the declaration: format 1, trans_a 2,
+// trans_b 3, M 4, N 5, K 6, alpha 7, A 8, lda 9, Q 10, ldq 11, S 12, lds 13, beta 14, C 15, ldc 16.
+int run_mx(bool f16, int format, int trans_a, int trans_b, int M, int N, int K, float alpha,
+           const uint16_t *A, int lda, const uint8_t *Q, int ldq, const uint8_t *S, int lds,
+           float beta, float *C, int ldc, void *stream) {
+    if (bad_format(format)) return -1;
+    if (bad_flag(trans_a)) return -2;
+    if (bad_flag(trans_b)) return -3;
+    if (M < 0) return -4;
+    if (N < 0) return -5;
+    if (K < 0) return -6;
+    const bool fp4 = format == REGTILE_MX_FP4;
+    const bool reads_ab = M > 0 && N > 0 && K > 0 && alpha != 0.0f;
+    const int lda_min = trans_a ? M : K, cols_b = trans_b ? K : N;
+    if (reads_ab && A == nullptr) return -8;
+    if (lda < (lda_min > 1 ? lda_min : 1)) return -9;
+    if (reads_ab && Q == nullptr) return -10;
+    const int64_t ldq_min = regtile::mx::row_bytes(fp4, cols_b), lds_min = regtile::mx::groups(cols_b);
+    if (ldq < (ldq_min > 1 ? ldq_min : 1)) return -11;
+    if (reads_ab && S == nullptr) return -12;
+    if (lds < (lds_min > 1 ? lds_min : 1)) return -13;
+    if (M > 0 && N > 0 && C == nullptr) return -15;
+    if (ldc < (N > 1 ? N : 1)) return -16;
+    regtile::MxProblem p;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.alpha = alpha;
+    p.beta = beta;
+    p.A = A;
+    p.lda = lda;
+    p.Q = Q;
+    p.ldq = ldq;
+    p.S = S;
+    p.lds = lds;
+    p.C = C;
+    p.ldc = ldc;
+    p.ta = trans_a != 0;
+    p.tb = trans_b != 0;
+    p.fp4 = fp4;
+    p.f16 = f16;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    int status;
+    if (quick_return(make_problem(M, N, K, alpha, A, lda, Q, ldq, beta, C, ldc, trans_a, trans_b), s, &status))
+        return status;
+    const char *name = "none";
+    const hipError_t err = regtile::launch_mx_mfma(p, s, &name);
+    return finish(err, name);
+}
+
+// Positions: format 1, dtype 2, rows 3, cols 4, then X 5, ldx 6, Q 7, ldq 8, S 9, lds 10 (to the
+// format) or Q 5, ldq 6, S 7, lds 8, X 9, ldx 10 (from it).
+int run_mx_convert(bool to_mx, int format, int dtype, int rows, int cols, void *X, int ldx, uint8_t *Q, int ldq,
+                   uint8_t *S, int lds, void *stream) {
+    if (bad_format(format)) return -1;
+    if (dtype != REGTILE_MX_F32 && dtype != REGTILE_MX_BF16 && dtype != REGTILE_MX_F16) return -2;
+    if (rows < 0) return -3;
+    if (cols < 0) return -4;
+    const bool fp4 = format == REGTILE_MX_FP4, some = rows > 0 && cols > 0;
+    const int64_t ldq_min = regtile::mx::row_bytes(fp4, cols), lds_min = regtile::mx::groups(cols);
+    const int x = to_mx ? 5 : 9, q = to_mx ? 7 : 5, sc = to_mx ? 9 : 7;
+    int bad = 0;  // the first position that is wrong
+    auto check = [&](int at, bool wrong) {
+        if (wrong && (bad == 0 || at < bad)) bad = at;
+    };
+    check(x, some && X == nullptr);
+    check(x + 1, ldx < (cols > 1 ? cols : 1));
+    check(q, some && Q == nullptr);
+    check(q + 1, ldq < (ldq_min > 1 ? ldq_min : 1));
+    check(sc, some && S == nullptr);
+    check(sc + 1, lds < (lds_min > 1 ? lds_min : 1));
+    // an element's own alignment; the codes are bytes
+    check(x, (reinterpret_cast<uintptr_t>(X) & (dtype == REGTILE_MX_F32 ? 3u : 1u)) != 0);
+    if (bad != 0) return -bad;
+    if (!some) {
+        g_last_kernel = "quick-return";
+        g_last_fn = nullptr;
+        return REGTILE_OK;
+    }
+    (void)hipGetLastError();
+    regtile::MxConvert p;
+    p.rows = rows;
+    p.cols = cols;
+    p.dtype = dtype;
+    p.fp4 = fp4;
+    p.X = X;
+    p.ldx = ldx;
+    p.Q = Q;
+    p.ldq = ldq;
+    p.S = S;
+    p.lds = lds;
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const char *name = "none";
+    const hipError_t err = to_mx ? regtile::launch_mx_quantize(p, s, &name) : regtile::launch_mx_dequantize(p, s, &name);
+    return finish(err, name);
+}
+
 }  // namespace
 
 namespace regtile {
@@ -223,6 +323,29 @@ int regtile_gemm_f16_ex(int algo, int trans_a, int trans_b, int M, int N, int K,
     if (bad_flag(trans_b)) return -3;
     return run_16b(true, 3, algo, trans_a, trans_b, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc,
                    stream);
+}
+
+int regtile_quantize_mx(int format, int dtype, int rows, int cols, const void *X, int ldx, uint8_t *Q, int ldq,
+                        uint8_t *S, int lds, void *stream) {
+    return run_mx_convert(true, format, dtype, rows, cols, const_cast<void *>(X), ldx, Q, ldq, S, lds, stream);
+}
+
+int regtile_dequantize_mx(int format, int dtype, int rows, int cols, const uint8_t *Q, int ldq, const uint8_t *S,
+                          int lds, void *X, int ldx, void *stream) {
+    return run_mx_convert(false, format, dtype, rows, cols, X, ldx, const_cast<uint8_t *>(Q), ldq,
+                          const_cast<uint8_t *>(S), lds, stream);
+}
+
+int regtile_gemm_bf16_mx(int format, int trans_a, int trans_b, int M, int N, int K, float alpha, const uint16_t *A,
+                         int lda, const uint8_t *Q, int ldq, const uint8_t *S, int lds, float beta, float *C, int ldc,
+                         void *stream) {
+    return run_mx(false, format, trans_a, trans_b, M, N, K, alpha, A, lda, Q, ldq, S, lds, beta, C, ldc, stream);
+}
+
+int regtile_gemm_f16_mx(int format, int trans_a, int trans_b, int M, int N, int K, float alpha, const uint16_t *A,
+                        int lda, const uint8_t *Q, int ldq, const uint8_t *S, int lds, float beta, float *C, int ldc,
+                        void *stream) {
+    return run_mx(true, format, trans_a, trans_b, M, N, K, alpha, A, lda, Q, ldq, S, lds, beta, C, ldc, stream);
 }
 
 const char *regtile_last_kernel(void) { return g_last_kernel; }

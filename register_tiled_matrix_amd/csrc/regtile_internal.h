@@ -23,6 +23,34 @@ struct Problem {
     bool ta = false, tb = false;
 };
 
+// One validated product with a block-scaled B (mx_common.h): the stored B is N x K with tb, else
+// K x N, each row ldq bytes of codes and lds scale bytes apart.
+struct MxProblem {
+    int M, N, K;
+    float alpha, beta;
+    const void *A;
+    int64_t lda;
+    const uint8_t *Q;
+    int64_t ldq;
+    const uint8_t *S;
+    int64_t lds;
+    float *C;
+    int64_t ldc;
+    bool ta, tb, fp4, f16;
+};
+
+// One validated conversion: X rows x cols of regtile_mx_dtype, and its codes and scales.
+struct MxConvert {
+    int rows, cols, dtype;
+    bool fp4;
+    void *X;
+    int64_t ldx;
+    uint8_t *Q;
+    int64_t ldq;
+    uint8_t *S;
+    int64_t lds;
+};
+
 // Every launch records the kernel it starts and its workgroup size just before launching it
 // (regtile_last_kernel_info queries that kernel's resources).
 void note_launch(const void *kernel, unsigned threads);
@@ -59,6 +87,10 @@ bool launch_bf16_mfma_dma_mn(const Problem &p, hipStream_t s, const char **name,
 // four storage orders, 16-byte aligned rows, within addr::sk_dma_takes.
 bool launch_bf16_mfma_splitk(const Problem &p, hipStream_t s, const char **name, bool f16,
                              hipError_t *err);
+// Block-scaled operands: conversions, and the product on MFMA tiles.
+hipError_t launch_mx_quantize(const MxConvert &p, hipStream_t s, const char **name);
+hipError_t launch_mx_dequantize(const MxConvert &p, hipStream_t s, const char **name);
+hipError_t launch_mx_mfma(const MxProblem &p, hipStream_t s, const char **name);
 // The default 16-bit entry points take the split-K kernel for problems of few 64x64 tiles with
 // enough K per wave: at most 256 tiles (one per CU) with K >= 1024 in any storage order, and at
 // most 512 with K >= 4096 for K-contiguous A and B ("n t") or M/N-contiguous both ("t n").
