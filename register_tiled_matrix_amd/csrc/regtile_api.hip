@@ -203,7 +203,8 @@ int run_mx(bool f16, int format, int trans_a, int trans_b, int M, int N, int K, 
     if (quick_return(make_problem(M, N, K, alpha, A, lda, Q, ldq, beta, C, ldc, trans_a, trans_b), s, &status))
         return status;
     const char *name = "none";
-    const hipError_t err = regtile::launch_mx_mfma(p, s, &name);
+    hipError_t err;
+    if (!regtile::launch_mx_token(p, s, &name, &err)) err = regtile::launch_mx_mfma(p, s, &name);
     return finish(err, name);
 }
 
