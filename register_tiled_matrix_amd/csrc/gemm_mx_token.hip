@@ -24,117 +24,74 @@ namespace regtile {
 namespace {
 using namespace mfma;
 
-// NF fragments of 16 / H rows of B and MC fragments of 16 / H tokens a wave; U chunks in flight
-template <bool FP4, bool F16, int H, int NF, int MC, int NW, int U>
-__global__ __launch_bounds__(NW * 64) void mx_token_kernel(int M, int N, int K, float alpha,
-                                                           const uint16_t *__restrict__ A, int64_t lda,
-                                                           const uint8_t *__restrict__ Q, int64_t ldq,
-                                                           const uint8_t *__restrict__ S, int64_t lds, float beta,
-                                                           float *__restrict__ C, int64_t ldc, int vec_c) {
-    typedef Frag<16, F16> F;
-    constexpr int R = 16 / H;            // rows of B (tokens) per fragment
-    constexpr int CHUNK = 128 * H;       // k per step of a wave
-    constexpr int GB = FP4 ? 16 : 32;    // bytes of a group's codes
-    __shared__ float4 part[NW][NF * MC][64];
+template <int NF, int MC>
+using Acc = f32x4[NF][MC];
 
-    const int tid = threadIdx.x;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-    const int r = lane & 15, j = lane >> 4;
-    const int64_t n0 = (int64_t)blockIdx.x * (R * NF);
-    const int koff = (j * H + r % H) * 32;  // this lane's group within a chunk
-    // rows past the end repeat the last one: their outputs are not stored
-    const uint8_t *qp[NF], *sp[NF];
+// acc += the products of one chunk: each lane's group of 32 codes of NF rows of B (q, scale bytes s)
+// with the same 32 of k of MC tokens (x, 8 to a uint4)
+template <bool FP4, bool F16, int NF, int MC>
+__device__ __forceinline__ void multiply_group(const uint32_t (&q)[NF][FP4 ? 4 : 8], const uint32_t (&s)[NF],
+                                               const uint4 (&x)[MC][4], Acc<NF, MC> &acc) {
+    float sc[NF];
 #pragma unroll
-    for (int f = 0; f < NF; ++f) {
-        const int64_t n = min(n0 + f * R + r / H, (int64_t)N - 1);
-        qp[f] = Q + n * ldq + koff / 32 * GB;
-        sp[f] = S + n * lds + koff / 32;
-    }
-    const uint16_t *xp[MC];
+    for (int f = 0; f < NF; ++f) sc[f] = mx::scale_value<FP4>(s[f]);
 #pragma unroll
-    for (int i = 0; i < MC; ++i) xp[i] = A + (int64_t)min(i * R + r / H, M - 1) * lda + koff;
-
-    typename F::acc_t acc[NF][MC];
-#pragma unroll
-    for (int f = 0; f < NF; ++f)
-#pragma unroll
-        for (int i = 0; i < MC; ++i) acc[f][i] = typename F::acc_t{0.f, 0.f, 0.f, 0.f};
-
-    uint32_t q[U][NF][GB / 4], s[U][NF];
-    uint4 x[U][MC][4];
-    auto compute = [&](int u) {
-        float sc[NF];
-#pragma unroll
-        for (int f = 0; f < NF; ++f) sc[f] = mx::scale_value<FP4>(s[u][f]);
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                const bf16x8 w = __builtin_bit_cast(bf16x8, mx::expand8<FP4, F16>(q[u][f], t, sc[f]));
-#pragma unroll
-                for (int i = 0; i < MC; ++i) acc[f][i] = F::mfma(w, __builtin_bit_cast(bf16x8, x[u][i][t]), acc[f][i]);
-            }
-    };
-
-    const int nfull = K / CHUNK;
-    for (int c0 = wave; c0 < nfull; c0 += NW * U) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t c = min(c0 + u * NW, nfull - 1);  // past the end: loaded again, not used
-#pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                mx::load_bytes<GB>(qp[f] + c * (CHUNK / 32 * GB), q[u][f]);
-                s[u][f] = sp[f][c * (CHUNK / 32)];
-            }
-#pragma unroll
-            for (int i = 0; i < MC; ++i) __builtin_memcpy(x[u][i], xp[i] + c * CHUNK, 64);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (c0 + u * NW < nfull) compute(u);
-    }
-    if (K % CHUNK != 0 && wave == nfull % NW) {  // the last, short chunk
-        const int64_t c = nfull;
-        const int left = K - nfull * CHUNK - koff;  // of this lane's group
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
-            const uint8_t *p = qp[f] + c * (CHUNK / 32 * GB);
+            const bf16x8 w = __builtin_bit_cast(bf16x8, mx::expand8<FP4, F16>(q[f], t, sc[f]));
 #pragma unroll
-            for (int i = 0; i < GB / 4; ++i) q[0][f][i] = 0;
-            s[0][f] = 0;
-            if (left > 0) {
-                s[0][f] = sp[f][c * (CHUNK / 32)];
-                if (left >= 32)
-                    mx::load_bytes<GB>(p, q[0][f]);
-                else
-                    mx::load_codes_tail<FP4, GB>(p, left, q[0][f]);
-            }
+            for (int i = 0; i < MC; ++i) acc[f][i] = Frag<16, F16>::mfma(w, __builtin_bit_cast(bf16x8, x[i][t]), acc[f][i]);
         }
-#pragma unroll
-        for (int i = 0; i < MC; ++i)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const uint16_t *p = xp[i] + c * CHUNK + 8 * t;
-                uint32_t d[4] = {0, 0, 0, 0};
-                if (left >= 8 * t + 8) {
-                    __builtin_memcpy(d, p, 16);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 7; ++e)
-                        if (8 * t + e < left) d[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
-                }
-                x[0][i][t] = make_uint4(d[0], d[1], d[2], d[3]);
-            }
-        compute(0);
-    }
+}
 
-    // accumulator v of lane l: row 4 (l / 16) + v of B's fragment, column l % 16 of A's
+// The last, short chunk: `left` of this lane's 32 of k remain (none below 1), read without touching
+// what lies behind them; qp, sp and xp point at the lane's group.
+template <bool FP4, bool F16, int NF, int MC>
+__device__ __forceinline__ void short_chunk(int left, const uint8_t *const (&qp)[NF], const uint8_t *const (&sp)[NF],
+                                            const uint16_t *const (&xp)[MC], Acc<NF, MC> &acc) {
+    constexpr int GB = FP4 ? 16 : 32;
+    uint32_t q[NF][GB / 4], s[NF];
+    uint4 x[MC][4];
 #pragma unroll
-    for (int f = 0; f < NF; ++f)
+    for (int f = 0; f < NF; ++f) {
 #pragma unroll
-        for (int i = 0; i < MC; ++i) part[wave][f * MC + i][lane] = __builtin_bit_cast(float4, acc[f][i]);
-    __syncthreads();
-    for (int o = tid; o < NF * MC * 64; o += NW * 64) {
+        for (int i = 0; i < GB / 4; ++i) q[f][i] = 0;
+        s[f] = 0;
+        if (left > 0) {
+            s[f] = *sp[f];
+            if (left >= 32)
+                mx::load_bytes<GB>(qp[f], q[f]);
+            else
+                mx::load_codes_tail<FP4, GB>(qp[f], left, q[f]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MC; ++i)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            const uint16_t *p = xp[i] + 8 * t;
+            uint32_t d[4] = {0, 0, 0, 0};
+            if (left >= 8 * t + 8) {
+                __builtin_memcpy(d, p, 16);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 7; ++e)
+                    if (8 * t + e < left) d[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
+            }
+            x[i][t] = make_uint4(d[0], d[1], d[2], d[3]);
+        }
+    multiply_group<FP4, F16, NF, MC>(q, s, x, acc);
+}
+
+// The sum of the waves' accumulators (part[wave][fragment][lane]) in wave order, and the epilogue.
+// Accumulator v of lane l: row 4 (l / 16) + v of B's fragment, column l % 16 of A's.
+template <int H, int NF, int MC, int NW>
+__device__ __forceinline__ void join_and_store(const float4 (&part)[NW][NF * MC][64], int M, int N, int64_t n0,
+                                               float alpha, float beta, float *__restrict__ C, int64_t ldc, int vec_c) {
+    constexpr int R = 16 / H;
+    const int lane = threadIdx.x & 63, r = lane & 15, j = lane >> 4;
+    for (int o = threadIdx.x; o < NF * MC * 64; o += NW * 64) {
         const int fi = o >> 6, f = fi / MC, i = fi % MC;
         float4 v = part[0][fi][lane];
 #pragma unroll
@@ -187,6 +144,224 @@ __global__ __launch_bounds__(NW * 64) void mx_token_kernel(int M, int N, int K, 
     }
 }
 
+// NF fragments of 16 / H rows of B and MC fragments of 16 / H tokens a wave; U chunks in flight
+template <bool FP4, bool F16, int H, int NF, int MC, int NW, int U>
+__global__ __launch_bounds__(NW * 64) void mx_token_kernel(int M, int N, int K, float alpha,
+                                                           const uint16_t *__restrict__ A, int64_t lda,
+                                                           const uint8_t *__restrict__ Q, int64_t ldq,
+                                                           const uint8_t *__restrict__ S, int64_t lds, float beta,
+                                                           float *__restrict__ C, int64_t ldc, int vec_c) {
+    constexpr int R = 16 / H;            // rows of B (tokens) per fragment
+    constexpr int CHUNK = 128 * H;       // k per step of a wave
+    constexpr int GB = FP4 ? 16 : 32;    // bytes of a group's codes
+    __shared__ float4 part[NW][NF * MC][64];
+
+    const int tid = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int r = lane & 15, j = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * (R * NF);
+    const int koff = (j * H + r % H) * 32;  // this lane's group within a chunk
+    // rows past the end repeat the last one: their outputs are not stored
+    const uint8_t *qp[NF], *sp[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+        const int64_t n = min(n0 + f * R + r / H, (int64_t)N - 1);
+        qp[f] = Q + n * ldq + koff / 32 * GB;
+        sp[f] = S + n * lds + koff / 32;
+    }
+    const uint16_t *xp[MC];
+#pragma unroll
+    for (int i = 0; i < MC; ++i) xp[i] = A + (int64_t)min(i * R + r / H, M - 1) * lda + koff;
+
+    Acc<NF, MC> acc;
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int i = 0; i < MC; ++i) acc[f][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    uint32_t q[U][NF][GB / 4], s[U][NF];
+    uint4 x[U][MC][4];
+    const int nfull = K / CHUNK;
+    for (int c0 = wave; c0 < nfull; c0 += NW * U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t c = min(c0 + u * NW, nfull - 1);  // past the end: loaded again, not used
+#pragma unroll
+            for (int f = 0; f < NF; ++f) {
+                mx::load_bytes<GB>(qp[f] + c * (CHUNK / 32 * GB), q[u][f]);
+                s[u][f] = sp[f][c * (CHUNK / 32)];
+            }
+#pragma unroll
+            for (int i = 0; i < MC; ++i) __builtin_memcpy(x[u][i], xp[i] + c * CHUNK, 64);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c0 + u * NW < nfull) multiply_group<FP4, F16, NF, MC>(q[u], s[u], x[u], acc);
+    }
+    if (K % CHUNK != 0 && wave == nfull % NW) {
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            qp[f] += (int64_t)nfull * (CHUNK / 32 * GB);
+            sp[f] += (int64_t)nfull * (CHUNK / 32);
+        }
+#pragma unroll
+        for (int i = 0; i < MC; ++i) xp[i] += (int64_t)nfull * CHUNK;
+        short_chunk<FP4, F16, NF, MC>(K - nfull * CHUNK - koff, qp, sp, xp, acc);
+    }
+
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int i = 0; i < MC; ++i) part[wave][f * MC + i][lane] = __builtin_bit_cast(float4, acc[f][i]);
+    __syncthreads();
+    join_and_store<H, NF, MC, NW>(part, M, N, n0, alpha, beta, C, ldc, vec_c);
+}
+
+// 4 bytes per lane from `src` into LDS at `dst` + lane * 4 (dst wave-uniform)
+__device__ __forceinline__ void dma4(const void *src, void *dst) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void *)dst, 4, 0, 0);
+#else
+    (void)src;
+    (void)dst;
+#endif
+}
+
+// The same product (H = 1) for more tokens and 16-byte aligned rows, through LDS. Reading fragments
+// straight from memory, 16 neighbouring lanes touch 16 rows, 16 bytes of each, and the loads of A (four
+// for one of fp4 codes) spend more of the CU's address unit than the codes do. Here each wave
+// brings its chunk (128 of k: 16 NF rows of codes, their scales, 16 MC rows of A) to its own part of LDS by
+// DMA, 256 consecutive bytes of a row of A and 64 (128) of a row of codes at a time, in a ring of D
+// chunks, and reads the fragments from there. Waves share nothing until their sums are joined, so the
+// loop has no barrier.
+//
+// A's rows are 16 chunks of 16 bytes, chunk c of row r at slot c ^ r; rows of codes are 4 (8) chunks, at
+// c ^ (r >> 2 & 3) (c ^ (r >> 1 & 7)): 16 lanes that read one chunk of 16 rows reach all banks.
+template <bool FP4, bool F16, int NF, int MC, int NW, int D>
+__global__ __launch_bounds__(NW * 64) void mx_batch_kernel(int M, int N, int K, float alpha,
+                                                           const uint16_t *__restrict__ A, int64_t lda,
+                                                           const uint8_t *__restrict__ Q, int64_t ldq,
+                                                           const uint8_t *__restrict__ S, int64_t lds, float beta,
+                                                           float *__restrict__ C, int64_t ldc, int vec_c) {
+    constexpr int QCH = FP4 ? 4 : 8;                 // 16-byte chunks of a row of codes
+    constexpr int XS = MC * 256, QS = NF * 16 * QCH;  // 16-byte slots of A and of the codes
+    constexpr int STAGE = XS + QS + 16;              // and of the scales (16 NF <= 64 dwords)
+    constexpr int PER = MC * 4 + NF * QCH / 4 + 1;   // DMA instructions of a chunk
+    static_assert(NF * 16 <= 64 && PER * (D - 1) < 64 && D >= 2, "scales of a chunk in one DMA; vmcnt range");
+    constexpr int SLOTS = NW * D * STAGE, SLOTS_PART = NW * NF * MC * 64;
+    static_assert(SLOTS * 16 <= 160 * 1024 && SLOTS_PART <= SLOTS, "LDS");
+    __shared__ uint4 smem[SLOTS];
+
+    const int tid = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int r = lane & 15, j = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * (16 * NF);
+    uint4 *const mine = smem + wave * (D * STAGE);
+    auto row_n = [&](int i) { return min(n0 + i, (int64_t)N - 1); };  // rows past the end repeat the last
+
+    // this lane's part of each DMA instruction
+    const uint16_t *xsrc[MC * 4];
+    const uint8_t *qsrc[NF * QCH / 4], *ssrc;
+#pragma unroll
+    for (int i = 0; i < MC * 4; ++i) {
+        const int row = 4 * i + (lane >> 4);
+        xsrc[i] = A + (int64_t)min(row, M - 1) * lda + ((lane & 15) ^ (row & 15)) * 8;
+    }
+#pragma unroll
+    for (int i = 0; i < NF * QCH / 4; ++i) {
+        const int slot = i * 64 + lane, row = slot / QCH, ch = slot % QCH;
+        qsrc[i] = Q + row_n(row) * ldq + (ch ^ (FP4 ? (row >> 2) & 3 : (row >> 1) & 7)) * 16;
+    }
+    ssrc = S + row_n(lane % (16 * NF)) * lds;
+    auto issue = [&](int64_t c, int st) {
+        uint4 *d = mine + st * STAGE;
+#pragma unroll
+        for (int i = 0; i < NF * QCH / 4; ++i) dma16(qsrc[i] + c * (QCH * 16), d + XS + i * 64);
+        dma4(ssrc + c * 4, d + XS + QS);
+#pragma unroll
+        for (int i = 0; i < MC * 4; ++i) dma16(xsrc[i] + c * 128, d + i * 64);
+    };
+
+    Acc<NF, MC> acc;
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int i = 0; i < MC; ++i) acc[f][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    const int nfull = K / 128;
+    const int mychunks = nfull > wave ? (nfull - wave + NW - 1) / NW : 0;
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i)
+        if (i < mychunks) issue(wave + i * NW, i);
+    int st = 0;
+    for (int i = 0; i < mychunks; ++i) {
+        if (i + D - 1 < mychunks) {
+            issue(wave + (int64_t)(i + D - 1) * NW, st == 0 ? D - 1 : st - 1);  // the chunk before's slot
+            wait_vmcnt<PER *(D - 1)>();
+        } else {
+            wait_vmcnt<0>();
+        }
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        const uint4 *d = mine + st * STAGE;
+        uint32_t q[NF][QCH], s[NF];
+        uint4 x[MC][4];
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            const uint4 *row = d + XS + (f * 16 + r) * QCH;
+#pragma unroll
+            for (int e = 0; e < QCH / 4; ++e) {
+                const uint4 v = row[FP4 ? j ^ ((r >> 2) & 3) : (2 * j + e) ^ ((r >> 1) & 7)];
+                q[f][4 * e] = v.x;
+                q[f][4 * e + 1] = v.y;
+                q[f][4 * e + 2] = v.z;
+                q[f][4 * e + 3] = v.w;
+            }
+            s[f] = reinterpret_cast<const uint8_t *>(d + XS + QS)[(f * 16 + r) * 4 + j];
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int m = 0; m < MC; ++m) x[m][t] = d[(m * 16 + r) * 16 + ((4 * j + t) ^ r)];
+        multiply_group<FP4, F16, NF, MC>(q, s, x, acc);
+        wait_lgkmcnt0();  // the chunk is in registers before its slot is filled again
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        st = st + 1 == D ? 0 : st + 1;
+    }
+    if (K % 128 != 0 && wave == nfull % NW) {
+        const uint8_t *qp[NF], *sp[NF];
+        const uint16_t *xp[MC];
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            qp[f] = Q + row_n(f * 16 + r) * ldq + ((int64_t)nfull * 4 + j) * (QCH * 4);
+            sp[f] = S + row_n(f * 16 + r) * lds + (int64_t)nfull * 4 + j;
+        }
+#pragma unroll
+        for (int m = 0; m < MC; ++m) xp[m] = A + (int64_t)min(m * 16 + r, M - 1) * lda + (int64_t)nfull * 128 + 32 * j;
+        short_chunk<FP4, F16, NF, MC>(K - nfull * 128 - 32 * j, qp, sp, xp, acc);
+    }
+
+    __syncthreads();  // the sums take the rings' place
+    auto &part = *reinterpret_cast<float4(*)[NW][NF * MC][64]>(smem);
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int m = 0; m < MC; ++m) part[wave][f * MC + m][lane] = __builtin_bit_cast(float4, acc[f][m]);
+    __syncthreads();
+    join_and_store<1, NF, MC, NW>(part, M, N, n0, alpha, beta, C, ldc, vec_c);
+}
+
+template <bool FP4, bool F16, int NF, int MC, int NW, int D>
+hipError_t launch_batch(const MxProblem &p, hipStream_t s) {
+    const int vec_c = p.ldc % 4 == 0 && aligned16(p.C);
+    note_launch(reinterpret_cast<const void *>(&mx_batch_kernel<FP4, F16, NF, MC, NW, D>), NW * 64);
+    hipLaunchKernelGGL((mx_batch_kernel<FP4, F16, NF, MC, NW, D>), dim3((unsigned)(((int64_t)p.N + 16 * NF - 1) / (16 * NF))),
+                       dim3(NW * 64), 0, s, p.M, p.N, p.K, p.alpha, (const uint16_t *)p.A, p.lda, p.Q, p.ldq, p.S, p.lds,
+                       p.beta, p.C, p.ldc, vec_c);
+    return hipGetLastError();
+}
+
 template <bool FP4, bool F16, int H, int NF, int MC, int NW, int U>
 hipError_t launch_token(const MxProblem &p, hipStream_t s) {
     constexpr int ROWS = 16 / H * NF;
@@ -198,11 +373,24 @@ hipError_t launch_token(const MxProblem &p, hipStream_t s) {
     return hipGetLastError();
 }
 
+#ifndef TK_MAX
+#define TK_MAX 4
+#endif
 #ifndef TK_CFG4
-#define TK_CFG4 1, 1, 8, 2
-#define TK_CFG2 1, 1, 8, 4
-#define TK_CFG1 1, 1, 8, 4
-#define TK_CFGM 1, 2, 8, 4
+#define TK_CFG4 4, 1, 8, 1
+#define TK_CFG2 4, 1, 8, 1
+#define TK_CFG1 2, 1, 8, 4
+#define TK_CFGM 2, 2, 4, 2
+#endif
+#ifndef BT_F1
+#define BT_F1 2, 1, 8, 3
+#define BT_I1 2, 1, 4, 4
+#define BT_F2 2, 2, 4, 3
+#define BT_I2 2, 2, 4, 3
+#define BT_F3 2, 3, 4, 2
+#define BT_I3 2, 3, 4, 2
+#define BT_F4 2, 4, 4, 2
+#define BT_I4 1, 4, 4, 2
 #endif
 
 template <bool FP4, bool F16>
@@ -212,18 +400,37 @@ hipError_t launch_token_rows(const MxProblem &p, hipStream_t s) {
     if (p.M <= 16) return launch_token<FP4, F16, 1, TK_CFG1>(p, s);
     return launch_token<FP4, F16, 1, TK_CFGM>(p, s);
 }
+template <bool F16>
+hipError_t launch_batch_rows(const MxProblem &p, hipStream_t s) {
+    if (p.M <= 16) return p.fp4 ? launch_batch<true, F16, BT_F1>(p, s) : launch_batch<false, F16, BT_I1>(p, s);
+    if (p.M <= 32) return p.fp4 ? launch_batch<true, F16, BT_F2>(p, s) : launch_batch<false, F16, BT_I2>(p, s);
+    if (p.M <= 48) return p.fp4 ? launch_batch<true, F16, BT_F3>(p, s) : launch_batch<false, F16, BT_I3>(p, s);
+    return p.fp4 ? launch_batch<true, F16, BT_F4>(p, s) : launch_batch<false, F16, BT_I4>(p, s);
+}
 
 }  // namespace
 
-// Takes (and launches, status in *err) products of at most 32 rows of A, row-major, with B stored
-// N x K; returns false, launching nothing, for any other.
+// Takes (and launches, status in *err) products of at most 64 rows of A, row-major, with B stored
+// N x K: the register kernel up to 4 rows (8 rows: fragments of two parts) and, up to 32, where rows are
+// not aligned for the LDS kernel, which takes the others. Returns false, launching nothing, for any
+// other problem.
 bool launch_mx_token(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err) {
-    if (p.ta || !p.tb || p.M > 32) return false;
-#define REGTILE_TOKEN_SET(elt, fmt) {elt "_" fmt "_token4", elt "_" fmt "_token8", elt "_" fmt "_token16", elt "_" fmt "_token32"}
-    static const char *const names[2][2][4] = {{REGTILE_TOKEN_SET("bf16", "int8"), REGTILE_TOKEN_SET("bf16", "fp4")},
-                                               {REGTILE_TOKEN_SET("f16", "int8"), REGTILE_TOKEN_SET("f16", "fp4")}};
+    if (p.ta || !p.tb) return false;
+    const bool lds = p.M > TK_MAX && p.M <= 64 && p.lda % 8 == 0 && aligned16(p.A) && p.ldq % 16 == 0 && aligned16(p.Q) &&
+                     p.lds % 4 == 0 && (reinterpret_cast<uintptr_t>(p.S) & 3u) == 0;
+    if (!lds && p.M > 32) return false;
+#define REGTILE_TOKEN_SET(elt, fmt)                                                                            \
+    {{elt "_" fmt "_token4", elt "_" fmt "_token8", elt "_" fmt "_token16", elt "_" fmt "_token32"},          \
+     {elt "_" fmt "_batch16", elt "_" fmt "_batch32", elt "_" fmt "_batch48", elt "_" fmt "_batch64"}}
+    static const char *const names[2][2][2][4] = {{REGTILE_TOKEN_SET("bf16", "int8"), REGTILE_TOKEN_SET("bf16", "fp4")},
+                                                  {REGTILE_TOKEN_SET("f16", "int8"), REGTILE_TOKEN_SET("f16", "fp4")}};
 #undef REGTILE_TOKEN_SET
-    *name = names[p.f16][p.fp4][p.M <= 4 ? 0 : p.M <= 8 ? 1 : p.M <= 16 ? 2 : 3];
+    if (lds) {
+        *name = names[p.f16][p.fp4][1][(p.M - 1) / 16];
+        *err = p.f16 ? launch_batch_rows<true>(p, s) : launch_batch_rows<false>(p, s);
+        return true;
+    }
+    *name = names[p.f16][p.fp4][0][p.M <= 4 ? 0 : p.M <= 8 ? 1 : p.M <= 16 ? 2 : 3];
     if (p.fp4)
         *err = p.f16 ? launch_token_rows<true, true>(p, s) : launch_token_rows<true, false>(p, s);
     else

@@ -172,7 +172,7 @@ def product(rng, fmt, dtype, order, M, N, K, alpha=1.0, beta=0.0, pad=0, e_lo=12
 
 
 SIZES = [(1, 1, 1), (1, 2, 31), (2, 33, 32), (1, 17, 33), (3, 64, 64), (16, 48, 512), (17, 100, 77), (33, 65, 129),
-         (64, 64, 64), (65, 127, 191), (1, 256, 1024), (4, 1000, 2049), (5, 130, 4161), (8, 36, 8192), (12, 50, 1100), (32, 40, 4128), (1, 6, 8224), (100, 150, 777), (130, 257, 95), (256, 320, 256)]
+         (64, 64, 64), (65, 127, 191), (1, 256, 1024), (4, 1000, 2049), (5, 130, 4161), (8, 36, 8192), (12, 50, 1100), (32, 40, 4128), (1, 6, 8224), (40, 33, 640), (64, 100, 1152), (49, 18, 8448), (100, 150, 777), (130, 257, 95), (256, 320, 256)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
