@@ -94,6 +94,9 @@ hipError_t launch_mx_mfma(const MxProblem &p, hipStream_t s, const char **name);
 // The product for a few rows of A (row-major) with B stored N x K; false, launching nothing, for
 // any other problem.
 bool launch_mx_token(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err);
+// The product on DMA-fed tiles for aligned A and whole groups of B (addr::mx_dma_takes); false,
+// launching nothing, for any other problem.
+bool launch_mx_dma(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err);
 // The default 16-bit entry points take the split-K kernel for problems of few 64x64 tiles with
 // enough K per wave: at most 256 tiles (one per CU) with K >= 1024 in any storage order, and at
 // most 512 with K >= 4096 for K-contiguous A and B ("n t") or M/N-contiguous both ("t n").

@@ -179,6 +179,14 @@ REGTILE_HD bool rows_dma_takes(bool nn, int M, int N, int K, int64_t lda, int64_
     return K > 0 && K % 8 == 0 && ld_dma % 8 == 0 && t * ld_dma * 2 < lim && runs_fit(cols_row, ld_row, 4) &&
            ((int64_t)K + 128) * ld_row * 2 + 512 < lim && t * ldc * 4 < lim;
 }
+// The block-scaled kernel (gemm_mx_dma.hip): A as above in either storage order (K-contiguous:
+// whole 16-byte chunks of k; M-contiguous: of m); B in whole groups of 32 along its rows.
+REGTILE_HD bool mx_dma_takes(bool ta, bool tb, int M, int N, int K, int64_t lda, int64_t ldc) {
+    const int64_t t = dma_tile(M, N), lim = int64_t(1) << 31;
+    if (K <= 0 || (tb ? K : N) % 32 != 0 || t * ldc * 4 >= lim) return false;
+    return ta ? runs_fit(M, lda, 8) && ((int64_t)K + 64) * lda * 2 + 512 < lim
+              : K % 8 == 0 && lda % 8 == 0 && t * lda * 2 < lim;
+}
 // The register-staged kernel's gather of an M/N-contiguous operand with `cols` columns goes
 // through a per-slab descriptor (8-byte runs) when this holds, else through predicated loads.
 REGTILE_HD bool gather_desc_takes(int64_t cols, int64_t ld) { return runs_fit(cols, ld, 4); }

@@ -192,6 +192,41 @@ def test_product_strides_alpha_beta(fmt, order, M, N, K):
     product(rng, fmt, "f16", order, M, N, K, alpha=-0.75, beta=1.0, pad=8, c_pad=4, label="padded")
 
 
+# the DMA kernels: one slab, slabs that end inside a group of four, tiles that end anywhere, 128 and
+# 256 wide tiles
+@pytest.mark.parametrize("M,N,K", [(72, 96, 32), (136, 160, 64), (200, 288, 96), (128, 128, 640), (264, 512, 224), (1000, 1504, 800),
+                                   (2304, 4096 + 32, 160), (4096, 2304, 64)])
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_product_dma(fmt, order, M, N, K):
+    rng = np.random.default_rng(M + N + K)
+    product(rng, fmt, "bf16", order, M, N, K, label="dma")
+    assert "_dma_" in rt.last_kernel()
+    product(rng, fmt, "f16", order, M, N, K, alpha=0.5, beta=-1.0, pad=16, c_pad=1, label="dma, padded")
+    assert "_dma_" in rt.last_kernel()
+
+
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_infinite_groups_do_not_reach_past_the_edge(fmt, order):
+    """The group at the end of K overflows to infinity: outputs are infinite, not NaN, though the
+    kernels multiply what lies past K by zero."""
+    M, N, K = 72, 96, 96
+    rows, cols = (N, K) if order[1] == "t" else (K, N)
+    w, g = mx.widths(fmt, cols)
+    codes = np.full((rows, w), 0x11 if fmt == mx.FP4 else 1, dtype=np.uint8)  # all positive
+    scales = np.full((rows, g), 120, dtype=np.uint8)
+    if order[1] == "t":
+        scales[:, -1] = 160
+    else:
+        scales[-1, :] = 160
+    A = torch.full((M, K), 1.0, dtype=torch.float16, device="cuda")
+    A = A.t().contiguous().t() if order[0] == "t" else A
+    B = rt.MXMatrix(fmt, dev(codes), dev(scales), cols)
+    got = rt.gemm_f16_mx(A, B.t() if order[1] == "t" else B)  # 2^26 and more overflow fp16
+    assert bool(torch.isposinf(got).all()), (rt.last_kernel(), got.unique())
+
+
 @pytest.mark.parametrize("order", ORDERS)
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_product_integers_bitwise(fmt, order):
