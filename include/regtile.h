@@ -231,16 +231,25 @@ int regtile_dequantize_mx(int format, int dtype, int rows, int cols, const uint8
  *   format   (arg 1) a regtile_mx_format value
  *   trans_a  (arg 2) as in regtile_gemm_bf16_ex;  trans_b (arg 3) 0: B stored K x N, groups along N;
  *            1: B stored N x K, groups along K
- *   M, N, K, alpha, A, lda (args 4-9), Q, ldq, S, lds (10-13), beta, C, ldc (14-16), stream (17)
- *   as above: 0 sizes, alpha == 0 and beta == 0 as for gemm_bf16.
- * Every output is summed in a fixed order: repeated calls give identical bits.
+ *   M, N, K, alpha, A, lda (args 4-9), Q, ldq, S, lds (10-13), beta, C, ldc (14-16), as above:
+ *            0 sizes, alpha == 0 and beta == 0 as for gemm_bf16
+ *   work, work_bytes (17-18) a workspace, or NULL and 0: device memory, 16-byte aligned, that nothing
+ *            else uses until the call has run. Products with few output tiles and a long K use it to
+ *            spread K over more of the chip, one M x N fp32 part for each split; with less than
+ *            regtile_gemm_mx_workspace() bytes they make fewer splits. Its contents need no
+ *            preparation and mean nothing afterwards.
+ *   stream   (arg 19)
+ * regtile_gemm_mx_workspace -- the bytes that such a call makes use of, 0 for most.
+ * Every output is summed in a fixed order: repeated calls (with the same workspace size) give
+ * identical bits.
  */
 int regtile_gemm_bf16_mx(int format, int trans_a, int trans_b, int M, int N, int K, float alpha,
                          const uint16_t *A, int lda, const uint8_t *Q, int ldq, const uint8_t *S,
-                         int lds, float beta, float *C, int ldc, void *stream);
+                         int lds, float beta, float *C, int ldc, void *work, int64_t work_bytes, void *stream);
 int regtile_gemm_f16_mx(int format, int trans_a, int trans_b, int M, int N, int K, float alpha,
                         const uint16_t *A, int lda, const uint8_t *Q, int ldq, const uint8_t *S,
-                        int lds, float beta, float *C, int ldc, void *stream);
+                        int lds, float beta, float *C, int ldc, void *work, int64_t work_bytes, void *stream);
+int64_t regtile_gemm_mx_workspace(int trans_a, int trans_b, int M, int N, int K, int lda, int ldc);
 
 /* Name of the kernel the calling thread launched last ("none" before the first launch,
  * "quick-return" when nothing was launched). Static storage; do not free. */

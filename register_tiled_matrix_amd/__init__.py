@@ -47,7 +47,7 @@ __all__ = [
     "regtile_gemm_f32_ex", "regtile_gemm_bf16_ex", "regtile_gemm_f16_ex",
     "MX_FP4", "MX_INT8", "MX_GROUP", "MXMatrix", "quantize_mx", "dequantize_mx", "gemm_bf16_mx", "gemm_f16_mx",
     "regtile_quantize_mx", "regtile_dequantize_mx", "regtile_gemm_bf16_mx", "regtile_gemm_f16_mx",
-    "last_kernel", "last_kernel_info", "strerror", "version", "EXPORTED_SYMBOLS",
+    "regtile_gemm_mx_workspace", "last_kernel", "last_kernel_info", "strerror", "version", "EXPORTED_SYMBOLS",
 ]
 
 ALGO_F32_AUTO, ALGO_F32_NAIVE, ALGO_F32_LDS, ALGO_F32_REGTILE, ALGO_F32_SPLITK = 0, 1, 2, 3, 4
@@ -60,7 +60,7 @@ EXPORTED_SYMBOLS = ("gemm_f32", "gemm_bf16", "gemm_f16", "regtile_gemm_f32_algo"
                     "regtile_gemm_bf16_algo", "regtile_gemm_f16_algo", "regtile_gemm_f32_ex",
                     "regtile_gemm_bf16_ex", "regtile_gemm_f16_ex",
                     "regtile_quantize_mx", "regtile_dequantize_mx", "regtile_gemm_bf16_mx",
-                    "regtile_gemm_f16_mx",
+                    "regtile_gemm_f16_mx", "regtile_gemm_mx_workspace",
                     "regtile_last_kernel", "regtile_last_kernel_info", "regtile_strerror",
                     "regtile_version")
 
@@ -103,7 +103,7 @@ def load():
         lib = ctypes.CDLL(_LIB_PATH)
         I, F, P = ctypes.c_int, ctypes.c_float, ctypes.c_void_p
         gemm = [I, I, I, F, P, I, P, I, F, P, I, P]
-        gemm_mx = [I, I, I, I, I, I, F, P, I, P, I, P, I, F, P, I, P]
+        gemm_mx = [I, I, I, I, I, I, F, P, I, P, I, P, I, F, P, I, P, ctypes.c_int64, P]
         convert_mx = [I, I, I, I, P, I, P, I, P, I, P]
         for name, args in (("regtile_gemm_bf16_mx", gemm_mx), ("regtile_gemm_f16_mx", gemm_mx),
                            ("regtile_quantize_mx", convert_mx), ("regtile_dequantize_mx", convert_mx),
@@ -117,6 +117,8 @@ def load():
             f = getattr(lib, name)
             f.argtypes = args
             f.restype = I
+        lib.regtile_gemm_mx_workspace.argtypes = [I] * 7
+        lib.regtile_gemm_mx_workspace.restype = ctypes.c_int64
         lib.regtile_last_kernel.argtypes = []
         lib.regtile_last_kernel.restype = ctypes.c_char_p
         lib.regtile_last_kernel_info.argtypes = [ctypes.POINTER(KernelInfo)]
@@ -200,15 +202,19 @@ def regtile_gemm_bf16_algo(algo, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, s
 
 
 def regtile_gemm_bf16_mx(format, trans_a, trans_b, M, N, K, alpha, A, lda, Q, ldq, S, lds, beta, C, ldc,
-                         stream=0) -> int:
+                         work=0, work_bytes=0, stream=0) -> int:
     return load().regtile_gemm_bf16_mx(format, trans_a, trans_b, M, N, K, alpha, A, lda, Q, ldq, S, lds,
-                                       beta, C, ldc, stream)
+                                       beta, C, ldc, work, work_bytes, stream)
 
 
 def regtile_gemm_f16_mx(format, trans_a, trans_b, M, N, K, alpha, A, lda, Q, ldq, S, lds, beta, C, ldc,
-                        stream=0) -> int:
+                        work=0, work_bytes=0, stream=0) -> int:
     return load().regtile_gemm_f16_mx(format, trans_a, trans_b, M, N, K, alpha, A, lda, Q, ldq, S, lds,
-                                      beta, C, ldc, stream)
+                                      beta, C, ldc, work, work_bytes, stream)
+
+
+def regtile_gemm_mx_workspace(trans_a, trans_b, M, N, K, lda, ldc) -> int:
+    return load().regtile_gemm_mx_workspace(trans_a, trans_b, M, N, K, lda, ldc)
 
 
 def regtile_quantize_mx(format, dtype, rows, cols, X, ldx, Q, ldq, S, lds, stream=0) -> int:
@@ -344,12 +350,14 @@ class MXMatrix:
             raise ValueError("codes must be uint8 (int8 is taken for MX_INT8)")
         if scales.dtype != torch.uint8:
             raise ValueError("scales must be uint8")
-        self._ldq, self._lds = _row_major_ld(codes, "codes"), _row_major_ld(scales, "scales")
-        rows = codes.shape[0]
-        if cols < 0 or codes.shape[1] != _row_bytes(format, cols):
-            raise ValueError(f"codes must be {_row_bytes(format, cols)} bytes wide for {cols} columns, not {codes.shape[1]}")
-        if tuple(scales.shape) != (rows, -(-cols // MX_GROUP)):
+        if codes.dim() != 2 or scales.dim() != 2:
+            raise ValueError("codes and scales must be 2-D")
+        rows, width = codes.shape
+        if cols < 0 or width != _row_bytes(format, cols):
+            raise ValueError(f"codes must be {_row_bytes(format, cols)} bytes wide for {cols} columns, not {width}")
+        if scales.shape != (rows, -(-cols // MX_GROUP)):
             raise ValueError(f"scales must be {(rows, -(-cols // MX_GROUP))}, not {tuple(scales.shape)}")
+        self._ldq, self._lds = _row_major_ld(codes, "codes"), _row_major_ld(scales, "scales")
         if codes.device != scales.device:
             raise ValueError("codes and scales are on different devices")
         self.format, self.codes, self.scales = format, codes, scales
@@ -366,9 +374,8 @@ class MXMatrix:
 
     def t(self):
         v = object.__new__(MXMatrix)
-        for name in MXMatrix.__slots__:
-            setattr(v, name, getattr(self, name))
-        v.transposed = not self.transposed
+        v.format, v.codes, v.scales, v.transposed = self.format, self.codes, self.scales, not self.transposed
+        v._rows, v._cols, v._ldq, v._lds = self._rows, self._cols, self._ldq, self._lds
         return v
 
     def __repr__(self):
@@ -377,42 +384,59 @@ class MXMatrix:
 
 
 class _Launch:
-    """Makes `device` the current device and, for what is allocated inside, `stream` the current
-    stream (so that the allocator knows where the memory is used); `handle` is the stream to
-    launch on. Nothing is switched where both are current already."""
+    """Makes `device` the current device and `stream` (None: that device's current one) its current
+    stream for what is allocated and launched inside, so that the allocator knows where the memory
+    is used; entering gives the stream's handle. Most calls switch nothing and skip it (_current)."""
 
-    __slots__ = ("handle", "_contexts")
+    __slots__ = ("_device", "_stream")
 
     def __init__(self, device, stream):
         import torch
 
-        self._contexts = []
-        if torch.cuda.current_device() != device.index:
-            self._contexts.append(torch.cuda.device(device))
         if stream is None:
-            self.handle = torch.cuda.current_stream(device).cuda_stream
-            return
-        if isinstance(stream, int):
+            stream = torch.cuda.current_stream(device)
+        elif isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the operands on {device}")
-        self._contexts.append(torch.cuda.stream(stream))
-        self.handle = stream.cuda_stream
+        self._device, self._stream = torch.cuda.device(device), torch.cuda.stream(stream)
 
     def __enter__(self):
-        for c in self._contexts:
-            c.__enter__()
-        return self.handle
+        self._device.__enter__()
+        self._stream.__enter__()
+        return self._stream.stream.cuda_stream
 
     def __exit__(self, *exc):
-        for c in reversed(self._contexts):
-            c.__exit__(*exc)
+        self._stream.__exit__(*exc)
+        self._device.__exit__(*exc)
+
+
+def _current(device, stream):
+    """The handle of the current stream, where the call is to run on the current device and stream;
+    None where _Launch has to switch."""
+    import torch
+
+    index = device.index
+    if stream is not None or torch.cuda.current_device() != index:
+        return None
+    try:  # the plain handle, without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(index)
+    except AttributeError:
+        return torch.cuda.current_stream(device).cuda_stream
+
+
+def _launched(run, device, stream):
+    """run(handle) on `device` and `stream`, as _Launch arranges it."""
+    handle = _current(device, stream)
+    if handle is not None:
+        return run(handle)
+    with _Launch(device, stream) as handle:
+        return run(handle)
 
 
 def _ints(*values):
-    for v in values:
-        if v > _INT_MAX:
-            raise ValueError(f"sizes and leading dimensions go up to 2**31 - 1, not {v}")
+    if max(values) > _INT_MAX:
+        raise ValueError(f"sizes and leading dimensions go up to 2**31 - 1, not {max(values)}")
 
 
 def _mx_dtype(dtype, name):
@@ -434,18 +458,23 @@ def quantize_mx(X, format=MX_INT8, out=None, stream=None):
     dt = _mx_dtype(X.dtype, "X")
     if not X.is_cuda:
         raise ValueError("quantize_mx takes a device tensor")
+    device = X.device
     ldx = _row_major_ld(X, "X")
     rows, cols = X.shape
-    with _Launch(X.device, stream) as handle:
-        if out is None:
-            out = MXMatrix(format, torch.empty((rows, _row_bytes(format, cols)), dtype=torch.uint8, device=X.device),
-                           torch.empty((rows, -(-cols // MX_GROUP)), dtype=torch.uint8, device=X.device), cols)
-        elif out.format != format or out.transposed or out.shape != (rows, cols) or out.device != X.device:
-            raise ValueError(f"out must be an untransposed MXMatrix of format {format}, shape {(rows, cols)} on {X.device}")
-        _ints(rows, cols, ldx, out._ldq, out._lds)
-        _check(regtile_quantize_mx(format, dt, rows, cols, X.data_ptr(), ldx, out.codes.data_ptr(), out._ldq,
-                                   out.scales.data_ptr(), out._lds, handle))
-    return out
+    if out is not None and (out.format != format or out.transposed or out.shape != (rows, cols) or out.device != device):
+        raise ValueError(f"out must be an untransposed MXMatrix of format {format}, shape {(rows, cols)} on {device}")
+
+    def run(handle):
+        Q = out
+        if Q is None:
+            Q = MXMatrix(format, torch.empty((rows, _row_bytes(format, cols)), dtype=torch.uint8, device=device),
+                         torch.empty((rows, -(-cols // MX_GROUP)), dtype=torch.uint8, device=device), cols)
+        _ints(rows, cols, ldx, Q._ldq, Q._lds)
+        _check(load().regtile_quantize_mx(format, dt, rows, cols, X.data_ptr(), ldx, Q.codes.data_ptr(), Q._ldq,
+                                          Q.scales.data_ptr(), Q._lds, handle))
+        return Q
+
+    return _launched(run, device, stream)
 
 
 def dequantize_mx(Q, dtype=None, out=None, stream=None):
@@ -454,36 +483,42 @@ def dequantize_mx(Q, dtype=None, out=None, stream=None):
     is given). Writes into ``out`` or a new tensor, and returns it."""
     import torch
 
-    if not Q.codes.is_cuda:
+    if not isinstance(Q, MXMatrix) or not Q.codes.is_cuda:
         raise ValueError("dequantize_mx takes an MXMatrix of device tensors")
     if dtype is None:
         dtype = torch.bfloat16 if out is None else out.dtype
     dt = _mx_dtype(dtype, "dtype")
-    rows, cols = Q._rows, Q._cols
-    with _Launch(Q.device, stream) as handle:
+    rows, cols, device = Q._rows, Q._cols, Q.device
+    if out is not None and (out.dtype != dtype or tuple(out.shape) != Q.shape or out.device != device):
+        raise ValueError(f"out must be {dtype} of shape {Q.shape} on {device}")
+
+    def run(handle):
         if out is None:
-            X = torch.empty((rows, cols), dtype=dtype, device=Q.device)
+            X = torch.empty((rows, cols), dtype=dtype, device=device)
         else:
-            if out.dtype != dtype or tuple(out.shape) != Q.shape or out.device != Q.device:
-                raise ValueError(f"out must be {dtype} of shape {Q.shape} on {Q.device}")
             X = out.t() if Q.transposed else out
         ldx = _row_major_ld(X, "out")
         _ints(rows, cols, ldx, Q._ldq, Q._lds)
-        _check(regtile_dequantize_mx(Q.format, dt, rows, cols, Q.codes.data_ptr(), Q._ldq, Q.scales.data_ptr(),
-                                     Q._lds, X.data_ptr(), ldx, handle))
+        _check(load().regtile_dequantize_mx(Q.format, dt, rows, cols, Q.codes.data_ptr(), Q._ldq, Q.scales.data_ptr(),
+                                            Q._lds, X.data_ptr(), ldx, handle))
+        return X
+
+    X = _launched(run, device, stream)
     if out is not None:
         return out
     return X.t() if Q.transposed else X
 
 
-def _gemm_mx(fn, want, label, A, B, C, alpha, beta, stream):
-    if A.dtype != want:
-        raise ValueError(f"{label} takes {want} A")
+def _gemm_mx(name, want, A, B, C, alpha, beta, stream):
+    import torch
+
     if not isinstance(B, MXMatrix):
-        raise ValueError(f"{label} takes an MXMatrix B")
+        raise ValueError(f"{name} takes an MXMatrix B")
+    if A.dtype != want:
+        raise ValueError(f"{name} takes {want} A")
     device = A.device
     if not A.is_cuda or B.codes.device != device or (C is not None and C.device != device):
-        raise ValueError(f"{label} takes device tensors, all on one device")
+        raise ValueError(f"{name} takes device tensors, all on one device")
     ta, lda = _layout(A, "A")
     M, K = A.shape
     K2, N = B.shape
@@ -491,13 +526,24 @@ def _gemm_mx(fn, want, label, A, B, C, alpha, beta, stream):
         raise ValueError(f"inner dimensions differ: {K} vs {K2}")
     if C is None and beta != 0.0:
         raise ValueError("beta != 0 needs C")
-    with _Launch(device, stream) as handle:
-        C = _out(C, M, N, A)
-        ldc = _row_major_ld(C, "C")
-        _ints(M, N, K, lda, B._ldq, B._lds, ldc)
-        _check(fn(B.format, ta, int(B.transposed), M, N, K, float(alpha), A.data_ptr(), lda, B.codes.data_ptr(),
-                  B._ldq, B.scales.data_ptr(), B._lds, float(beta), C.data_ptr(), ldc, handle))
-    return C
+    ldc = max(N, 1) if C is None else _row_major_ld(_out(C, M, N, A), "C")
+    ldq, lds, tb = B._ldq, B._lds, 1 if B.transposed else 0
+    _ints(M, N, K, lda, ldq, lds, ldc)
+    lib = _lib or load()
+
+    def run(handle):
+        out = torch.empty((M, N), dtype=torch.float32, device=device) if C is None else C
+        work, size = None, 0
+        if M > 64:  # fewer rows never use a workspace
+            size = lib.regtile_gemm_mx_workspace(ta, tb, M, N, K, lda, ldc)
+            if size > 0:
+                work = torch.empty(size, dtype=torch.uint8, device=device)
+        _check(getattr(lib, name)(B.format, ta, tb, M, N, K, alpha, A.data_ptr(), lda, B.codes.data_ptr(), ldq,
+                                  B.scales.data_ptr(), lds, beta, out.data_ptr(), ldc,
+                                  0 if work is None else work.data_ptr(), size, handle))
+        return out
+
+    return _launched(run, device, stream)
 
 
 def gemm_bf16_mx(A, B, C=None, alpha=1.0, beta=0.0, stream=None):
@@ -506,11 +552,11 @@ def gemm_bf16_mx(A, B, C=None, alpha=1.0, beta=0.0, stream=None):
     when None)."""
     import torch
 
-    return _gemm_mx(regtile_gemm_bf16_mx, torch.bfloat16, "gemm_bf16_mx", A, B, C, alpha, beta, stream)
+    return _gemm_mx("regtile_gemm_bf16_mx", torch.bfloat16, A, B, C, alpha, beta, stream)
 
 
 def gemm_f16_mx(A, B, C=None, alpha=1.0, beta=0.0, stream=None):
     """As gemm_bf16_mx with a float16 A; B's values are taken in float16."""
     import torch
 
-    return _gemm_mx(regtile_gemm_f16_mx, torch.float16, "gemm_f16_mx", A, B, C, alpha, beta, stream)
+    return _gemm_mx("regtile_gemm_f16_mx", torch.float16, A, B, C, alpha, beta, stream)

@@ -40,7 +40,8 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
                                                         const uint16_t *__restrict__ A, int64_t lda,
                                                         const uint8_t *__restrict__ Q, int64_t ldq,
                                                         const uint8_t *__restrict__ S, int64_t lds, float beta,
-                                                        float *__restrict__ C, int64_t ldc, int tiles_m, int tiles_n) {
+                                                        float *__restrict__ C, int64_t ldc, int tiles_m, int tiles_n,
+                                                        int per_split, int64_t split_stride) {
     constexpr int MF = 32, KCH = MXD_BK / 8, MCH = T / 8;
     typedef Frag<MF, F16> F;
     constexpr int WT = T / 2, MI = WT / MF, NI = WT / MF;
@@ -59,10 +60,14 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int wm = wave >> 1, wn = wave & 1;
+    const int id = xcd_contiguous_id(blockIdx.x, gridDim.x), tiles = tiles_m * tiles_n;
+    const int split = id / tiles;  // part of k, per_split slabs
     int tm, tn;
-    grouped_tile<8>(xcd_contiguous_id(blockIdx.x, gridDim.x), tiles_m, tiles_n, tm, tn);
+    grouped_tile<8>(id - split * tiles, tiles_m, tiles_n, tm, tn);
     const int m0 = tm * T, n0 = tn * T;
-    const int nslabs = (K + MXD_BK - 1) / MXD_BK, k_last = (nslabs - 1) * MXD_BK;
+    const int all_slabs = (K + MXD_BK - 1) / MXD_BK, k_last = (all_slabs - 1) * MXD_BK;
+    const int first_slab = split * per_split, nslabs = min(per_split, all_slabs - first_slab);
+    C += split * split_stride;
 
     // ---- A ----
     const rsrc_t a_rsrc = A_MN ? make_rsrc(A + m0, addr::desc_bytes(K, lda, M - m0, 2))
@@ -76,7 +81,7 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
         if (A_MN) a_voff[j] = addr::mn_dma_lane(lane, j, lda, MCH);
     }
     auto dma_a = [&](int q, int slab, int half) {
-        const int k0 = min(slab, nslabs - 1) * MXD_BK;
+        const int k0 = (first_slab + min(slab, nslabs - 1)) * MXD_BK;
         const uint32_t voff = KTAIL && !A_MN && k0 == k_last ? a_voff_last[q & 1] : a_voff[q & 1];
         const uint32_t soff = A_MN ? addr::mn_dma_instr(wave, JA, q, k0, lda, MCH) : addr::kc_dma_instr<KCH>(q, k0, lda);
         dma16_buf(a_rsrc, voff, soff, smem + half * HALF + (wave * JA + q) * 64);
@@ -102,7 +107,8 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
         sbase[i] = S + row * lds + g;
     }
     uint32_t q[NG][GB / 4], sc[NG];
-    auto load_group = [&](int i, int slab) {
+    auto load_group = [&](int i, int s) {
+        const int slab = first_slab + s;
         int64_t qo, so;
         if constexpr (B_MN) {
             const int64_t k = min((int64_t)slab * MXD_BK + b_row[i], (int64_t)K - 1);
@@ -120,7 +126,8 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
         const int low = T == 256 ? ((r & 1) << 1) | ((c >> 4) & 1) : r & 3;
         return r * MCH + (c ^ (4 * (r & 3)) ^ low);
     };
-    auto write_group = [&](int i, int slab, int half) {
+    auto write_group = [&](int i, int s_, int half) {
+        const int slab = first_slab + s_;
         const bool past = B_MN ? slab * MXD_BK + b_row[i] >= K : 2 * slab + b_g[i] > last_g;
         const float s = mx::scale_value<FP4>(past ? 0u : sc[i]);
         uint4 *d = smem + half * HALF;
@@ -303,6 +310,47 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
     }
 }
 
+// C = alpha (sum of the splits' parts, in their order) + beta C; bound by reading the parts
+__global__ __launch_bounds__(256) void mx_join_kernel(int splits, int M, int N, float alpha,
+                                                      const float *__restrict__ work, float beta,
+                                                      float *__restrict__ C, int64_t ldc, int vec) {
+    const int64_t n = (int64_t)M * N, per_row = vec ? N / 4 : N, total = vec ? n / 4 : n;
+    for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < total; u += (int64_t)gridDim.x * 256) {
+        int64_t row, unit;
+        if (total < (int64_t(1) << 32)) {
+            row = (uint32_t)u / (uint32_t)per_row;
+            unit = (uint32_t)u - (uint32_t)row * (uint32_t)per_row;
+        } else {
+            row = u / per_row;
+            unit = u - row * per_row;
+        }
+        if (vec) {
+            const float4 *w = reinterpret_cast<const float4 *>(work) + u;
+            float4 v = w[0];
+            for (int z = 1; z < splits; ++z) {
+                const float4 p = w[z * (n / 4)];
+                v.x += p.x;
+                v.y += p.y;
+                v.z += p.z;
+                v.w += p.w;
+            }
+            float4 *c = reinterpret_cast<float4 *>(C + row * ldc) + unit;
+            if (beta == 0.0f) {
+                *c = make_float4(alpha * v.x, alpha * v.y, alpha * v.z, alpha * v.w);
+            } else {
+                const float4 o = *c;
+                *c = make_float4(fmaf(alpha, v.x, beta * o.x), fmaf(alpha, v.y, beta * o.y), fmaf(alpha, v.z, beta * o.z),
+                                 fmaf(alpha, v.w, beta * o.w));
+            }
+        } else {
+            float v = work[u];
+            for (int z = 1; z < splits; ++z) v += work[z * n + u];
+            float *c = C + row * ldc + unit;
+            *c = epilogue_value(v, alpha, beta, c);
+        }
+    }
+}
+
 #ifndef MXD_WIN
 #define MXD_WIN 1
 #define MXD_STAG 1
@@ -311,30 +359,56 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
 #endif
 
 template <bool FP4, bool F16, bool A_MN, bool B_MN, bool KTAIL>
-hipError_t launch_mxd(const MxProblem &p, hipStream_t s, int t) {
+hipError_t launch_mxd(const MxProblem &p, hipStream_t s, int t, int splits) {
     const int tiles_m = (p.M + t - 1) / t, tiles_n = (p.N + t - 1) / t;
-    const dim3 grid((unsigned)((int64_t)tiles_m * tiles_n));
+    const dim3 grid((unsigned)((int64_t)tiles_m * tiles_n * splits));
+    const int slabs = (p.K + MXD_BK - 1) / MXD_BK, per = (slabs + splits - 1) / splits;
+    // with more than one split the tiles' sums go to the workspace, M x N for each split
+    const bool direct = splits == 1;
+    float *const out = direct ? p.C : (float *)p.work;
+    const int64_t ldo = direct ? p.ldc : p.N, stride = direct ? 0 : (int64_t)p.M * p.N;
+    const float alpha = direct ? p.alpha : 1.0f, beta = direct ? p.beta : 0.0f;
 #define REGTILE_MXD(T_, W_, S_)                                                                                    \
     do {                                                                                                           \
         note_launch(reinterpret_cast<const void *>(&mx_dma_kernel<T_, FP4, F16, A_MN, B_MN, KTAIL, W_, S_>), MXD_NT); \
         hipLaunchKernelGGL((mx_dma_kernel<T_, FP4, F16, A_MN, B_MN, KTAIL, W_, S_>), grid, dim3(MXD_NT), 0, s, p.M,   \
-                           p.N, p.K, p.alpha, (const uint16_t *)p.A, p.lda, p.Q, p.ldq, p.S, p.lds, p.beta, p.C,    \
-                           p.ldc, tiles_m, tiles_n);                                                               \
+                           p.N, p.K, alpha, (const uint16_t *)p.A, p.lda, p.Q, p.ldq, p.S, p.lds, beta, out, ldo,   \
+                           tiles_m, tiles_n, per, stride);                                                         \
     } while (0)
     if (t == 256) REGTILE_MXD(256, MXD_WIN, MXD_STAG);
     else REGTILE_MXD(128, MXD_SWIN, MXD_SSTAG);
 #undef REGTILE_MXD
+    if (!direct) {
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        const int64_t n = (int64_t)p.M * p.N;
+        const int vec = p.N % 4 == 0 && p.ldc % 4 == 0 && aligned16(p.C) && aligned16(p.work);
+        const int64_t units = vec ? n / 4 : n, blocks = (units + 255) / 256;
+        hipLaunchKernelGGL(mx_join_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, splits,
+                           p.M, p.N, p.alpha, (const float *)p.work, p.beta, p.C, p.ldc, vec);
+    }
     return hipGetLastError();
 }
 template <bool FP4, bool F16>
-hipError_t launch_mxd_order(const MxProblem &p, hipStream_t s, int t) {
+hipError_t launch_mxd_order(const MxProblem &p, hipStream_t s, int t, int splits) {
     const bool ktail = p.K % MXD_BK != 0;  // (an M-contiguous A ends with its descriptor)
-    if (p.ta) return p.tb ? launch_mxd<FP4, F16, true, false, false>(p, s, t) : launch_mxd<FP4, F16, true, true, false>(p, s, t);
-    if (p.tb) return ktail ? launch_mxd<FP4, F16, false, false, true>(p, s, t) : launch_mxd<FP4, F16, false, false, false>(p, s, t);
-    return ktail ? launch_mxd<FP4, F16, false, true, true>(p, s, t) : launch_mxd<FP4, F16, false, true, false>(p, s, t);
+    if (p.ta) return p.tb ? launch_mxd<FP4, F16, true, false, false>(p, s, t, splits) : launch_mxd<FP4, F16, true, true, false>(p, s, t, splits);
+    if (p.tb) return ktail ? launch_mxd<FP4, F16, false, false, true>(p, s, t, splits) : launch_mxd<FP4, F16, false, false, false>(p, s, t, splits);
+    return ktail ? launch_mxd<FP4, F16, false, true, true>(p, s, t, splits) : launch_mxd<FP4, F16, false, true, false>(p, s, t, splits);
 }
 
 }  // namespace
+
+// How many parts of k the product wants (1: none): see launch_mx_dma.
+int mx_splits(bool ta, bool tb, int M, int N, int K, int64_t lda, int64_t ldc) {
+    if (!addr::mx_dma_takes(ta, tb, M, N, K, lda, ldc)) return 1;
+    const int64_t tiles = (int64_t)((M + 127) / 128) * ((N + 127) / 128);
+    const int slabs = (K + MXD_BK - 1) / MXD_BK;
+    if (tiles > 128) return 1;
+    const int64_t want = 512 / tiles, most = slabs / 8;
+    const int64_t n = want < most ? want : most;
+    return n < 1 ? 1 : n > 16 ? 16 : (int)n;
+}
 
 // Takes (and launches, status in *err) a problem whose A meets the 16-bit kernels' DMA conditions
 // in its storage order (addr::mx_dma_takes) with 16-byte aligned rows and whose B has whole groups;
@@ -342,6 +416,22 @@ hipError_t launch_mxd_order(const MxProblem &p, hipStream_t s, int t) {
 bool launch_mx_dma(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err) {
     if (!addr::mx_dma_takes(p.ta, p.tb, p.M, p.N, p.K, p.lda, p.ldc) || !aligned16(p.A)) return false;
     const int t = addr::dma_tile(p.M, p.N);
+    int splits = 1;
+    if (t == 128 && p.work != nullptr) {
+        const int64_t part = (int64_t)p.M * p.N * 4;
+        const int64_t fit = p.work_bytes / part;
+#ifdef MXD_FORCE
+        const int want = 1 << 20;
+#else
+        const int want = mx_splits(p.ta, p.tb, p.M, p.N, p.K, p.lda, p.ldc);
+#endif
+        splits = (int)(fit < want ? fit : want);
+        const int slabs = (p.K + MXD_BK - 1) / MXD_BK;
+        if (splits > slabs) splits = slabs;
+        if (splits < 1) splits = 1;
+        const int per = (slabs + splits - 1) / splits;
+        splits = (slabs + per - 1) / per;  // every split has slabs
+    }
 #define REGTILE_MXD_NAMES(elt, fmt, t) \
     {{elt "_" fmt "_dma_" t "_nn", elt "_" fmt "_dma_" t "_nt"}, {elt "_" fmt "_dma_" t "_tn", elt "_" fmt "_dma_" t "_tt"}}
 #define REGTILE_MXD_SIZES(elt, fmt) {REGTILE_MXD_NAMES(elt, fmt, "256x256x64"), REGTILE_MXD_NAMES(elt, fmt, "128x128x64")}
@@ -351,9 +441,9 @@ bool launch_mx_dma(const MxProblem &p, hipStream_t s, const char **name, hipErro
 #undef REGTILE_MXD_NAMES
     *name = names[p.f16][p.fp4][t == 128][p.ta][p.tb];
     if (p.fp4)
-        *err = p.f16 ? launch_mxd_order<true, true>(p, s, t) : launch_mxd_order<true, false>(p, s, t);
+        *err = p.f16 ? launch_mxd_order<true, true>(p, s, t, splits) : launch_mxd_order<true, false>(p, s, t, splits);
     else
-        *err = p.f16 ? launch_mxd_order<false, true>(p, s, t) : launch_mxd_order<false, false>(p, s, t);
+        *err = p.f16 ? launch_mxd_order<false, true>(p, s, t, splits) : launch_mxd_order<false, false>(p, s, t, splits);
     return true;
 }
 

@@ -158,10 +158,11 @@ int run_16b(bool f16, int shift, int algo, bool ta, bool tb, int M, int N, int K
 bool bad_format(int f) { return f != REGTILE_MX_FP4 && f != REGTILE_MX_INT8; }
 
 // The product with a block-scaled B. Positions as in the declaration: format 1, trans_a 2,
-// trans_b 3, M 4, N 5, K 6, alpha 7, A 8, lda 9, Q 10, ldq 11, S 12, lds 13, beta 14, C 15, ldc 16.
+// trans_b 3, M 4, N 5, K 6, alpha 7, A 8, lda 9, Q 10, ldq 11, S 12, lds 13, beta 14, C 15, ldc 16,
+// work 17, work_bytes 18.
 int run_mx(bool f16, int format, int trans_a, int trans_b, int M, int N, int K, float alpha,
            const uint16_t *A, int lda, const uint8_t *Q, int ldq, const uint8_t *S, int lds,
-           float beta, float *C, int ldc, void *stream) {
+           float beta, float *C, int ldc, void *work, int64_t work_bytes, void *stream) {
     if (bad_format(format)) return -1;
     if (bad_flag(trans_a)) return -2;
     if (bad_flag(trans_b)) return -3;
@@ -180,6 +181,8 @@ int run_mx(bool f16, int format, int trans_a, int trans_b, int M, int N, int K, 
     if (lds < (lds_min > 1 ? lds_min : 1)) return -13;
     if (M > 0 && N > 0 && C == nullptr) return -15;
     if (ldc < (N > 1 ? N : 1)) return -16;
+    if ((reinterpret_cast<uintptr_t>(work) & 15u) != 0) return -17;
+    if (work_bytes < 0 || (work == nullptr && work_bytes != 0)) return -18;
     regtile::MxProblem p;
     p.M = M;
     p.N = N;
@@ -198,6 +201,8 @@ int run_mx(bool f16, int format, int trans_a, int trans_b, int M, int N, int K, 
     p.tb = trans_b != 0;
     p.fp4 = fp4;
     p.f16 = f16;
+    p.work = work;
+    p.work_bytes = work_bytes;
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     int status;
     if (quick_return(make_problem(M, N, K, alpha, A, lda, Q, ldq, beta, C, ldc, trans_a, trans_b), s, &status))
@@ -340,14 +345,22 @@ int regtile_dequantize_mx(int format, int dtype, int rows, int cols, const uint8
 
 int regtile_gemm_bf16_mx(int format, int trans_a, int trans_b, int M, int N, int K, float alpha, const uint16_t *A,
                          int lda, const uint8_t *Q, int ldq, const uint8_t *S, int lds, float beta, float *C, int ldc,
-                         void *stream) {
-    return run_mx(false, format, trans_a, trans_b, M, N, K, alpha, A, lda, Q, ldq, S, lds, beta, C, ldc, stream);
+                         void *work, int64_t work_bytes, void *stream) {
+    return run_mx(false, format, trans_a, trans_b, M, N, K, alpha, A, lda, Q, ldq, S, lds, beta, C, ldc, work,
+                  work_bytes, stream);
 }
 
 int regtile_gemm_f16_mx(int format, int trans_a, int trans_b, int M, int N, int K, float alpha, const uint16_t *A,
                         int lda, const uint8_t *Q, int ldq, const uint8_t *S, int lds, float beta, float *C, int ldc,
-                        void *stream) {
-    return run_mx(true, format, trans_a, trans_b, M, N, K, alpha, A, lda, Q, ldq, S, lds, beta, C, ldc, stream);
+                        void *work, int64_t work_bytes, void *stream) {
+    return run_mx(true, format, trans_a, trans_b, M, N, K, alpha, A, lda, Q, ldq, S, lds, beta, C, ldc, work, work_bytes,
+                  stream);
+}
+
+int64_t regtile_gemm_mx_workspace(int trans_a, int trans_b, int M, int N, int K, int lda, int ldc) {
+    if (bad_flag(trans_a) || bad_flag(trans_b) || M <= 0 || N <= 0 || K <= 0) return 0;
+    const int n = regtile::mx_splits(trans_a != 0, trans_b != 0, M, N, K, lda, ldc);
+    return n > 1 ? (int64_t)n * M * N * 4 : 0;
 }
 
 const char *regtile_last_kernel(void) { return g_last_kernel; }

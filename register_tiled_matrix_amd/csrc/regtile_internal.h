@@ -37,6 +37,8 @@ struct MxProblem {
     float *C;
     int64_t ldc;
     bool ta, tb, fp4, f16;
+    void *work;  // workspace, or null
+    int64_t work_bytes;
 };
 
 // One validated conversion: X rows x cols of regtile_mx_dtype, and its codes and scales.
@@ -97,6 +99,9 @@ bool launch_mx_token(const MxProblem &p, hipStream_t s, const char **name, hipEr
 // The product on DMA-fed tiles for aligned A and whole groups of B (addr::mx_dma_takes); false,
 // launching nothing, for any other problem.
 bool launch_mx_dma(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err);
+// Parts of k that launch_mx_dma makes of a product when it is given a workspace of one M x N fp32
+// matrix for each (1: it makes no use of one).
+int mx_splits(bool ta, bool tb, int M, int N, int K, int64_t lda, int64_t ldc);
 // The default 16-bit entry points take the split-K kernel for problems of few 64x64 tiles with
 // enough K per wave: at most 256 tiles (one per CU) with K >= 1024 in any storage order, and at
 // most 512 with K >= 4096 for K-contiguous A and B ("n t") or M/N-contiguous both ("t n").

@@ -206,6 +206,36 @@ def test_product_dma(fmt, order, M, N, K):
     assert "_dma_" in rt.last_kernel()
 
 
+@pytest.mark.parametrize("M,N,K", [(72, 96, 2048), (128, 288, 4096 + 32), (264, 136 + 24, 8192)])
+@pytest.mark.parametrize("order", ORDERS)
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_product_split_over_workgroups(fmt, order, M, N, K):
+    """Few tiles, long K: partial sums through the workspace, joined in order; with any smaller
+    workspace (none among them) the call makes fewer splits."""
+    rng = np.random.default_rng(M + N + K)
+    ta, tb = order[0] == "t", order[1] == "t"
+    size = rt.regtile_gemm_mx_workspace(int(ta), int(tb), M, N, K, M if ta else K, N)
+    assert size >= 2 * M * N * 4
+    product(rng, fmt, "bf16", order, M, N, K, label="split")
+    product(rng, fmt, "f16", order, M, N, K, alpha=-1.5, beta=1.0, c_pad=1, label="split")
+    A = half_matrix(rng, *((K, M) if ta else (M, K)), "bf16")
+    rows, cols = (N, K) if tb else (K, N)
+    codes, scales = random_codes(rng, fmt, rows, cols)
+    Ad, Qd, Sd = A.cuda(), dev(codes), dev(scales)
+    a, b = A.double().numpy(), mx.decode(codes, scales, fmt, cols)
+    a, b = (a.T if ta else a), (b.T if tb else b)
+    for parts in (0, 1, 2, 3, 1000):
+        work = torch.full((parts * M * N + 4,), float("nan"), device="cuda")
+        C = torch.empty(M, N, device="cuda")
+        assert rt.regtile_gemm_bf16_mx(fmt, int(ta), int(tb), M, N, K, 1.0, Ad.data_ptr(), Ad.stride(0), Qd.data_ptr(),
+                                       Qd.stride(0), Sd.data_ptr(), Sd.stride(0), 0.0, C.data_ptr(), N,
+                                       work.data_ptr() if parts else 0, parts * M * N * 4,
+                                       torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        assert_close(C, a @ b, np.abs(a) @ np.abs(b), f"{parts} parts")
+        assert bool(work[parts * M * N:].isnan().all())
+
+
 @pytest.mark.parametrize("order", ORDERS)
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_infinite_groups_do_not_reach_past_the_edge(fmt, order):
@@ -323,7 +353,7 @@ def test_refusals():
 
 def test_repeated_calls_give_identical_bits():
     rng = np.random.default_rng(5)
-    for order, M, N, K in (("nt", 1, 1024, 4096), ("nt", 24, 512, 4096), ("nn", 200, 256, 1000), ("tn", 256, 256, 4096)):
+    for order, M, N, K in (("nt", 1, 1024, 4096), ("nt", 24, 512, 4096), ("nn", 200, 256, 1000), ("tn", 256, 256, 4096), ("tn", 256, 256, 8192)):
         rows, cols = (N, K) if order[1] == "t" else (K, N)
         codes, scales = random_codes(rng, mx.INT8, rows, cols)
         B = rt.MXMatrix(mx.INT8, dev(codes), dev(scales), cols)

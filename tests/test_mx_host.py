@@ -26,7 +26,7 @@ def _built():
 def test_gemm_arguments(fn):
     f = getattr(rt, fn)
     base = dict(format=rt.MX_FP4, ta=0, tb=1, M=4, N=5, K=65, alpha=1.0, A=DUMMY, lda=65, Q=DUMMY, ldq=33, S=DUMMY,
-                lds=3, beta=0.0, C=DUMMY, ldc=5)
+                lds=3, beta=0.0, C=DUMMY, ldc=5, work=0, work_bytes=0)
 
     def call(**kw):
         return f(*{**base, **kw}.values(), 0)
@@ -41,6 +41,8 @@ def test_gemm_arguments(fn):
     assert call(format=rt.MX_INT8, ldq=64) == -11
     assert call(S=0) == -12 and call(lds=2) == -13
     assert call(C=0) == -15 and call(ldc=4) == -16
+    assert call(work=DUMMY + 8, work_bytes=64) == -17
+    assert call(work=DUMMY, work_bytes=-1) == -18 and call(work_bytes=16) == -18
     # B stored K x N: its rows are N columns wide
     assert call(tb=0, ldq=2) == -11 and call(tb=0, N=33, ldc=33, ldq=17, lds=1) == -13
     # nothing is read or launched where there is no output
@@ -132,3 +134,13 @@ def test_reference_encoder_on_known_groups():
     assert E.tolist() == [[255]]
     _, E = mx.encode(np.zeros((1, 40)), mx.FP4)
     assert E.tolist() == [[0, 0]]
+
+
+def test_workspace_sizes():
+    f = rt.regtile_gemm_mx_workspace
+    # few tiles and a long K: whole parts of M x N floats
+    n = f(1, 0, 1024, 1024, 16384, 1024, 1024)
+    assert n > 0 and n % (1024 * 1024 * 4) == 0
+    assert f(0, 1, 8192, 8192, 8192, 8192, 8192) == 0   # the tiles fill the chip
+    assert f(0, 1, 128, 128, 64, 64, 128) == 0          # nothing to split
+    assert f(0, 1, 0, 128, 64, 64, 128) == 0 and f(2, 1, 128, 128, 64, 64, 128) == 0
