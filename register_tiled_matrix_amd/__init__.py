@@ -330,6 +330,28 @@ def _check_format(format):
         raise ValueError(f"unknown block-scaled format {format!r}")
 
 
+_torch = None  # torch, once the first of these calls needs it
+
+
+def _import_torch():
+    global _torch
+    import torch
+
+    _torch = torch
+    return torch
+
+
+def _rows(t, name):
+    """(leading dimension, rows, columns) of a row-major 2-D tensor; others are rejected."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, cols = t.shape
+    row, col = t.stride()
+    if (col == 1 or cols <= 1) and (row >= cols or rows <= 1):
+        return max(row, cols, 1), rows, cols
+    return _row_major_ld(t, name), rows, cols  # raises
+
+
 class MXMatrix:
     """A block-scaled matrix of ``rows`` x ``cols`` values (include/regtile.h states the layout).
 
@@ -342,22 +364,19 @@ class MXMatrix:
     __slots__ = ("format", "codes", "scales", "transposed", "_rows", "_cols", "_ldq", "_lds")
 
     def __init__(self, format, codes, scales, cols, transposed=False):
-        import torch
-
+        torch = _torch or _import_torch()
         _check_format(format)
         cols = int(cols)
-        if codes.dtype != torch.uint8 and not (codes.dtype == torch.int8 and format == MX_INT8):
+        if codes.dtype is not torch.uint8 and not (codes.dtype is torch.int8 and format == MX_INT8):
             raise ValueError("codes must be uint8 (int8 is taken for MX_INT8)")
-        if scales.dtype != torch.uint8:
+        if scales.dtype is not torch.uint8:
             raise ValueError("scales must be uint8")
-        if codes.dim() != 2 or scales.dim() != 2:
-            raise ValueError("codes and scales must be 2-D")
-        rows, width = codes.shape
+        self._ldq, rows, width = _rows(codes, "codes")
+        self._lds, srows, groups = _rows(scales, "scales")
         if cols < 0 or width != _row_bytes(format, cols):
             raise ValueError(f"codes must be {_row_bytes(format, cols)} bytes wide for {cols} columns, not {width}")
-        if scales.shape != (rows, -(-cols // MX_GROUP)):
-            raise ValueError(f"scales must be {(rows, -(-cols // MX_GROUP))}, not {tuple(scales.shape)}")
-        self._ldq, self._lds = _row_major_ld(codes, "codes"), _row_major_ld(scales, "scales")
+        if srows != rows or groups != -(-cols // MX_GROUP):
+            raise ValueError(f"scales must be {(rows, -(-cols // MX_GROUP))}, not {(srows, groups)}")
         if codes.device != scales.device:
             raise ValueError("codes and scales are on different devices")
         self.format, self.codes, self.scales = format, codes, scales
@@ -414,8 +433,7 @@ class _Launch:
 def _current(device, stream):
     """The handle of the current stream, where the call is to run on the current device and stream;
     None where _Launch has to switch."""
-    import torch
-
+    torch = _torch or _import_torch()
     index = device.index
     if stream is not None or torch.cuda.current_device() != index:
         return None
@@ -425,13 +443,13 @@ def _current(device, stream):
         return torch.cuda.current_stream(device).cuda_stream
 
 
-def _launched(run, device, stream):
-    """run(handle) on `device` and `stream`, as _Launch arranges it."""
+def _launched(run, device, stream, *args):
+    """run(*args, handle) on `device` and `stream`, as _Launch arranges it."""
     handle = _current(device, stream)
     if handle is not None:
-        return run(handle)
+        return run(*args, handle)
     with _Launch(device, stream) as handle:
-        return run(handle)
+        return run(*args, handle)
 
 
 def _ints(*values):
@@ -440,8 +458,7 @@ def _ints(*values):
 
 
 def _mx_dtype(dtype, name):
-    import torch
-
+    torch = _torch or _import_torch()
     try:
         return {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}[dtype]
     except KeyError:
@@ -452,69 +469,61 @@ def quantize_mx(X, format=MX_INT8, out=None, stream=None):
     """The block-scaled form of a row-major device tensor X (float32, bfloat16 or float16); groups
     run along its rows. Writes into ``out`` (an MXMatrix of X's shape and the format) or a new
     MXMatrix, and returns it."""
-    import torch
-
     _check_format(format)
     dt = _mx_dtype(X.dtype, "X")
     if not X.is_cuda:
         raise ValueError("quantize_mx takes a device tensor")
-    device = X.device
-    ldx = _row_major_ld(X, "X")
-    rows, cols = X.shape
-    if out is not None and (out.format != format or out.transposed or out.shape != (rows, cols) or out.device != device):
-        raise ValueError(f"out must be an untransposed MXMatrix of format {format}, shape {(rows, cols)} on {device}")
+    ldx, rows, cols = _rows(X, "X")
+    if out is not None and (out.format != format or out.transposed or out.shape != (rows, cols) or out.device != X.device):
+        raise ValueError(f"out must be an untransposed MXMatrix of format {format}, shape {(rows, cols)} on {X.device}")
+    return _launched(_run_quantize, X.device, stream, X, format, dt, rows, cols, ldx, out)
 
-    def run(handle):
-        Q = out
-        if Q is None:
-            Q = MXMatrix(format, torch.empty((rows, _row_bytes(format, cols)), dtype=torch.uint8, device=device),
-                         torch.empty((rows, -(-cols // MX_GROUP)), dtype=torch.uint8, device=device), cols)
-        _ints(rows, cols, ldx, Q._ldq, Q._lds)
-        _check(load().regtile_quantize_mx(format, dt, rows, cols, X.data_ptr(), ldx, Q.codes.data_ptr(), Q._ldq,
-                                          Q.scales.data_ptr(), Q._lds, handle))
-        return Q
 
-    return _launched(run, device, stream)
+def _run_quantize(X, format, dt, rows, cols, ldx, Q, handle):
+    if Q is None:
+        u8 = _torch.uint8
+        Q = MXMatrix(format, X.new_empty((rows, _row_bytes(format, cols)), dtype=u8),
+                     X.new_empty((rows, -(-cols // MX_GROUP)), dtype=u8), cols)
+    _ints(rows, cols, ldx, Q._ldq, Q._lds)
+    _check((_lib or load()).regtile_quantize_mx(format, dt, rows, cols, X.data_ptr(), ldx, Q.codes.data_ptr(), Q._ldq,
+                                                Q.scales.data_ptr(), Q._lds, handle))
+    return Q
 
 
 def dequantize_mx(Q, dtype=None, out=None, stream=None):
     """The values of an MXMatrix as a row-major tensor of its shape (of a transposed one: the
     transposed view of a row-major tensor), rounded to ``dtype`` (bfloat16 when neither it nor ``out``
     is given). Writes into ``out`` or a new tensor, and returns it."""
-    import torch
-
+    torch = _torch or _import_torch()
     if not isinstance(Q, MXMatrix) or not Q.codes.is_cuda:
         raise ValueError("dequantize_mx takes an MXMatrix of device tensors")
     if dtype is None:
         dtype = torch.bfloat16 if out is None else out.dtype
     dt = _mx_dtype(dtype, "dtype")
-    rows, cols, device = Q._rows, Q._cols, Q.device
-    if out is not None and (out.dtype != dtype or tuple(out.shape) != Q.shape or out.device != device):
-        raise ValueError(f"out must be {dtype} of shape {Q.shape} on {device}")
-
-    def run(handle):
-        if out is None:
-            X = torch.empty((rows, cols), dtype=dtype, device=device)
-        else:
-            X = out.t() if Q.transposed else out
-        ldx = _row_major_ld(X, "out")
-        _ints(rows, cols, ldx, Q._ldq, Q._lds)
-        _check(load().regtile_dequantize_mx(Q.format, dt, rows, cols, Q.codes.data_ptr(), Q._ldq, Q.scales.data_ptr(),
-                                            Q._lds, X.data_ptr(), ldx, handle))
-        return X
-
-    X = _launched(run, device, stream)
+    if out is not None and (out.dtype != dtype or tuple(out.shape) != Q.shape or out.device != Q.device):
+        raise ValueError(f"out must be {dtype} of shape {Q.shape} on {Q.device}")
+    X = _launched(_run_dequantize, Q.device, stream, Q, dtype, dt, out)
     if out is not None:
         return out
     return X.t() if Q.transposed else X
 
 
-def _gemm_mx(name, want, A, B, C, alpha, beta, stream):
-    import torch
+def _run_dequantize(Q, dtype, dt, out, handle):
+    if out is None:
+        X = Q.codes.new_empty((Q._rows, Q._cols), dtype=dtype)
+    else:
+        X = out.t() if Q.transposed else out
+    ldx, rows, cols = _rows(X, "out")
+    _ints(rows, cols, ldx, Q._ldq, Q._lds)
+    _check((_lib or load()).regtile_dequantize_mx(Q.format, dt, rows, cols, Q.codes.data_ptr(), Q._ldq,
+                                                  Q.scales.data_ptr(), Q._lds, X.data_ptr(), ldx, handle))
+    return X
 
+
+def _gemm_mx(name, want, A, B, C, alpha, beta, stream):
     if not isinstance(B, MXMatrix):
         raise ValueError(f"{name} takes an MXMatrix B")
-    if A.dtype != want:
+    if A.dtype is not want:
         raise ValueError(f"{name} takes {want} A")
     device = A.device
     if not A.is_cuda or B.codes.device != device or (C is not None and C.device != device):
@@ -524,39 +533,39 @@ def _gemm_mx(name, want, A, B, C, alpha, beta, stream):
     K2, N = B.shape
     if K != K2:
         raise ValueError(f"inner dimensions differ: {K} vs {K2}")
-    if C is None and beta != 0.0:
-        raise ValueError("beta != 0 needs C")
-    ldc = max(N, 1) if C is None else _row_major_ld(_out(C, M, N, A), "C")
-    ldq, lds, tb = B._ldq, B._lds, 1 if B.transposed else 0
-    _ints(M, N, K, lda, ldq, lds, ldc)
+    if C is None:
+        if beta != 0.0:
+            raise ValueError("beta != 0 needs C")
+        ldc = N if N > 0 else 1
+    else:
+        ldc = _rows(_out(C, M, N, A), "C")[0]
+    _ints(M, N, K, lda, B._ldq, B._lds, ldc)
+    return _launched(_run_gemm_mx, device, stream, name, A, ta, lda, B, M, N, K, C, ldc, alpha, beta)
+
+
+def _run_gemm_mx(name, A, ta, lda, B, M, N, K, C, ldc, alpha, beta, handle):
     lib = _lib or load()
-
-    def run(handle):
-        out = torch.empty((M, N), dtype=torch.float32, device=device) if C is None else C
-        work, size = None, 0
-        if M > 64:  # fewer rows never use a workspace
-            size = lib.regtile_gemm_mx_workspace(ta, tb, M, N, K, lda, ldc)
-            if size > 0:
-                work = torch.empty(size, dtype=torch.uint8, device=device)
-        _check(getattr(lib, name)(B.format, ta, tb, M, N, K, alpha, A.data_ptr(), lda, B.codes.data_ptr(), ldq,
-                                  B.scales.data_ptr(), lds, beta, out.data_ptr(), ldc,
-                                  0 if work is None else work.data_ptr(), size, handle))
-        return out
-
-    return _launched(run, device, stream)
+    if C is None:
+        C = A.new_empty((M, N), dtype=_torch.float32)
+    tb = 1 if B.transposed else 0
+    work, at, size = None, None, 0
+    if M > 64:  # fewer rows never use a workspace
+        size = lib.regtile_gemm_mx_workspace(ta, tb, M, N, K, lda, ldc)
+        if size > 0:
+            work = A.new_empty(size, dtype=_torch.uint8)  # stays until the launch is queued
+            at = work.data_ptr()
+    _check(getattr(lib, name)(B.format, ta, tb, M, N, K, alpha, A.data_ptr(), lda, B.codes.data_ptr(), B._ldq,
+                              B.scales.data_ptr(), B._lds, beta, C.data_ptr(), ldc, at, size, handle))
+    return C
 
 
 def gemm_bf16_mx(A, B, C=None, alpha=1.0, beta=0.0, stream=None):
     """C = alpha*A@B + beta*C; bf16 A (M x K), row-major or a transposed view, times a block-scaled B
     (an MXMatrix, K x N; ``W.t()`` for weights stored N x K), fp32 C row-major; returns C (allocated
     when None)."""
-    import torch
-
-    return _gemm_mx("regtile_gemm_bf16_mx", torch.bfloat16, A, B, C, alpha, beta, stream)
+    return _gemm_mx("regtile_gemm_bf16_mx", (_torch or _import_torch()).bfloat16, A, B, C, alpha, beta, stream)
 
 
 def gemm_f16_mx(A, B, C=None, alpha=1.0, beta=0.0, stream=None):
     """As gemm_bf16_mx with a float16 A; B's values are taken in float16."""
-    import torch
-
-    return _gemm_mx("regtile_gemm_f16_mx", torch.float16, A, B, C, alpha, beta, stream)
+    return _gemm_mx("regtile_gemm_f16_mx", (_torch or _import_torch()).float16, A, B, C, alpha, beta, stream)

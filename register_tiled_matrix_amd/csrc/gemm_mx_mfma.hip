@@ -1,16 +1,23 @@
 // gemm_mx_mfma.hip -- C = alpha op(A) op(B) + beta C for a bf16 / fp16 A and a block-scaled (MX) B,
 // any storage order, any size and any alignment.
 //
-// A workgroup of 4 waves owns a T x T tile of C (T = 128, or 64 for few tiles) and walks K in slabs
-// of 64. Both operands go through registers: A as 16-byte chunks, B as 16 codes of one group with
-// their scale byte, expanded to the 16-bit type (mx_common.h; exact) before they are written to LDS.
-// The next slab is loaded while the current one is multiplied, on two LDS stages with one barrier
-// per slab.
+// Four waves own a T x T tile of C and walk K in slabs of 64. Both operands go through registers: A as
+// 16-byte chunks, B as 16 codes of one group with their scale byte, expanded to the 16-bit type
+// (mx_common.h; exact) before they are written to LDS. 64-wide tiles load two slabs ahead of the
+// one that is multiplied (a load takes longer than a slab), into two sets of registers; 128-wide ones,
+// whose slabs take longer, one. Slabs pass through two LDS stages with one barrier per slab that
+// waits for LDS only.
+//
+// Few tiles leave most of the chip idle and their slabs are a chain of memory latencies. There KS = 4
+// groups of four waves share a 64 x 64 tile, each with its own slabs (every fourth) and its own
+// stages, and the four sums are added through LDS in order.
 //
 // LDS holds each operand in its own storage order, in the layouts of tile_addressing.h: K-contiguous
 // slabs (rows of 64 k) feed the 32x32x16 MFMAs with 16-byte reads, M/N-contiguous ones (64 rows of T
 // elements) with transposing reads. Groups run along the stored rows and tiles and slabs start at
 // multiples of 32, so no run of 16 codes has two scales.
+#include <type_traits>
+
 #include "mfma_common.h"
 #include "mx_common.h"
 #include "regtile_internal.h"
@@ -21,7 +28,7 @@ namespace {
 using namespace mfma;
 
 constexpr int MXT_BK = 64;   // slab depth
-constexpr int MXT_NT = 256;  // threads: 2 x 2 waves
+constexpr int MXT_NT = 256;  // threads of a group: 2 x 2 waves
 
 // slot (16-byte units) of chunk c of slab row r
 template <bool MAJOR_K, int T>
@@ -33,8 +40,8 @@ __device__ __forceinline__ int slab_slot(int r, int c) {
 
 // The stored operand as rows x cols: K-contiguous, rows are the tile's M (or N) index and columns k;
 // otherwise rows are k and columns the tile's.
-template <int T, bool FP4, bool F16, bool TA, bool TB>
-__global__ __launch_bounds__(MXT_NT) void mx_mfma_kernel(int M, int N, int K, float alpha,
+template <int T, int KS, bool FP4, bool F16, bool TA, bool TB>
+__global__ __launch_bounds__(MXT_NT *KS, KS == 1 ? 2 : 4) void mx_mfma_kernel(int M, int N, int K, float alpha,
                                                          const uint16_t *__restrict__ A, int64_t lda,
                                                          const uint8_t *__restrict__ Q, int64_t ldq,
                                                          const uint8_t *__restrict__ S, int64_t lds, float beta,
@@ -46,9 +53,13 @@ __global__ __launch_bounds__(MXT_NT) void mx_mfma_kernel(int M, int N, int K, fl
     constexpr int JA = SLOTS / MXT_NT;         // chunks of A per thread and slab
     constexpr int JB = SLOTS / 2 / MXT_NT;     // half groups (16 codes) of B per thread and slab
     constexpr int HB = FP4 ? 8 : 16;           // bytes of a half group
-    __shared__ uint4 smem[2][2][SLOTS];
+    constexpr int PSTRIDE = T + 4;             // row stride (floats) of a group's sums in LDS
+    constexpr int STAGES = KS * 2 * 2 * SLOTS, SUMS = KS * T * PSTRIDE / 4;
+    __shared__ uint4 lds_all[KS > 1 && SUMS > STAGES ? SUMS : STAGES];
+    const int group = KS == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / MXT_NT);
+    uint4(*const smem)[2][SLOTS] = reinterpret_cast<uint4(*)[2][SLOTS]>(lds_all + group * (4 * SLOTS));
 
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x % MXT_NT;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int wm = wave >> 1, wn = wave & 1;
     int tm, tn;
@@ -64,64 +75,126 @@ __global__ __launch_bounds__(MXT_NT) void mx_mfma_kernel(int M, int N, int K, fl
         c = p % per_row * run;
     };
 
-    uint4 ra[JA];
-    uint32_t rq[JB][HB / 4], rs[JB];
-    auto load = [&](int64_t slab) {
+    // Runs that pass their row's end (in K-contiguous storage only the last slab has them, in
+    // M/N-contiguous storage every slab of the last tiles) are loaded as the whole run that ends
+    // there and moved down when they are written to LDS, so that every load has the same time to
+    // land; rows shorter than a run are read by element.
+        constexpr int PF = T == 128 ? 1 : 2;  // register sets: slabs loaded ahead
+    uint32_t ra[PF][JA][4], rq[PF][JB][HB / 4], rs[PF][JB];
+    const int a_cols = A_K ? K : M, b_cols = B_K ? K : N;
+    const int b_bytes = FP4 ? (b_cols + 1) / 2 : b_cols;
+    auto load_edge = [&](int64_t slab, int set) {
         const int64_t k0 = slab * MXT_BK;
 #pragma unroll
         for (int j = 0; j < JA; ++j) {
             int r, c;
             place(A_K, 8, j, r, c);
             const int64_t row = (A_K ? m0 : k0) + r, col = (A_K ? k0 : m0) + c;
-            const int64_t left = (A_K ? K : M) - col;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (row < (A_K ? M : K) && left > 0) {
-                const uint16_t *p = A + row * lda + col;
-                if (left >= 8) {
-                    __builtin_memcpy(&v, p, 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ra[set][j][i] = 0;
+            if (row < (A_K ? M : K) && col < a_cols) {
+                const uint16_t *p = A + row * lda;
+                if (a_cols >= 8) {
+                    __builtin_memcpy(ra[set][j], p + min(col, (int64_t)a_cols - 8), 16);
                 } else {
-                    uint32_t d[4] = {0, 0, 0, 0};
 #pragma unroll
                     for (int i = 0; i < 7; ++i)
-                        if (i < left) d[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-                    v = make_uint4(d[0], d[1], d[2], d[3]);
+                        if (i < a_cols) ra[set][j][i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
                 }
             }
-            ra[j] = v;
         }
 #pragma unroll
         for (int j = 0; j < JB; ++j) {
             int r, c;
             place(B_K, 16, j, r, c);
             const int64_t row = (B_K ? n0 : k0) + r, col = (B_K ? k0 : n0) + c;
-            const int64_t left = (B_K ? K : N) - col;
 #pragma unroll
-            for (int i = 0; i < HB / 4; ++i) rq[j][i] = 0;
-            rs[j] = 0;
-            if (row < (B_K ? N : K) && left > 0) {
-                const uint8_t *p = Q + row * ldq + (FP4 ? col / 2 : col);
-                rs[j] = S[row * lds + col / mx::GROUP];
-                if (left >= 16)
-                    mx::load_bytes<HB>(p, rq[j]);
+            for (int i = 0; i < HB / 4; ++i) rq[set][j][i] = 0;
+            rs[set][j] = 0;
+            if (row < (B_K ? N : K) && col < b_cols) {
+                const uint8_t *p = Q + row * ldq;
+                rs[set][j] = S[row * lds + col / mx::GROUP];
+                if (b_bytes >= HB)
+                    mx::load_bytes<HB>(p + min(FP4 ? col / 2 : col, (int64_t)b_bytes - HB), rq[set][j]);
                 else
-                    mx::load_codes_tail<FP4, HB>(p, (int)left, rq[j]);
+                    mx::load_codes_tail<FP4, HB>(p, b_cols, rq[set][j]);
             }
         }
     };
-    auto write = [&](int st) {
+    // Slabs that end before K need no checks: rows (columns) past M or N are loaded from the last
+    // ones and feed outputs that are not stored.
+    const uint16_t *pa[JA];
+    const uint8_t *pq[JB], *ps[JB];
+    const bool a_runs = a_cols >= 8, b_runs = b_bytes >= HB;  // rows as long as a run
+#pragma unroll
+    for (int j = 0; j < JA; ++j) {
+        int r, c;
+        place(A_K, 8, j, r, c);
+        pa[j] = A + (A_K ? min(m0 + r, (int64_t)M - 1) * lda + c : r * lda + min(m0 + c, (int64_t)M - 8));
+    }
+#pragma unroll
+    for (int j = 0; j < JB; ++j) {
+        int r, c;
+        place(B_K, 16, j, r, c);
+        const int64_t row = B_K ? min(n0 + r, (int64_t)N - 1) : r, col = B_K ? c : n0 + c;
+        pq[j] = Q + row * ldq + (B_K ? (FP4 ? col / 2 : col) : min(FP4 ? col / 2 : col, (int64_t)b_bytes - HB));
+        ps[j] = S + row * lds + (B_K ? col / mx::GROUP : min(col / mx::GROUP, ((int64_t)N - 1) / mx::GROUP));
+    }
+    auto load = [&](int64_t slab, int set) {
+        if (!a_runs || !b_runs || (slab + 1) * MXT_BK > K) {
+            load_edge(slab, set);
+            return;
+        }
+        const int64_t k0 = slab * MXT_BK, ao = A_K ? k0 : k0 * lda;
+        const int64_t qo = B_K ? (FP4 ? k0 / 2 : k0) : k0 * ldq, so = B_K ? k0 / mx::GROUP : k0 * lds;
+#pragma unroll
+        for (int j = 0; j < JA; ++j) __builtin_memcpy(ra[set][j], pa[j] + ao, 16);
+#pragma unroll
+        for (int j = 0; j < JB; ++j) {
+            mx::load_bytes<HB>(pq[j] + qo, rq[set][j]);
+            rs[set][j] = ps[j][so];
+        }
+    };
+    auto write = [&](int64_t slab, int st, int set) {
+        const int64_t k0 = slab * MXT_BK;
+        // does this slab of this tile hold runs that pass the end of their rows?
+        if (a_runs && (A_K ? k0 + MXT_BK > K : m0 + T > M)) {
+#pragma unroll
+            for (int j = 0; j < JA; ++j) {
+                int r, c;
+                place(A_K, 8, j, r, c);
+                const int64_t early = (A_K ? k0 : m0) + c - (a_cols - 8);  // elements
+                if (early > 0 && early < 8) mx::move_down(ra[set][j], 2 * (int)early);
+            }
+        }
+        if (b_runs && (B_K ? k0 + MXT_BK > K : n0 + T > N)) {
+#pragma unroll
+            for (int j = 0; j < JB; ++j) {
+                int r, c;
+                place(B_K, 16, j, r, c);
+                const int64_t col = (B_K ? k0 : n0) + c, early = (FP4 ? col / 2 : col) - (b_bytes - HB);  // bytes
+                if (early >= 0 && early < HB) {
+                    mx::move_down(rq[set][j], (int)early);
+                    const int at = HB - 1 - (int)early;  // the half byte behind an odd row
+#pragma unroll
+                    for (int i = 0; i < HB / 4; ++i)
+                        if (FP4 && (b_cols & 1) && at / 4 == i) rq[set][j][i] &= ~(0xF0u << (8 * (at % 4)));
+                }
+            }
+        }
 #pragma unroll
         for (int j = 0; j < JA; ++j) {
             int r, c;
             place(A_K, 8, j, r, c);
-            smem[st][0][slab_slot<A_K, T>(r, c / 8)] = ra[j];
+            smem[st][0][slab_slot<A_K, T>(r, c / 8)] = make_uint4(ra[set][j][0], ra[set][j][1], ra[set][j][2], ra[set][j][3]);
         }
 #pragma unroll
         for (int j = 0; j < JB; ++j) {
             int r, c;
             place(B_K, 16, j, r, c);
-            const float s = mx::scale_value<FP4>(rs[j]);
-            smem[st][1][slab_slot<B_K, T>(r, c / 8)] = mx::expand8<FP4, F16>(rq[j], 0, s);
-            smem[st][1][slab_slot<B_K, T>(r, c / 8 + 1)] = mx::expand8<FP4, F16>(rq[j], 1, s);
+            const float s = mx::scale_value<FP4>(rs[set][j]);
+            smem[st][1][slab_slot<B_K, T>(r, c / 8)] = mx::expand8<FP4, F16>(rq[set][j], 0, s);
+            smem[st][1][slab_slot<B_K, T>(r, c / 8 + 1)] = mx::expand8<FP4, F16>(rq[set][j], 1, s);
         }
     };
 
@@ -151,81 +224,125 @@ __global__ __launch_bounds__(MXT_NT) void mx_mfma_kernel(int M, int N, int K, fl
 #pragma unroll
             for (int v = 0; v < F::NACC; ++v) acc[i][j][v] = 0.0f;
 
-    load(0);
-    write(0);
-    __syncthreads();
-    for (int64_t s = 0; s < nslabs; ++s) {
-        const int st = (int)(s & 1);
-        if (s + 1 < nslabs) load(s + 1);
+    // This group's slabs are group, group + KS, ...; every group walks `steps` of them, those past
+    // the end (past K) all zeros. Step i uses stage i % 2 (and, with two sets, registers i % 2).
+    const int64_t steps = (nslabs + KS - 1) / KS;
+    auto slab_of = [&](int64_t i) { return group + i * KS; };
+    auto step = [&](int64_t i, auto parity) {
+        constexpr int P = decltype(parity)::value;
+        if (i + PF < steps) load(slab_of(i + PF), PF == 2 ? P : 0);
 #pragma unroll
         for (int kk = 0; kk < MXT_BK / F::KSTEP; ++kk) {
             bf16x8 fa[MI], fb[NI];
 #pragma unroll
-            for (int i = 0; i < MI; ++i)
-                fa[i] = frag(std::integral_constant<bool, A_K>{}, smem[st][0], wm * (T / 2) + 32 * i, kk);
+            for (int a = 0; a < MI; ++a)
+                fa[a] = frag(std::integral_constant<bool, A_K>{}, smem[P][0], wm * (T / 2) + 32 * a, kk);
 #pragma unroll
-            for (int j = 0; j < NI; ++j)
-                fb[j] = frag(std::integral_constant<bool, B_K>{}, smem[st][1], wn * (T / 2) + 32 * j, kk);
+            for (int b = 0; b < NI; ++b)
+                fb[b] = frag(std::integral_constant<bool, B_K>{}, smem[P][1], wn * (T / 2) + 32 * b, kk);
 #pragma unroll
-            for (int i = 0; i < MI; ++i)
+            for (int a = 0; a < MI; ++a)
 #pragma unroll
-                for (int j = 0; j < NI; ++j) acc[i][j] = F::mfma(fa[i], fb[j], acc[i][j]);
+                for (int b = 0; b < NI; ++b) acc[a][b] = F::mfma(fa[a], fb[b], acc[a][b]);
         }
-        if (s + 1 < nslabs) write(st ^ 1);
-        __syncthreads();
+        if (i + 1 < steps) write(slab_of(i + 1), P ^ 1, PF == 2 ? P ^ 1 : 0);
+        wait_lgkmcnt0();
+        lds_barrier();  // the next stage is written, this one has been read
+    };
+    load(slab_of(0), 0);
+    if (PF == 2 && steps > 1) load(slab_of(1), PF - 1);
+    write(slab_of(0), 0, 0);
+    wait_lgkmcnt0();
+    lds_barrier();
+    for (int64_t i = 0; i < steps; i += 2) {
+        step(i, std::integral_constant<int, 0>{});
+        if (i + 1 < steps) step(i + 1, std::integral_constant<int, 1>{});
     }
 
     const int rl = F::row_lane(lane);
+    if constexpr (KS == 1) {
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < NI; ++j) {
-            const int64_t col = n0 + wn * (T / 2) + 32 * j + (lane & 31);
+            for (int j = 0; j < NI; ++j) {
+                const int64_t col = n0 + wn * (T / 2) + 32 * j + (lane & 31);
 #pragma unroll
-            for (int v = 0; v < F::NACC; ++v) {
-                const int64_t row = m0 + wm * (T / 2) + 32 * i + rl + F::row_acc(v);
-                if (row < M && col < N) {
-                    float *c = C + row * ldc + col;
-                    *c = epilogue_value(acc[i][j][v], alpha, beta, c);
+                for (int v = 0; v < F::NACC; ++v) {
+                    const int64_t row = m0 + wm * (T / 2) + 32 * i + rl + F::row_acc(v);
+                    if (row < M && col < N) {
+                        float *c = C + row * ldc + col;
+                        *c = epilogue_value(acc[i][j][v], alpha, beta, c);
+                    }
                 }
             }
+    } else {
+        // (the last step's barrier has freed the stages)
+        float *const sums = reinterpret_cast<float *>(lds_all);
+        float *const mine = sums + group * (T * PSTRIDE);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NI; ++j)
+#pragma unroll
+                for (int v = 0; v < F::NACC; ++v)
+                    mine[(wm * (T / 2) + 32 * i + rl + F::row_acc(v)) * PSTRIDE + wn * (T / 2) + 32 * j + (lane & 31)] =
+                        acc[i][j][v];
+        __syncthreads();
+        for (int e = threadIdx.x; e < T * T; e += MXT_NT * KS) {
+            const int r = e / T, c = e % T;
+            if (m0 + r < M && n0 + c < N) {
+                float v = sums[r * PSTRIDE + c];
+#pragma unroll
+                for (int g = 1; g < KS; ++g) v += sums[g * (T * PSTRIDE) + r * PSTRIDE + c];
+                float *cp = C + (m0 + r) * ldc + n0 + c;
+                *cp = epilogue_value(v, alpha, beta, cp);
+            }
         }
+    }
 }
 
-template <int T, bool FP4, bool F16, bool TA, bool TB>
+template <int T, int KS, bool FP4, bool F16, bool TA, bool TB>
 hipError_t launch_mxt(const MxProblem &p, hipStream_t s) {
     const int tiles_m = (int)(((int64_t)p.M + T - 1) / T), tiles_n = (int)(((int64_t)p.N + T - 1) / T);
-    note_launch(reinterpret_cast<const void *>(&mx_mfma_kernel<T, FP4, F16, TA, TB>), MXT_NT);
-    hipLaunchKernelGGL((mx_mfma_kernel<T, FP4, F16, TA, TB>), dim3((unsigned)((int64_t)tiles_m * tiles_n)), dim3(MXT_NT),
-                       0, s, p.M, p.N, p.K, p.alpha, (const uint16_t *)p.A, p.lda, p.Q, p.ldq, p.S, p.lds, p.beta, p.C,
-                       p.ldc, tiles_m, tiles_n);
+    note_launch(reinterpret_cast<const void *>(&mx_mfma_kernel<T, KS, FP4, F16, TA, TB>), MXT_NT * KS);
+    hipLaunchKernelGGL((mx_mfma_kernel<T, KS, FP4, F16, TA, TB>), dim3((unsigned)((int64_t)tiles_m * tiles_n)),
+                       dim3(MXT_NT * KS), 0, s, p.M, p.N, p.K, p.alpha, (const uint16_t *)p.A, p.lda, p.Q, p.ldq, p.S,
+                       p.lds, p.beta, p.C, p.ldc, tiles_m, tiles_n);
     return hipGetLastError();
 }
-template <int T, bool FP4, bool F16>
+template <int T, int KS, bool FP4, bool F16>
 hipError_t launch_mxt_order(const MxProblem &p, hipStream_t s) {
-    if (p.ta) return p.tb ? launch_mxt<T, FP4, F16, true, true>(p, s) : launch_mxt<T, FP4, F16, true, false>(p, s);
-    return p.tb ? launch_mxt<T, FP4, F16, false, true>(p, s) : launch_mxt<T, FP4, F16, false, false>(p, s);
+    if (p.ta) return p.tb ? launch_mxt<T, KS, FP4, F16, true, true>(p, s) : launch_mxt<T, KS, FP4, F16, true, false>(p, s);
+    return p.tb ? launch_mxt<T, KS, FP4, F16, false, true>(p, s) : launch_mxt<T, KS, FP4, F16, false, false>(p, s);
 }
-template <int T>
+template <int T, int KS>
 hipError_t launch_mxt_types(const MxProblem &p, hipStream_t s) {
-    if (p.fp4) return p.f16 ? launch_mxt_order<T, true, true>(p, s) : launch_mxt_order<T, true, false>(p, s);
-    return p.f16 ? launch_mxt_order<T, false, true>(p, s) : launch_mxt_order<T, false, false>(p, s);
+    if (p.fp4) return p.f16 ? launch_mxt_order<T, KS, true, true>(p, s) : launch_mxt_order<T, KS, true, false>(p, s);
+    return p.f16 ? launch_mxt_order<T, KS, false, true>(p, s) : launch_mxt_order<T, KS, false, false>(p, s);
 }
 
 }  // namespace
 
 hipError_t launch_mx_mfma(const MxProblem &p, hipStream_t s, const char **name) {
     const int64_t tiles128 = (((int64_t)p.M + 127) / 128) * (((int64_t)p.N + 127) / 128);
-    const bool small = tiles128 < 256;  // fewer than one 128 x 128 tile per CU
+    const int64_t tiles64 = (((int64_t)p.M + 63) / 64) * (((int64_t)p.N + 63) / 64);
+    // 128-wide tiles from one per CU (3001x2003x1001 fp4 nt, 384 of them: 31 us against 37 on 64-wide
+    // ones; 1500x2200x1001 nn, 216: 28 against 26); four groups to a 64-wide tile up to one of those
+    // per CU (1000x777x1500 nn, 208: 13.7 us against 32; 1000x1500x777 nt, 384: 17.9 against 14.8)
+    const int kind = tiles128 >= 256 ? 0 : tiles64 > 256 ? 1 : 2;
 #define REGTILE_MX_NAMES(elt, fmt, t) \
     {{elt "_" fmt "_mfma_" t "_nn", elt "_" fmt "_mfma_" t "_nt"}, {elt "_" fmt "_mfma_" t "_tn", elt "_" fmt "_mfma_" t "_tt"}}
-#define REGTILE_MX_SIZES(elt, fmt) {REGTILE_MX_NAMES(elt, fmt, "128x128x64"), REGTILE_MX_NAMES(elt, fmt, "64x64x64")}
-    static const char *const names[2][2][2][2][2] = {{REGTILE_MX_SIZES("bf16", "int8"), REGTILE_MX_SIZES("bf16", "fp4")},
+#define REGTILE_MX_SIZES(elt, fmt)                                                                              \
+    {REGTILE_MX_NAMES(elt, fmt, "128x128x64"), REGTILE_MX_NAMES(elt, fmt, "64x64x64"),                           \
+     REGTILE_MX_NAMES(elt, fmt, "64x64x64_k4")}
+    static const char *const names[2][2][3][2][2] = {{REGTILE_MX_SIZES("bf16", "int8"), REGTILE_MX_SIZES("bf16", "fp4")},
                                                      {REGTILE_MX_SIZES("f16", "int8"), REGTILE_MX_SIZES("f16", "fp4")}};
 #undef REGTILE_MX_SIZES
 #undef REGTILE_MX_NAMES
-    *name = names[p.f16][p.fp4][small][p.ta][p.tb];
-    return small ? launch_mxt_types<64>(p, s) : launch_mxt_types<128>(p, s);
+    *name = names[p.f16][p.fp4][kind][p.ta][p.tb];
+    return kind == 0   ? launch_mxt_types<128, 1>(p, s)
+           : kind == 1 ? launch_mxt_types<64, 1>(p, s)
+                       : launch_mxt_types<64, 4>(p, s);
 }
 
 }  // namespace regtile

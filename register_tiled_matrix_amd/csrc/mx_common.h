@@ -120,5 +120,28 @@ __device__ __forceinline__ void load_codes_tail(const uint8_t *p, int count, uin
     }
 }
 
+// A short run at a row's end without byte loads: the NB bytes that end where the row ends are loaded
+// instead (the row must have that many), and moved down by the bytes they start too early; zeros
+// come in behind.
+template <int N>
+__device__ __forceinline__ void move_down(uint32_t (&d)[N], int bytes) {
+    static_assert(N == 2 || N == 4, "8 or 16 bytes");
+    const int s = 8 * bytes;
+    uint64_t lo = d[0] | (uint64_t)d[1] << 32, hi = N == 4 ? d[N - 2] | (uint64_t)d[N - 1] << 32 : 0;
+    if (s >= 64) {
+        lo = hi >> (s - 64);
+        hi = 0;
+    } else if (s > 0) {
+        lo = lo >> s | hi << (64 - s);
+        hi >>= s;
+    }
+    d[0] = (uint32_t)lo;
+    d[1] = (uint32_t)(lo >> 32);
+    if constexpr (N == 4) {
+        d[2] = (uint32_t)hi;
+        d[3] = (uint32_t)(hi >> 32);
+    }
+}
+
 }  // namespace mx
 }  // namespace regtile
