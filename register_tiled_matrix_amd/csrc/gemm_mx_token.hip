@@ -373,50 +373,52 @@ hipError_t launch_token(const MxProblem &p, hipStream_t s) {
     return hipGetLastError();
 }
 
-#ifndef TK_MAX
-#define TK_MAX 4
-#endif
-#ifndef TK_CFG4
-#define TK_CFG4 4, 1, 8, 1
-#define TK_CFG2 4, 1, 8, 1
-#define TK_CFG1 2, 1, 8, 4
-#define TK_CFGM 2, 2, 4, 2
-#endif
-#ifndef BT_F1
-#define BT_F1 2, 1, 8, 3
-#define BT_I1 2, 1, 4, 4
-#define BT_F2 2, 2, 4, 3
-#define BT_I2 2, 2, 4, 3
-#define BT_F3 2, 3, 4, 2
-#define BT_I3 2, 3, 4, 2
-#define BT_F4 2, 4, 4, 2
-#define BT_I4 1, 4, 4, 2
-#endif
-
+// Shapes <NF, MC, NW, U or D>, times in us at N x K = 8192 x 8192 unless stated. Register kernel: more
+// rows of B a wave reuse A's fragments (the loads of A bound it: at one token fp4 13.1, 10.6, 10.0 with NF
+// = 1, 2, 4), fewer fill more of the chip (2048 x 2048: 3.3, 3.1, 3.4), so NF = 4 waits for N = 8192;
+// int8 codes take twice the registers and stay at NF = 2 (17.3; NF = 4: 19.9). Eight waves: four lose
+// 0-12%, sixteen 10-40%.
 template <bool FP4, bool F16>
 hipError_t launch_token_rows(const MxProblem &p, hipStream_t s) {
-    if (p.M <= 4) return launch_token<FP4, F16, 4, TK_CFG4>(p, s);
-    if (p.M <= 8) return launch_token<FP4, F16, 2, TK_CFG2>(p, s);
-    if (p.M <= 16) return launch_token<FP4, F16, 1, TK_CFG1>(p, s);
-    return launch_token<FP4, F16, 1, TK_CFGM>(p, s);
+    if (p.M <= 4) {
+        if constexpr (FP4) {
+            if (p.N >= 8192) return launch_token<FP4, F16, 4, 4, 1, 8, 1>(p, s);
+            return launch_token<FP4, F16, 4, 2, 1, 8, 2>(p, s);
+        } else {
+            return launch_token<FP4, F16, 4, 2, 1, 8, 1>(p, s);
+        }
+    }
+    if (p.M <= 8) return launch_token<FP4, F16, 2, 2, 1, 8, 2>(p, s);
+    if (p.M <= 16) return launch_token<FP4, F16, 1, 2, 1, 8, 4>(p, s);
+    return launch_token<FP4, F16, 1, 2, 2, 4, 2>(p, s);
 }
+// LDS kernel: 16 NF rows of B a workgroup. One fragment while that gives at most one workgroup per CU
+// (N <= 4096; 16 tokens at 4096 x 4096 fp4: 5.6 against 6.7 with two), then two, which read A half as
+// often (14.5 against 19.0 at 8192 x 8192). LDS is split into as many waves as leave two chunks each
+// (three where that is no fewer waves than eight): more waves hide more latency than deeper rings (32
+// tokens fp4 7 waves x 2 chunks 18.7, 5 x 3 19.3, 3 x 5 25.2).
 template <bool F16>
 hipError_t launch_batch_rows(const MxProblem &p, hipStream_t s) {
-    if (p.M <= 16) return p.fp4 ? launch_batch<true, F16, BT_F1>(p, s) : launch_batch<false, F16, BT_I1>(p, s);
-    if (p.M <= 32) return p.fp4 ? launch_batch<true, F16, BT_F2>(p, s) : launch_batch<false, F16, BT_I2>(p, s);
-    if (p.M <= 48) return p.fp4 ? launch_batch<true, F16, BT_F3>(p, s) : launch_batch<false, F16, BT_I3>(p, s);
-    return p.fp4 ? launch_batch<true, F16, BT_F4>(p, s) : launch_batch<false, F16, BT_I4>(p, s);
+    if (p.N <= 4096) {
+        if (p.M <= 16) return p.fp4 ? launch_batch<true, F16, 1, 1, 12, 2>(p, s) : launch_batch<false, F16, 1, 1, 12, 2>(p, s);
+        if (p.M <= 32) return p.fp4 ? launch_batch<true, F16, 1, 2, 8, 2>(p, s) : launch_batch<false, F16, 1, 2, 7, 2>(p, s);
+        if (p.M <= 48) return p.fp4 ? launch_batch<true, F16, 1, 3, 6, 2>(p, s) : launch_batch<false, F16, 1, 3, 5, 2>(p, s);
+        return p.fp4 ? launch_batch<true, F16, 1, 4, 4, 2>(p, s) : launch_batch<false, F16, 1, 4, 4, 2>(p, s);
+    }
+    if (p.M <= 16) return p.fp4 ? launch_batch<true, F16, 2, 1, 8, 3>(p, s) : launch_batch<false, F16, 2, 1, 9, 2>(p, s);
+    if (p.M <= 32) return p.fp4 ? launch_batch<true, F16, 2, 2, 7, 2>(p, s) : launch_batch<false, F16, 2, 2, 6, 2>(p, s);
+    if (p.M <= 48) return p.fp4 ? launch_batch<true, F16, 2, 3, 5, 2>(p, s) : launch_batch<false, F16, 2, 3, 4, 2>(p, s);
+    return p.fp4 ? launch_batch<true, F16, 2, 4, 4, 2>(p, s) : launch_batch<false, F16, 2, 4, 3, 2>(p, s);
 }
 
 }  // namespace
 
 // Takes (and launches, status in *err) products of at most 64 rows of A, row-major, with B stored
-// N x K: the register kernel up to 4 rows (8 rows: fragments of two parts) and, up to 32, where rows are
-// not aligned for the LDS kernel, which takes the others. Returns false, launching nothing, for any
-// other problem.
+// N x K: the register kernel up to 8 rows and, up to 32, where rows are not aligned for the LDS
+// kernel, which takes the others. Returns false, launching nothing, for any other problem.
 bool launch_mx_token(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err) {
     if (p.ta || !p.tb) return false;
-    const bool lds = p.M > TK_MAX && p.M <= 64 && p.lda % 8 == 0 && aligned16(p.A) && p.ldq % 16 == 0 && aligned16(p.Q) &&
+    const bool lds = p.M > 8 && p.M <= 64 && p.lda % 8 == 0 && aligned16(p.A) && p.ldq % 16 == 0 && aligned16(p.Q) &&
                      p.lds % 4 == 0 && (reinterpret_cast<uintptr_t>(p.S) & 3u) == 0;
     if (!lds && p.M > 32) return false;
 #define REGTILE_TOKEN_SET(elt, fmt)                                                                            \

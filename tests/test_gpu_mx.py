@@ -192,6 +192,17 @@ def test_product_strides_alpha_beta(fmt, order, M, N, K):
     product(rng, fmt, "f16", order, M, N, K, alpha=-0.75, beta=1.0, pad=8, c_pad=4, label="padded")
 
 
+@pytest.mark.parametrize("M", [1, 3, 5, 8, 9, 16, 17, 32, 33, 48, 49, 64])
+@pytest.mark.parametrize("N", [40, 4112, 8200])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_product_tokens(fmt, N, M):
+    """Every shape of the kernels for a few rows: K of whole chunks and with a short one, fewer
+    chunks than waves, unaligned rows."""
+    rng = np.random.default_rng(M * N)
+    for K, pad in ((1536, 0), (2080, 16), (77, 0), (1100, 1)):
+        product(rng, fmt, "bf16" if K != 2080 else "f16", "nt", M, N, K, beta=0.5 if pad else 0.0, pad=pad, c_pad=pad % 2, label="tokens")
+
+
 # the DMA kernels: one slab, slabs that end inside a group of four, tiles that end anywhere, 128 and
 # 256 wide tiles
 @pytest.mark.parametrize("M,N,K", [(72, 96, 32), (136, 160, 64), (200, 288, 96), (128, 128, 640), (264, 512, 224), (1000, 1504, 800),
