@@ -6,9 +6,10 @@
 // the next k step read and DMA issued between the MFMAs of this one, one barrier a slab. Slab t's A
 // part sits in half (2 t) % 5 and its B part in half (2 t + 1) % 5.
 //
-// B: a thread owns T / 128 groups of 32 codes of each slab. Codes and scale bytes are loaded two slabs
-// ahead, and while slab s is multiplied those of slab s + 1 are expanded to the 16-bit type (exact;
-// mx_common.h) and written to their half, a group in a k step, between MFMAs. Expanding costs 0.5
+// B: a thread owns T / 128 groups of 32 codes of each slab. Codes and scale bytes are loaded ahead (by
+// one slab's time, or two on 128-wide tiles, whose slabs are short), and while slab s is multiplied those
+// of slab s + 1 are expanded to the 16-bit type (exact; mx_common.h) and written to their half, a
+// group in a k step, between MFMAs. Expanding costs 0.5
 // (fp4) or 2.5 (int8) vector instructions a value and happens once a workgroup; keeping the codes in
 // LDS and expanding fragments would repeat it in the two waves that share each column.
 //
@@ -53,6 +54,7 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
     constexpr int KSTEPS = MXD_BK / F::KSTEP, NMFMA = MI * NI;
     constexpr int NREAD = MI * (A_MN ? 2 : 1) + NI * (B_MN ? 2 : 1);
     constexpr int PER_WIN = JA / NWIN;
+    constexpr int PF = T == 128 ? 2 : 1;       // register sets for B's groups
     static_assert(KSTEPS == 4 && JA % NWIN == 0 && NWIN + STAGGER <= 2, "windows at the last and the first k step");
     static_assert(NG == 1 || NG == 2, "groups go in k steps 1 and 2");
     __shared__ uint4 smem[5 * HALF];
@@ -106,8 +108,8 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
         qbase[i] = Q + row * ldq + g * GB;
         sbase[i] = S + row * lds + g;
     }
-    uint32_t q[NG][GB / 4], sc[NG];
-    auto load_group = [&](int i, int s) {
+    uint32_t q[PF][NG][GB / 4], sc[PF][NG];
+    auto load_group = [&](int i, int s, int set) {
         const int slab = first_slab + s;
         int64_t qo, so;
         if constexpr (B_MN) {
@@ -118,21 +120,21 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
             so = min(2 * slab + b_g[i], last_g);
             qo = so * GB;
         }
-        mx::load_bytes<GB>(qbase[i] + qo, q[i]);
-        sc[i] = sbase[i][so];
+        mx::load_bytes<GB>(qbase[i] + qo, q[set][i]);
+        sc[set][i] = sbase[i][so];
     };
     auto b_slot = [](int r, int c) {
         if constexpr (!B_MN) return r * KCH + (c ^ slab_key<KCH, MF>(r));
         const int low = T == 256 ? ((r & 1) << 1) | ((c >> 4) & 1) : r & 3;
         return r * MCH + (c ^ (4 * (r & 3)) ^ low);
     };
-    auto write_group = [&](int i, int s_, int half) {
+    auto write_group = [&](int i, int s_, int half, int set) {
         const int slab = first_slab + s_;
         const bool past = B_MN ? slab * MXD_BK + b_row[i] >= K : 2 * slab + b_g[i] > last_g;
-        const float s = mx::scale_value<FP4>(past ? 0u : sc[i]);
+        const float s = mx::scale_value<FP4>(past ? 0u : sc[set][i]);
         uint4 *d = smem + half * HALF;
 #pragma unroll
-        for (int t = 0; t < 4; ++t) d[b_slot(b_row[i], 4 * b_g[i] + t)] = mx::expand8<FP4, F16>(q[i], t, s);
+        for (int t = 0; t < 4; ++t) d[b_slot(b_row[i], 4 * b_g[i] + t)] = mx::expand8<FP4, F16>(q[set][i], t, s);
     };
 
     // ---- fragments ----
@@ -215,24 +217,30 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
     auto loop = [&](auto shift_tag) {
         constexpr int SH = decltype(shift_tag)::value;
 #pragma unroll
-        for (int i = 0; i < NG; ++i) load_group(i, 0);
+        for (int i = 0; i < NG; ++i) load_group(i, 0, 0);
 #pragma unroll
         for (int d = 0; d < JA; ++d) dma_a(d, 0, 0);
+        if (PF == 2) {
+#pragma unroll
+            for (int i = 0; i < NG; ++i) load_group(i, 1, PF - 1);
+        }
 #pragma unroll
         for (int d = 0; d < JA; ++d) dma_a(d, 1, 2);
 #pragma unroll
-        for (int i = 0; i < NG; ++i) write_group(i, 0, 1);
+        for (int i = 0; i < NG; ++i) write_group(i, 0, 1, 0);
 #pragma unroll
-        for (int i = 0; i < NG; ++i) load_group(i, 1);
+        for (int i = 0; i < NG; ++i) load_group(i, PF, 0);
         if (SH == 0) window(0, 2, 4);
         __builtin_amdgcn_sched_barrier(0);
-        // A of slab 0 has landed: only A of slab 1, B's loads and the window are younger
-        wait_vmcnt<JA + NG * LG + (SH == 0 ? PER_WIN : 0)>();
+        // A of slab 0 has landed: only A of slab 1, B's loads after it and the window are younger
+        wait_vmcnt<JA + PF * NG * LG + (SH == 0 ? PER_WIN : 0)>();
         wait_lgkmcnt0();
         lds_barrier();
         read_frags(0, 1, 0, 0);
         int ha = 0;
-        for (int s = 0; s < nslabs; ++s) {
+        // slab s; set: the registers of slab s + 1's groups, which then take those of slab s + 1 + PF
+        auto slab = [&](int s, auto set_tag) {
+            constexpr int SET = decltype(set_tag)::value;
             const int hb = wrap5(ha + 1), hna = wrap5(ha + 2), hnb = wrap5(ha + 3), hfa = wrap5(ha + 4);
 #pragma unroll
             for (int kk = 0; kk < KSTEPS; ++kk) {
@@ -249,19 +257,22 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
                     }
                     const int i = kk - (3 - NG);  // the group of this k step
                     if (i >= 0 && kk > 0 && i < NG) {
-                        // younger than the group: the groups after it, A's windows, and the groups
-                        // already loaded for slab s + 2. (So A of slab s + 1, older than all of
-                        // them, has landed too.)
-                        wait_vmcnt<JA + (NG - 1) * LG>();
+                        // younger than the group: with one set A's windows and the slab's other
+                        // group, with two A's windows twice and a group
+                        wait_vmcnt<PF * JA + (PF * NG - 1) * LG>();
                         __builtin_amdgcn_sched_barrier(0);
-                        write_group(i, s + 1, hnb);
-                        load_group(i, s + 2);
+                        write_group(i, s + 1, hnb, SET);
+                        load_group(i, s + 1 + PF, SET);
                         vmem += LG;
                         valu = NVALU;
                         dsw = 4;
                     }
                     mfmas(cb, vmem, valu, dsw);
                 } else {
+                    // A of slab s + 1 has landed: with one set it is older than the groups that
+                    // were waited for; with two, the groups of slab s + 2, A's windows and the
+                    // groups of slab s + 3 are younger
+                    if (PF == 2) wait_vmcnt<JA + 2 * NG * LG>();
                     lds_barrier();  // slab s + 1 published; slab s's halves read by nobody any more
                     read_frags(hna, hnb, 0, cb ^ 1);
                     if (SH == 0) window(0, s + 3, hb);
@@ -269,6 +280,14 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
                 }
             }
             ha = wrap5(ha + 2);
+        };
+        if constexpr (PF == 1) {
+            for (int s = 0; s < nslabs; ++s) slab(s, std::integral_constant<int, 0>{});
+        } else {
+            for (int s = 0; s < nslabs; s += 2) {
+                slab(s, std::integral_constant<int, 1>{});
+                if (s + 1 < nslabs) slab(s + 1, std::integral_constant<int, 0>{});
+            }
         }
     };
     if (STAGGER && wave >= 2)
