@@ -370,6 +370,9 @@ __global__ __launch_bounds__(256) void mx_join_kernel(int splits, int M, int N, 
     }
 }
 
+#ifndef MXS_WANT
+#define MXS_WANT 512
+#endif
 #ifndef MXD_WIN
 #define MXD_WIN 1
 #define MXD_STAG 1
@@ -382,31 +385,19 @@ hipError_t launch_mxd(const MxProblem &p, hipStream_t s, int t, int splits) {
     const int tiles_m = (p.M + t - 1) / t, tiles_n = (p.N + t - 1) / t;
     const dim3 grid((unsigned)((int64_t)tiles_m * tiles_n * splits));
     const int slabs = (p.K + MXD_BK - 1) / MXD_BK, per = (slabs + splits - 1) / splits;
-    // with more than one split the tiles' sums go to the workspace, M x N for each split
-    const bool direct = splits == 1;
-    float *const out = direct ? p.C : (float *)p.work;
-    const int64_t ldo = direct ? p.ldc : p.N, stride = direct ? 0 : (int64_t)p.M * p.N;
-    const float alpha = direct ? p.alpha : 1.0f, beta = direct ? p.beta : 0.0f;
+    const MxParts o = mx_parts(p, splits);
 #define REGTILE_MXD(T_, W_, S_)                                                                                    \
     do {                                                                                                           \
         note_launch(reinterpret_cast<const void *>(&mx_dma_kernel<T_, FP4, F16, A_MN, B_MN, KTAIL, W_, S_>), MXD_NT); \
         hipLaunchKernelGGL((mx_dma_kernel<T_, FP4, F16, A_MN, B_MN, KTAIL, W_, S_>), grid, dim3(MXD_NT), 0, s, p.M,   \
-                           p.N, p.K, alpha, (const uint16_t *)p.A, p.lda, p.Q, p.ldq, p.S, p.lds, beta, out, ldo,   \
-                           tiles_m, tiles_n, per, stride);                                                         \
+                           p.N, p.K, o.alpha, (const uint16_t *)p.A, p.lda, p.Q, p.ldq, p.S, p.lds, o.beta, o.C,    \
+                           o.ldc, tiles_m, tiles_n, per, o.stride);                                                \
     } while (0)
     if (t == 256) REGTILE_MXD(256, MXD_WIN, MXD_STAG);
     else REGTILE_MXD(128, MXD_SWIN, MXD_SSTAG);
 #undef REGTILE_MXD
-    if (!direct) {
-        hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        const int64_t n = (int64_t)p.M * p.N;
-        const int vec = p.N % 4 == 0 && p.ldc % 4 == 0 && aligned16(p.C) && aligned16(p.work);
-        const int64_t units = vec ? n / 4 : n, blocks = (units + 255) / 256;
-        hipLaunchKernelGGL(mx_join_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, splits,
-                           p.M, p.N, p.alpha, (const float *)p.work, p.beta, p.C, p.ldc, vec);
-    }
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess && splits > 1 ? launch_mx_join(p, s, splits) : e;
 }
 template <bool FP4, bool F16>
 hipError_t launch_mxd_order(const MxProblem &p, hipStream_t s, int t, int splits) {
@@ -418,15 +409,37 @@ hipError_t launch_mxd_order(const MxProblem &p, hipStream_t s, int t, int splits
 
 }  // namespace
 
-// How many parts of k the product wants (1: none): see launch_mx_dma.
+hipError_t launch_mx_join(const MxProblem &p, hipStream_t s, int splits) {
+    const int64_t n = (int64_t)p.M * p.N;
+    const int vec = p.N % 4 == 0 && p.ldc % 4 == 0 && aligned16(p.C) && aligned16(p.work);
+    const int64_t units = vec ? n / 4 : n, blocks = (units + 255) / 256;
+    hipLaunchKernelGGL(mx_join_kernel, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, splits, p.M, p.N,
+                       p.alpha, (const float *)p.work, p.beta, p.C, p.ldc, vec);
+    return hipGetLastError();
+}
+
 int mx_splits(bool ta, bool tb, int M, int N, int K, int64_t lda, int64_t ldc) {
-    if (!addr::mx_dma_takes(ta, tb, M, N, K, lda, ldc)) return 1;
-    const int64_t tiles = (int64_t)((M + 127) / 128) * ((N + 127) / 128);
-    const int slabs = (K + MXD_BK - 1) / MXD_BK;
-    if (tiles > 128) return 1;
-    const int64_t want = 512 / tiles, most = slabs / 8;
+    const bool sk = !ta && tb && mx_splitk_preferred(M, N, K);
+    if (!sk && !addr::mx_dma_takes(ta, tb, M, N, K, lda, ldc)) return 1;
+    const int64_t t = sk ? 64 : 128, tiles = ((M + t - 1) / t) * ((N + t - 1) / t);
+    const int64_t want = (sk ? MXS_WANT : 512) / tiles, most = K / 512;  // parts of at least 512 k
+    if (!sk && tiles > 128) return 1;
     const int64_t n = want < most ? want : most;
     return n < 1 ? 1 : n > 16 ? 16 : (int)n;
+}
+
+int mx_fit_splits(const MxProblem &p, int slabs) {
+#ifdef MXD_FORCE
+    int64_t n = 1 << 20;
+#else
+    int64_t n = mx_splits(p.ta, p.tb, p.M, p.N, p.K, p.lda, p.ldc);
+#endif
+    const int64_t room = p.work_bytes / ((int64_t)p.M * p.N * 4);
+    if (n > room) n = room;
+    if (n > slabs) n = slabs;
+    if (n < 1) return 1;
+    const int64_t per = (slabs + n - 1) / n;
+    return (int)((slabs + per - 1) / per);
 }
 
 // Takes (and launches, status in *err) a problem whose A meets the 16-bit kernels' DMA conditions
@@ -435,22 +448,7 @@ int mx_splits(bool ta, bool tb, int M, int N, int K, int64_t lda, int64_t ldc) {
 bool launch_mx_dma(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err) {
     if (!addr::mx_dma_takes(p.ta, p.tb, p.M, p.N, p.K, p.lda, p.ldc) || !aligned16(p.A)) return false;
     const int t = addr::dma_tile(p.M, p.N);
-    int splits = 1;
-    if (t == 128 && p.work != nullptr) {
-        const int64_t part = (int64_t)p.M * p.N * 4;
-        const int64_t fit = p.work_bytes / part;
-#ifdef MXD_FORCE
-        const int want = 1 << 20;
-#else
-        const int want = mx_splits(p.ta, p.tb, p.M, p.N, p.K, p.lda, p.ldc);
-#endif
-        splits = (int)(fit < want ? fit : want);
-        const int slabs = (p.K + MXD_BK - 1) / MXD_BK;
-        if (splits > slabs) splits = slabs;
-        if (splits < 1) splits = 1;
-        const int per = (slabs + splits - 1) / splits;
-        splits = (slabs + per - 1) / per;  // every split has slabs
-    }
+    const int splits = t == 128 ? mx_fit_splits(p, (p.K + MXD_BK - 1) / MXD_BK) : 1;
 #define REGTILE_MXD_NAMES(elt, fmt, t) \
     {{elt "_" fmt "_dma_" t "_nn", elt "_" fmt "_dma_" t "_nt"}, {elt "_" fmt "_dma_" t "_tn", elt "_" fmt "_dma_" t "_tt"}}
 #define REGTILE_MXD_SIZES(elt, fmt) {REGTILE_MXD_NAMES(elt, fmt, "256x256x64"), REGTILE_MXD_NAMES(elt, fmt, "128x128x64")}

@@ -217,16 +217,6 @@ __global__ __launch_bounds__(NW * 64) void mx_token_kernel(int M, int N, int K, 
     join_and_store<H, NF, MC, NW>(part, M, N, n0, alpha, beta, C, ldc, vec_c);
 }
 
-// 4 bytes per lane from `src` into LDS at `dst` + lane * 4 (dst wave-uniform)
-__device__ __forceinline__ void dma4(const void *src, void *dst) {
-#if defined(__HIP_DEVICE_COMPILE__)
-    __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void *)dst, 4, 0, 0);
-#else
-    (void)src;
-    (void)dst;
-#endif
-}
-
 // The same product (H = 1) for more tokens and 16-byte aligned rows, through LDS. Reading fragments
 // straight from memory, 16 neighbouring lanes touch 16 rows, 16 bytes of each, and the loads of A (four
 // for one of fp4 codes) spend more of the CU's address unit than the codes do. Here each wave
@@ -311,18 +301,16 @@ __global__ __launch_bounds__(NW * 64) void mx_batch_kernel(int M, int N, int K, 
             const uint4 *row = d + XS + (f * 16 + r) * QCH;
 #pragma unroll
             for (int e = 0; e < QCH / 4; ++e) {
-                const uint4 v = row[FP4 ? j ^ ((r >> 2) & 3) : (2 * j + e) ^ ((r >> 1) & 7)];
-                q[f][4 * e] = v.x;
-                q[f][4 * e + 1] = v.y;
-                q[f][4 * e + 2] = v.z;
-                q[f][4 * e + 3] = v.w;
+                const u32x4 v = lds_read16(&row[FP4 ? j ^ ((r >> 2) & 3) : (2 * j + e) ^ ((r >> 1) & 7)]);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) q[f][4 * e + u] = v[u];
             }
             s[f] = reinterpret_cast<const uint8_t *>(d + XS + QS)[(f * 16 + r) * 4 + j];
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int m = 0; m < MC; ++m) x[m][t] = d[(m * 16 + r) * 16 + ((4 * j + t) ^ r)];
+            for (int m = 0; m < MC; ++m) x[m][t] = __builtin_bit_cast(uint4, lds_read16(&d[(m * 16 + r) * 16 + ((4 * j + t) ^ r)]));
         multiply_group<FP4, F16, NF, MC>(q, s, x, acc);
         wait_lgkmcnt0();  // the chunk is in registers before its slot is filled again
         asm volatile("" ::: "memory");
@@ -418,8 +406,7 @@ hipError_t launch_batch_rows(const MxProblem &p, hipStream_t s) {
 // kernel, which takes the others. Returns false, launching nothing, for any other problem.
 bool launch_mx_token(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err) {
     if (p.ta || !p.tb) return false;
-    const bool lds = p.M > 8 && p.M <= 64 && p.lda % 8 == 0 && aligned16(p.A) && p.ldq % 16 == 0 && aligned16(p.Q) &&
-                     p.lds % 4 == 0 && (reinterpret_cast<uintptr_t>(p.S) & 3u) == 0;
+    const bool lds = p.M > 8 && p.M <= 64 && mx_rows_aligned(p);
     if (!lds && p.M > 32) return false;
 #define REGTILE_TOKEN_SET(elt, fmt)                                                                            \
     {{elt "_" fmt "_token4", elt "_" fmt "_token8", elt "_" fmt "_token16", elt "_" fmt "_token32"},          \

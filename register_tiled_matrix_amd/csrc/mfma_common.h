@@ -29,6 +29,27 @@ __device__ __forceinline__ void dma16(const void *src, void *dst) {
 #endif
 }
 
+// 4 bytes per lane from `src` into LDS at `dst` + lane * 4 (dst wave-uniform)
+__device__ __forceinline__ void dma4(const void *src, void *dst) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_global_load_lds(src, (__attribute__((address_space(3))) void *)dst, 4, 0, 0);
+#else
+    (void)src;
+    (void)dst;
+#endif
+}
+
+// LDS accesses of kernels that keep LDS DMA in flight, 16 (8) bytes at a 16 (8) byte aligned address.
+// They go through vector types on purpose: before an LDS access of HIP's uint4 / uint2 members the compiler
+// waits for every LDS DMA load under way (s_waitcnt vmcnt(0)), which the kernels order themselves.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u32x4 lds_read16(const void *p) { return *reinterpret_cast<const u32x4 *>(p); }
+__device__ __forceinline__ u32x2 lds_read8(const void *p) { return *reinterpret_cast<const u32x2 *>(p); }
+__device__ __forceinline__ void lds_write16(void *p, uint4 v) {
+    *reinterpret_cast<u32x4 *>(p) = __builtin_bit_cast(u32x4, v);
+}
+
 // Buffer descriptor over `bytes` bytes at `base`, raw (untyped) dword access: data format
 // 32 in the fourth descriptor word, stride 0 (num_records counts bytes), and the hardware
 // returns zero for any byte past num_records. Host-pass stubs exist only to type-check.

@@ -209,7 +209,8 @@ int run_mx(bool f16, int format, int trans_a, int trans_b, int M, int N, int K, 
         return status;
     const char *name = "none";
     hipError_t err;
-    if (!regtile::launch_mx_token(p, s, &name, &err) && !regtile::launch_mx_dma(p, s, &name, &err))
+    if (!regtile::launch_mx_token(p, s, &name, &err) && !regtile::launch_mx_splitk(p, s, &name, &err) &&
+        !regtile::launch_mx_dma(p, s, &name, &err))
         err = regtile::launch_mx_mfma(p, s, &name);
     return finish(err, name);
 }

@@ -99,9 +99,28 @@ bool launch_mx_token(const MxProblem &p, hipStream_t s, const char **name, hipEr
 // The product on DMA-fed tiles for aligned A and whole groups of B (addr::mx_dma_takes); false,
 // launching nothing, for any other problem.
 bool launch_mx_dma(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err);
-// Parts of k that launch_mx_dma makes of a product when it is given a workspace of one M x N fp32
-// matrix for each (1: it makes no use of one).
+// The product of few tiles with a row-major aligned A and B stored N x K, k split over waves; false,
+// launching nothing, for any other problem.
+bool launch_mx_splitk(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err);
+bool mx_splitk_preferred(int M, int N, int K);
+// Parts of k that the two kernels above make of a product when they are given a workspace of one
+// M x N fp32 matrix for each (1: they make no use of one). `aligned`: mx_rows_aligned.
 int mx_splits(bool ta, bool tb, int M, int N, int K, int64_t lda, int64_t ldc);
+// The parts that the workspace of `p` has room for, each with at least one of the `slabs`.
+int mx_fit_splits(const MxProblem &p, int slabs);
+// Where a launch of `splits` parts writes: C itself, or the workspace's M x N parts, unscaled.
+struct MxParts {
+    float *C;
+    int64_t ldc, stride;
+    float alpha, beta;
+};
+inline MxParts mx_parts(const MxProblem &p, int splits) {
+    if (splits == 1) return {p.C, p.ldc, 0, p.alpha, p.beta};
+    return {static_cast<float *>(p.work), p.N, (int64_t)p.M * p.N, 1.0f, 0.0f};
+}
+// C = alpha (sum of the parts, in order) + beta C
+hipError_t launch_mx_join(const MxProblem &p, hipStream_t s, int splits);
+
 // The default 16-bit entry points take the split-K kernel for problems of few 64x64 tiles with
 // enough K per wave: at most 256 tiles (one per CU) with K >= 1024 in any storage order, and at
 // most 512 with K >= 4096 for K-contiguous A and B ("n t") or M/N-contiguous both ("t n").
@@ -120,6 +139,11 @@ inline bool bf16_splitk_preferred(const Problem &p) {
 // Host-side launch checks.
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+// Rows of A, codes and scales that DMA can read from any chunk of 128 k on
+inline bool mx_rows_aligned(const MxProblem &p) {
+    return p.lda % 8 == 0 && aligned16(p.A) && p.ldq % 16 == 0 && aligned16(p.Q) && p.lds % 4 == 0 &&
+           (reinterpret_cast<uintptr_t>(p.S) & 3u) == 0;
+}
 
 // Four consecutive floats at any 4-byte-aligned address as one global_load_dwordx4:
 // multi-dword global loads need only dword alignment on gfx9-class GPUs (the compiler emits

@@ -36,6 +36,15 @@ def dev(x, pad=0, fill=0):
     return v
 
 
+def dev_aligned(x, fill=0):
+    """`x` on the GPU with rows that start at multiples of 16 elements, `fill` behind them."""
+    x = torch.as_tensor(x)
+    full = torch.full((x.shape[0], (x.shape[1] + 15) // 16 * 16), fill, dtype=x.dtype, device="cuda")
+    v = full[:, :x.shape[1]]
+    v.copy_(x)
+    return v
+
+
 def random_codes(rng, fmt, rows, cols, e_lo=120, e_hi=130):
     w, g = mx.widths(fmt, cols)
     codes = rng.integers(0, 256, (rows, w), dtype=np.uint8)
@@ -144,13 +153,16 @@ def test_conversions_touch_their_rows_only(fmt, dtype, rows, cols):
 
 
 # ---- products ------------------------------------------------------------------------------
-def product(rng, fmt, dtype, order, M, N, K, alpha=1.0, beta=0.0, pad=0, e_lo=120, e_hi=130, c_pad=0, label=""):
+def product(rng, fmt, dtype, order, M, N, K, alpha=1.0, beta=0.0, pad=0, e_lo=120, e_hi=130, c_pad=0, label="", aligned=False):
     """One product against 64 bits; the padding of every operand is NaN (codes 0xFF, scales 255), C's
     must stay."""
     A = half_matrix(rng, K, M, dtype) if order[0] == "t" else half_matrix(rng, M, K, dtype)
     rows, cols = (N, K) if order[1] == "t" else (K, N)
     codes, scales = random_codes(rng, fmt, rows, cols, e_lo, e_hi)
-    Ad, Qd, Sd = dev(A, pad, float("nan")), dev(codes, pad, 255), dev(scales, pad, 255)
+    if aligned:
+        Ad, Qd, Sd = dev_aligned(A, float("nan")), dev_aligned(codes, 255), dev_aligned(scales, 255)
+    else:
+        Ad, Qd, Sd = dev(A, pad, float("nan")), dev(codes, pad, 255), dev(scales, pad, 255)
     B = rt.MXMatrix(fmt, Qd, Sd, cols)
     C0 = torch.from_numpy(rng.standard_normal((M, N))).float()
     Cf = torch.full((M, N + 2 * c_pad), 3.0, device="cuda")
@@ -203,6 +215,18 @@ def test_product_tokens(fmt, N, M):
         product(rng, fmt, "bf16" if K != 2080 else "f16", "nt", M, N, K, beta=0.5 if pad else 0.0, pad=pad, c_pad=pad % 2, label="tokens")
 
 
+# K split over the waves of 64x64 tiles: whole slabs of 128 and a tail, fewer slabs than the ring, one
+# part and several
+@pytest.mark.parametrize("M,N,K", [(65, 40, 512), (100, 1500, 777), (128, 64, 1024), (130, 200, 4096 + 72), (192, 72, 2049), (300, 520, 640)])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_product_split_over_waves(fmt, M, N, K):
+    rng = np.random.default_rng(M + N + K)
+    product(rng, fmt, "bf16", "nt", M, N, K, label="split-K", aligned=True)
+    assert "splitk4" in rt.last_kernel()
+    product(rng, fmt, "f16", "nt", M, N, K, alpha=-0.5, beta=2.0, c_pad=1, label="split-K", aligned=True)
+    assert "splitk4" in rt.last_kernel()
+
+
 # the DMA kernels: one slab, slabs that end inside a group of four, tiles that end anywhere, 128 and
 # 256 wide tiles
 @pytest.mark.parametrize("M,N,K", [(72, 96, 32), (136, 160, 64), (200, 288, 96), (128, 128, 640), (264, 512, 224), (1000, 1504, 800),
@@ -212,9 +236,9 @@ def test_product_tokens(fmt, N, M):
 def test_product_dma(fmt, order, M, N, K):
     rng = np.random.default_rng(M + N + K)
     product(rng, fmt, "bf16", order, M, N, K, label="dma")
-    assert "_dma_" in rt.last_kernel()
+    assert "_dma_" in rt.last_kernel() or "_splitk4_" in rt.last_kernel()
     product(rng, fmt, "f16", order, M, N, K, alpha=0.5, beta=-1.0, pad=16, c_pad=1, label="dma, padded")
-    assert "_dma_" in rt.last_kernel()
+    assert "_dma_" in rt.last_kernel() or "_splitk4_" in rt.last_kernel()
 
 
 @pytest.mark.parametrize("M,N,K", [(72, 96, 2048), (128, 288, 4096 + 32), (264, 136 + 24, 8192)])
