@@ -6,10 +6,9 @@
 // the next k step read and DMA issued between the MFMAs of this one, one barrier a slab. Slab t's A
 // part sits in half (2 t) % 5 and its B part in half (2 t + 1) % 5.
 //
-// B: a thread owns T / 128 groups of 32 codes of each slab. Codes and scale bytes are loaded ahead (by
-// one slab's time, or two on 128-wide tiles, whose slabs are short), and while slab s is multiplied those
-// of slab s + 1 are expanded to the 16-bit type (exact; mx_common.h) and written to their half, a
-// group in a k step, between MFMAs. Expanding costs 0.5
+// B: a thread owns T / 128 groups of 32 codes of each slab. Codes and scale bytes are loaded two slabs
+// ahead, and while slab s is multiplied those of slab s + 1 are expanded to the 16-bit type (exact;
+// mx_common.h) and written to their half, a group in a k step, between MFMAs. Expanding costs 0.5
 // (fp4) or 2.5 (int8) vector instructions a value and happens once a workgroup; keeping the codes in
 // LDS and expanding fragments would repeat it in the two waves that share each column.
 //
@@ -36,6 +35,13 @@ using namespace mfma;
 
 constexpr int MXD_BK = 64, MXD_NT = 256;
 
+// f on four parts of LDS that do not overlap
+template <class F>
+__device__ __forceinline__ void apart(const uint4 *__restrict__ ra, const uint4 *__restrict__ rb, uint4 *__restrict__ wa,
+                                      uint4 *__restrict__ wb, F f) {
+    f(ra, rb, wa, wb);
+}
+
 template <int T, bool FP4, bool F16, bool A_MN, bool B_MN, bool KTAIL, int NWIN, int STAGGER>
 __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, float alpha,
                                                         const uint16_t *__restrict__ A, int64_t lda,
@@ -54,7 +60,6 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
     constexpr int KSTEPS = MXD_BK / F::KSTEP, NMFMA = MI * NI;
     constexpr int NREAD = MI * (A_MN ? 2 : 1) + NI * (B_MN ? 2 : 1);
     constexpr int PER_WIN = JA / NWIN;
-    constexpr int PF = T == 128 ? 2 : 1;       // register sets for B's groups
     static_assert(KSTEPS == 4 && JA % NWIN == 0 && NWIN + STAGGER <= 2, "windows at the last and the first k step");
     static_assert(NG == 1 || NG == 2, "groups go in k steps 1 and 2");
     __shared__ uint4 smem[5 * HALF];
@@ -82,13 +87,13 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
         a_voff_last[j] = k_last + ka < K ? a_voff[j] : a_voff[j] | addr::kPastEnd;
         if (A_MN) a_voff[j] = addr::mn_dma_lane(lane, j, lda, MCH);
     }
-    auto dma_a = [&](int q, int slab, int half) {
+    auto dma_a = [&](int q, int slab, uint4 *half) {
         const int k0 = (first_slab + min(slab, nslabs - 1)) * MXD_BK;
         const uint32_t voff = KTAIL && !A_MN && k0 == k_last ? a_voff_last[q & 1] : a_voff[q & 1];
         const uint32_t soff = A_MN ? addr::mn_dma_instr(wave, JA, q, k0, lda, MCH) : addr::kc_dma_instr<KCH>(q, k0, lda);
-        dma16_buf(a_rsrc, voff, soff, smem + half * HALF + (wave * JA + q) * 64);
+        dma16_buf(a_rsrc, voff, soff, half + (wave * JA + q) * 64);
     };
-    auto window = [&](int win, int slab, int half) {
+    auto window = [&](int win, int slab, uint4 *half) {
 #pragma unroll
         for (int d = 0; d < PER_WIN; ++d) dma_a(win * PER_WIN + d, slab, half);
     };
@@ -108,8 +113,9 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
         qbase[i] = Q + row * ldq + g * GB;
         sbase[i] = S + row * lds + g;
     }
-    uint32_t q[PF][NG][GB / 4], sc[PF][NG];
-    auto load_group = [&](int i, int s, int set) {
+    uint32_t q[NG][GB / 4];
+    uint8_t sc[NG];  // (as bytes: widened where they are loaded, they are waited for there)
+    auto load_group = [&](int i, int s) {
         const int slab = first_slab + s;
         int64_t qo, so;
         if constexpr (B_MN) {
@@ -120,21 +126,21 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
             so = min(2 * slab + b_g[i], last_g);
             qo = so * GB;
         }
-        mx::load_bytes<GB>(qbase[i] + qo, q[set][i]);
-        sc[set][i] = sbase[i][so];
+        mx::load_bytes<GB>(qbase[i] + qo, q[i]);
+        sc[i] = sbase[i][so];
     };
     auto b_slot = [](int r, int c) {
         if constexpr (!B_MN) return r * KCH + (c ^ slab_key<KCH, MF>(r));
         const int low = T == 256 ? ((r & 1) << 1) | ((c >> 4) & 1) : r & 3;
         return r * MCH + (c ^ (4 * (r & 3)) ^ low);
     };
-    auto write_group = [&](int i, int s_, int half, int set) {
+    auto write_group = [&](int i, int s_, uint4 *half) {
         const int slab = first_slab + s_;
         const bool past = B_MN ? slab * MXD_BK + b_row[i] >= K : 2 * slab + b_g[i] > last_g;
-        const float s = mx::scale_value<FP4>(past ? 0u : sc[set][i]);
-        uint4 *d = smem + half * HALF;
+        const float s = mx::scale_value<FP4>(past ? 0u : sc[i]);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) d[b_slot(b_row[i], 4 * b_g[i] + t)] = mx::expand8<FP4, F16>(q[set][i], t, s);
+        for (int t = 0; t < 4; ++t)
+            lds_write16(half + b_slot(b_row[i], 4 * b_g[i] + t), mx::expand8<FP4, F16>(q[i], t, s));
     };
 
     // ---- fragments ----
@@ -150,15 +156,14 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
     const int tr_col = 16 * ((lane >> 4) & 1) + 4 * (tr_t & 3);  // column within the fragment
     auto kc_frag = [&](const uint4 *slab, int row0, int kk) {
         const int row = row0 + (lane & 31), chunk = 2 * kk + (lane >> 5);
-        return __builtin_bit_cast(bf16x8, slab[row * KCH + (chunk ^ slab_key<KCH, MF>(row))]);
+        return __builtin_bit_cast(bf16x8, lds_read16(&slab[row * KCH + (chunk ^ slab_key<KCH, MF>(row))]));
     };
     auto pair = [](const char *lo_at, const char *hi_at) {
         const uint2 lo = lds_read_tr16(lo_at), hi = lds_read_tr16(hi_at);
         return __builtin_bit_cast(bf16x8, make_uint4(lo.x, lo.y, hi.x, hi.y));
     };
     bf16x8 fa[2][MI], fb[2][NI];
-    auto read_frags = [&](int ha, int hb, int kk, int buf) {
-        const uint4 *sa = smem + ha * HALF, *sb = smem + hb * HALF;
+    auto read_frags = [&](const uint4 *sa, const uint4 *sb, int kk, int buf) {
         const int row = 16 * kk + tr_row;
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
@@ -212,83 +217,78 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
     };
     constexpr int NVALU = FP4 ? 18 : (F16 ? 84 : 84);  // of a group's expansion
 
+    // One barrier to the next: the last k step of slab s - 1 (its fragments are in registers), then the
+    // first three of slab s, whose parts are `ra` and `rb`. Freed by the barrier: `wa`, which takes the
+    // A part of slab s + 2, and `wb`, which takes the B part of slab s + 1. The four halves differ; the
+    // restrict qualifiers say so, without which the compiler waits for all DMA under way before each
+    // transposing read.
+    auto period = [&](int s, const uint4 *ra, const uint4 *rb, uint4 *wa, uint4 *wb, auto first_tag, auto shift_tag) {
+        constexpr bool FIRST = decltype(first_tag)::value;  // slab 0: nothing precedes it
+        constexpr int SH = decltype(shift_tag)::value;
+        if constexpr (!FIRST) {
+            read_frags(ra, rb, 0, 0);
+            if (SH == 0) window(0, s + 2, wa);
+            mfmas(1, SH == 0 ? PER_WIN : 0, 0, 0);
+        }
+#pragma unroll
+        for (int kk = 0; kk + 1 < KSTEPS; ++kk) {
+            const int cb = kk & 1;
+            wait_lgkmcnt0();  // this step's fragments
+            __builtin_amdgcn_sched_barrier(0);
+            read_frags(ra, rb, kk + 1, cb ^ 1);
+            int vmem = 0, valu = 0, dsw = 0;
+            if (kk == 0 && 1 - SH < NWIN) {
+                window(1 - SH, s + 2, wa);
+                vmem += PER_WIN;
+            }
+            const int i = kk - (3 - NG);  // the group of this k step
+            if (i >= 0 && kk > 0 && i < NG) {
+                // younger than the group: A's windows and the slab's other group. (So A of slab
+                // s + 1, older than all of them, has landed too.)
+                wait_vmcnt<JA + (NG - 1) * LG>();
+                __builtin_amdgcn_sched_barrier(0);
+                write_group(i, s + 1, wb);
+                load_group(i, s + 2);
+                vmem += LG;
+                valu = NVALU;
+                dsw = 4;
+            }
+            mfmas(cb, vmem, valu, dsw);
+        }
+        wait_lgkmcnt0();  // the last step's fragments and the writes of slab s + 1
+    };
+
     auto wrap5 = [](int h) { return h >= 5 ? h - 5 : h; };
     // SH: with STAGGER the second half of the waves issues its DMA a k step later
     auto loop = [&](auto shift_tag) {
         constexpr int SH = decltype(shift_tag)::value;
 #pragma unroll
-        for (int i = 0; i < NG; ++i) load_group(i, 0, 0);
+        for (int i = 0; i < NG; ++i) load_group(i, 0);
 #pragma unroll
-        for (int d = 0; d < JA; ++d) dma_a(d, 0, 0);
-        if (PF == 2) {
+        for (int d = 0; d < JA; ++d) dma_a(d, 0, smem);
 #pragma unroll
-            for (int i = 0; i < NG; ++i) load_group(i, 1, PF - 1);
-        }
+        for (int d = 0; d < JA; ++d) dma_a(d, 1, smem + 2 * HALF);
 #pragma unroll
-        for (int d = 0; d < JA; ++d) dma_a(d, 1, 2);
+        for (int i = 0; i < NG; ++i) write_group(i, 0, smem + HALF);
 #pragma unroll
-        for (int i = 0; i < NG; ++i) write_group(i, 0, 1, 0);
-#pragma unroll
-        for (int i = 0; i < NG; ++i) load_group(i, PF, 0);
-        if (SH == 0) window(0, 2, 4);
+        for (int i = 0; i < NG; ++i) load_group(i, 1);
+        if (SH == 0) window(0, 2, smem + 4 * HALF);
         __builtin_amdgcn_sched_barrier(0);
         // A of slab 0 has landed: only A of slab 1, B's loads after it and the window are younger
-        wait_vmcnt<JA + PF * NG * LG + (SH == 0 ? PER_WIN : 0)>();
+        wait_vmcnt<JA + NG * LG + (SH == 0 ? PER_WIN : 0)>();
         wait_lgkmcnt0();
         lds_barrier();
-        read_frags(0, 1, 0, 0);
-        int ha = 0;
-        // slab s; set: the registers of slab s + 1's groups, which then take those of slab s + 1 + PF
-        auto slab = [&](int s, auto set_tag) {
-            constexpr int SET = decltype(set_tag)::value;
-            const int hb = wrap5(ha + 1), hna = wrap5(ha + 2), hnb = wrap5(ha + 3), hfa = wrap5(ha + 4);
-#pragma unroll
-            for (int kk = 0; kk < KSTEPS; ++kk) {
-                const int cb = kk & 1;
-                wait_lgkmcnt0();  // this step's fragments, and in the last step the writes of slab s + 1
-                __builtin_amdgcn_sched_barrier(0);
-                if (kk + 1 < KSTEPS) {
-                    read_frags(ha, hb, kk + 1, cb ^ 1);
-                    int vmem = 0, valu = 0, dsw = 0;
-                    const int win = kk + 1 - SH;  // the windows after slab s - 1's barrier
-                    if (win >= 0 && win < NWIN && kk == 0) {
-                        window(win, s + 2, hfa);
-                        vmem += PER_WIN;
-                    }
-                    const int i = kk - (3 - NG);  // the group of this k step
-                    if (i >= 0 && kk > 0 && i < NG) {
-                        // younger than the group: with one set A's windows and the slab's other
-                        // group, with two A's windows twice and a group
-                        wait_vmcnt<PF * JA + (PF * NG - 1) * LG>();
-                        __builtin_amdgcn_sched_barrier(0);
-                        write_group(i, s + 1, hnb, SET);
-                        load_group(i, s + 1 + PF, SET);
-                        vmem += LG;
-                        valu = NVALU;
-                        dsw = 4;
-                    }
-                    mfmas(cb, vmem, valu, dsw);
-                } else {
-                    // A of slab s + 1 has landed: with one set it is older than the groups that
-                    // were waited for; with two, the groups of slab s + 2, A's windows and the
-                    // groups of slab s + 3 are younger
-                    if (PF == 2) wait_vmcnt<JA + 2 * NG * LG>();
-                    lds_barrier();  // slab s + 1 published; slab s's halves read by nobody any more
-                    read_frags(hna, hnb, 0, cb ^ 1);
-                    if (SH == 0) window(0, s + 3, hb);
-                    mfmas(cb, SH == 0 ? PER_WIN : 0, 0, 0);
-                }
-            }
+        read_frags(smem, smem + HALF, 0, 0);
+        apart(smem, smem + HALF, smem + 4 * HALF, smem + 3 * HALF,
+              [&](const uint4 *ra, const uint4 *rb, uint4 *wa, uint4 *wb) { period(0, ra, rb, wa, wb, std::true_type{}, shift_tag); });
+        int ha = 0;  // the half of slab s - 1's A part
+        for (int s = 1; s < nslabs; ++s) {
+            lds_barrier();  // slab s published; slab s - 1's halves read by nobody any more
             ha = wrap5(ha + 2);
-        };
-        if constexpr (PF == 1) {
-            for (int s = 0; s < nslabs; ++s) slab(s, std::integral_constant<int, 0>{});
-        } else {
-            for (int s = 0; s < nslabs; s += 2) {
-                slab(s, std::integral_constant<int, 1>{});
-                if (s + 1 < nslabs) slab(s + 1, std::integral_constant<int, 0>{});
-            }
+            apart(smem + ha * HALF, smem + wrap5(ha + 1) * HALF, smem + wrap5(ha + 4) * HALF, smem + wrap5(ha + 3) * HALF,
+                  [&](const uint4 *ra, const uint4 *rb, uint4 *wa, uint4 *wb) { period(s, ra, rb, wa, wb, std::false_type{}, shift_tag); });
         }
+        mfmas(1, 0, 0, 0);  // the last k step
     };
     if (STAGGER && wave >= 2)
         loop(std::integral_constant<int, STAGGER ? 1 : 0>{});
@@ -371,7 +371,7 @@ __global__ __launch_bounds__(256) void mx_join_kernel(int splits, int M, int N, 
 }
 
 #ifndef MXS_WANT
-#define MXS_WANT 512
+#define MXS_WANT 256
 #endif
 #ifndef MXD_WIN
 #define MXD_WIN 1
