@@ -370,15 +370,9 @@ __global__ __launch_bounds__(256) void mx_join_kernel(int splits, int M, int N, 
     }
 }
 
-#ifndef MXS_WANT
-#define MXS_WANT 256
-#endif
-#ifndef MXD_WIN
-#define MXD_WIN 1
-#define MXD_STAG 1
-#define MXD_SWIN 2
-#define MXD_SSTAG 0
-#endif
+// DMA windows a slab and stagger, as in the 16-bit kernel (two windows and no stagger on 256-wide tiles:
+// 939 against 912 us at 8192^3 fp4 nt, 287 against 252 at 4096 x 4096 x 8192 nn)
+constexpr int MXD_WIN = 1, MXD_STAG = 1, MXD_SWIN = 2, MXD_SSTAG = 0;
 
 template <bool FP4, bool F16, bool A_MN, bool B_MN, bool KTAIL>
 hipError_t launch_mxd(const MxProblem &p, hipStream_t s, int t, int splits) {
@@ -418,22 +412,22 @@ hipError_t launch_mx_join(const MxProblem &p, hipStream_t s, int splits) {
     return hipGetLastError();
 }
 
+// Enough parts to fill the chip (two 128-wide workgroups, or one of the split-K kernel's, to a CU), each
+// of at least 512 k, and none where the tiles do that. us by number of parts, fp4 / int8, 128-wide:
+// tn 1024 x 1024 x 16384: 1 315, 2 163, 4 88, 8 57, 16 66; nn 1024 x 1024 x 4096: 1 68, 2 40, 4 30, 6 27,
+// 8 29, 16 35; nt 1024 x 1024 x 1024: 1 15.7, 2 16.8, 4 18.8.
 int mx_splits(bool ta, bool tb, int M, int N, int K, int64_t lda, int64_t ldc) {
     const bool sk = !ta && tb && mx_splitk_preferred(M, N, K);
     if (!sk && !addr::mx_dma_takes(ta, tb, M, N, K, lda, ldc)) return 1;
     const int64_t t = sk ? 64 : 128, tiles = ((M + t - 1) / t) * ((N + t - 1) / t);
-    const int64_t want = (sk ? MXS_WANT : 512) / tiles, most = K / 512;  // parts of at least 512 k
+    const int64_t want = (sk ? 256 : 512) / tiles, most = K / 512;  // workgroups: what LDS lets run at once
     if (!sk && tiles > 128) return 1;
     const int64_t n = want < most ? want : most;
     return n < 1 ? 1 : n > 16 ? 16 : (int)n;
 }
 
 int mx_fit_splits(const MxProblem &p, int slabs) {
-#ifdef MXD_FORCE
-    int64_t n = 1 << 20;
-#else
     int64_t n = mx_splits(p.ta, p.tb, p.M, p.N, p.K, p.lda, p.ldc);
-#endif
     const int64_t room = p.work_bytes / ((int64_t)p.M * p.N * 4);
     if (n > room) n = room;
     if (n > slabs) n = slabs;

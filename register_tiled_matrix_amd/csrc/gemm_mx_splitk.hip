@@ -248,13 +248,8 @@ __global__ __launch_bounds__(MXS_NT) void mx_splitk_kernel(int M, int N, int K, 
     }
 }
 
-#ifndef MXS_TILES
-#define MXS_TILES 512
-#endif
-#ifndef MXS_RF
-#define MXS_RF 7
-#define MXS_RI 6
-#endif
+// slabs in the ring, as many as LDS holds
+constexpr int MXS_RF = 7, MXS_RI = 6;
 
 template <bool FP4, bool F16>
 hipError_t launch_mxs(const MxProblem &p, hipStream_t s, int splits) {
@@ -272,9 +267,13 @@ hipError_t launch_mxs(const MxProblem &p, hipStream_t s, int splits) {
 
 }  // namespace
 
+// Two rounds of tiles at most, and few tiles where K is long: past tiles x K = 2^21 the tiles re-read
+// A and B from L2 more than 128-wide ones, split over workgroups, lose. us, this kernel against that one
+// (fp4): 1024 x 2048 x 1024 14.9, 21.2; 256 x 4096 x 4096 19.0, 27.1; 1024 x 1024 x 8192 34.0, 33.8;
+// 512 x 8192 x 4096 47.5, 46.6; past it 1024 x 1024 x 16384 62.9, 56.6; 256 x 8192 x 8192 60.9, 53.2.
 bool mx_splitk_preferred(int M, int N, int K) {
     const int64_t tiles = (((int64_t)M + MXS_T - 1) / MXS_T) * (((int64_t)N + MXS_T - 1) / MXS_T);
-    return M > 64 && K >= 512 && tiles <= MXS_TILES;
+    return M > 64 && K >= 512 && tiles <= 512 && tiles * K <= (int64_t(1) << 21);
 }
 
 // Takes (and launches, status in *err) products with a row-major A and B stored N x K whose rows are
