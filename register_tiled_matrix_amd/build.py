@@ -27,7 +27,7 @@ ARCH = "gfx950"
 SOURCES = ["regtile_api.hip", "gemm_simple.hip", "gemm_f32_regtile.hip", "gemm_f32_splitk.hip",
            "gemm_bf16_mfma.hip", "gemm_bf16_mfma_dma.hip", "gemm_bf16_mfma_splitk.hip",
            "mx_convert.hip", "gemm_mx_mfma.hip", "gemm_mx_token.hip",
-           "gemm_mx_dma.hip", "gemm_mx_splitk.hip"]
+           "gemm_mx_dma.hip", "gemm_mx_splitk.hip", "gemm_mx_codes.hip"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

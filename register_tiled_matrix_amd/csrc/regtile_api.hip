@@ -210,7 +210,7 @@ int run_mx(bool f16, int format, int trans_a, int trans_b, int M, int N, int K, 
     const char *name = "none";
     hipError_t err;
     if (!regtile::launch_mx_token(p, s, &name, &err) && !regtile::launch_mx_splitk(p, s, &name, &err) &&
-        !regtile::launch_mx_dma(p, s, &name, &err))
+        !regtile::launch_mx_codes(p, s, &name, &err) && !regtile::launch_mx_dma(p, s, &name, &err))
         err = regtile::launch_mx_mfma(p, s, &name);
     return finish(err, name);
 }
