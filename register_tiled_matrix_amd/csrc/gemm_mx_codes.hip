@@ -1,14 +1,15 @@
 // gemm_mx_codes.hip -- C = alpha A op(B) + beta C for large products with a row-major A and a 4-bit
 // block-scaled (MX fp4) B stored N x K: B stays in codes in LDS and is expanded as fragments are read.
 //
-// The 256x256 tile of 4 waves, the LDS DMA and the schedule are those of gemm_mx_dma.hip; what differs is
-// B. There, codes pass through registers into 16-bit LDS slabs, 64 KB written and read back 64 KB (each
-// column by two waves) a slab and CU. Here they go to LDS by DMA and each wave expands its own fragments:
-// 8 KB in and 16 KB out. The expansion is done twice (in the two waves that share a column), but it
-// is 4 conversions for a fragment that feeds 4 MFMAs, and they fit between those.
+// The T x T tile of 4 waves (T = 256, or 128 for few tiles), the LDS DMA and the schedule are those of
+// gemm_mx_dma.hip; what differs is B. There, codes pass through registers into 16-bit LDS slabs: at T =
+// 256, 32 KB are written and 64 KB read back (each column by two waves) a slab. Here they go to LDS by
+// DMA and each wave expands its own fragments: 8 KB in and 16 KB out. The expansion is done twice (in
+// the two waves that share a column), but it is 4 conversions for a fragment that feeds 4 (2) MFMAs,
+// and they fit between those. Against that kernel: 8192^3 809 us, 887.
 //
 // Units of K are 128 deep: two slabs of A (a ring of three, 32 KB each) and 64 bytes of codes and one
-// dword of scale bytes for each column (a ring of two units, 17 KB each). The k order inside a group
+// dword of scale bytes for each column (a ring of two units, 17 KB each; half of all that at T = 128). The k order inside a group
 // of 32 is free as long as both operands agree: lanes 0-31 take k 0 .. 15 and lanes 32-63 k 16 .. 31, 8 of
 // them in each of two k steps, so that a lane's codes for both are one 8-byte read.
 //
@@ -25,19 +26,20 @@ namespace regtile {
 namespace {
 using namespace mfma;
 
-constexpr int MXC_T = 256, MXC_NT = 256;
+constexpr int MXC_NT = 256;
 typedef uint32_t __attribute__((may_alias)) u32_any;  // as lds_read16 and lds_read8: no wait for DMA
 
-template <bool F16>
+template <int T, bool F16>
 __global__ __launch_bounds__(MXC_NT) void mx_codes_kernel(int M, int N, int K, float alpha,
                                                           const uint16_t *__restrict__ A, int64_t lda,
                                                           const uint8_t *__restrict__ Q, int64_t ldq,
                                                           const uint8_t *__restrict__ S, int64_t lds, float beta,
-                                                          float *__restrict__ C, int64_t ldc, int tiles_m, int tiles_n) {
-    constexpr int T = MXC_T, MF = 32, KCH = 8;
+                                                          float *__restrict__ C, int64_t ldc, int tiles_m, int tiles_n,
+                                                          int per_split, int64_t split_stride) {
+    constexpr int MF = 32, KCH = 8;
     typedef Frag<MF, F16> F;
     constexpr int WT = T / 2, MI = WT / MF, NI = WT / MF, NMFMA = MI * NI;
-    constexpr int SLAB = T * KCH, CODES = T * 4, UNIT = CODES + T / 4;  // 16-byte slots
+    constexpr int SLAB = T * KCH, CODES = T * 4, UNIT = CODES + MXC_NT / 4;  // 16-byte slots
     constexpr int JA = SLAB / MXC_NT, JQ = CODES / MXC_NT, PER_UNIT = JQ + 1;
     __shared__ uint4 smem[3 * SLAB + 2 * UNIT];
     uint4 *const units = smem + 3 * SLAB;
@@ -46,9 +48,12 @@ __global__ __launch_bounds__(MXC_NT) void mx_codes_kernel(int M, int N, int K, f
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int wm = wave >> 1, wn = wave & 1;
     int tm, tn;
-    grouped_tile<8>(xcd_contiguous_id(blockIdx.x, gridDim.x), tiles_m, tiles_n, tm, tn);
+    const int id = xcd_contiguous_id(blockIdx.x, gridDim.x), tiles = tiles_m * tiles_n;
+    const int split = id / tiles;  // part of k, per_split units
+    grouped_tile<8>(id - split * tiles, tiles_m, tiles_n, tm, tn);
     const int m0 = tm * T, n0 = tn * T;
-    const int nunits = K / 128, nslabs = 2 * nunits;
+    const int first = split * per_split, nunits = min(per_split, K / 128 - first), nslabs = 2 * nunits;
+    C += split * split_stride;
 
     // ---- DMA ----
     const rsrc_t a_rsrc = make_rsrc(A + (int64_t)m0 * lda, addr::desc_bytes(min(T, M - m0), lda, K, 2));
@@ -59,7 +64,7 @@ __global__ __launch_bounds__(MXC_NT) void mx_codes_kernel(int M, int N, int K, f
         a_voff[j] = addr::kc_dma_lane<KCH, MF>(wave, JA, j, lane, lda, &ka);
     }
     auto dma_a = [&](int slab, int slot) {  // past the last slab the last again, into a free slot
-        const int k0 = min(slab, nslabs - 1) * 64;
+        const int k0 = (2 * first + min(slab, nslabs - 1)) * 64;
 #pragma unroll
         for (int q = 0; q < JA; ++q)
             dma16_buf(a_rsrc, a_voff[q & 1], addr::kc_dma_instr<KCH>(q, k0, lda), smem + slot * SLAB + (wave * JA + q) * 64);
@@ -71,9 +76,9 @@ __global__ __launch_bounds__(MXC_NT) void mx_codes_kernel(int M, int N, int K, f
         const int p = (wave * JQ + j) * 64 + lane, r = p / 4, c = (p % 4) ^ ((r >> 2) & 3);
         qsrc[j] = Q + (int64_t)row_n(r) * ldq + c * 16;
     }
-    ssrc = S + (int64_t)row_n(wave * 64 + lane) * lds;
+    ssrc = S + (int64_t)row_n((wave * 64 + lane) % T) * lds;  // (T = 128: twice, to keep the waves' counts alike)
     auto dma_codes = [&](int unit, int slot) {
-        const int64_t u = min(unit, nunits - 1);
+        const int64_t u = first + min(unit, nunits - 1);
         uint4 *d = units + slot * UNIT;
 #pragma unroll
         for (int j = 0; j < JQ; ++j) dma16(qsrc[j] + u * 64, d + (wave * JQ + j) * 64);
@@ -135,10 +140,16 @@ __global__ __launch_bounds__(MXC_NT) void mx_codes_kernel(int M, int N, int K, f
 #pragma unroll
         for (int m = 0; m < NMFMA; ++m) {
             __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            if (share(vmem, m)) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-            if (share(reads, m)) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-            if (m < 12) __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);  // 4 conversions a column
-            if (m < 12 && (m & 3) == 3) __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                if (t < share(vmem, m)) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                if (t < share(reads, m)) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            if (m < NMFMA - MI) {  // the next column's 4 conversions and its scale
+                __builtin_amdgcn_sched_group_barrier(0x002, 4 / MI, 0);
+                if (m % MI == MI - 1) __builtin_amdgcn_sched_group_barrier(0x002, 1, 0);
+            }
         }
         __builtin_amdgcn_sched_barrier(0);
     };
@@ -243,27 +254,38 @@ __global__ __launch_bounds__(MXC_NT) void mx_codes_kernel(int M, int N, int K, f
     }
 }
 
-template <bool F16>
-hipError_t launch_codes(const MxProblem &p, hipStream_t s) {
-    const int tiles_m = (p.M + MXC_T - 1) / MXC_T, tiles_n = (p.N + MXC_T - 1) / MXC_T;
-    note_launch(reinterpret_cast<const void *>(&mx_codes_kernel<F16>), MXC_NT);
-    hipLaunchKernelGGL((mx_codes_kernel<F16>), dim3((unsigned)((int64_t)tiles_m * tiles_n)), dim3(MXC_NT), 0, s, p.M, p.N,
-                       p.K, p.alpha, (const uint16_t *)p.A, p.lda, p.Q, p.ldq, p.S, p.lds, p.beta, p.C, p.ldc, tiles_m,
-                       tiles_n);
-    return hipGetLastError();
+template <int T, bool F16>
+hipError_t launch_codes(const MxProblem &p, hipStream_t s, int splits) {
+    const int tiles_m = (p.M + T - 1) / T, tiles_n = (p.N + T - 1) / T;
+    const int per = (p.K / 128 + splits - 1) / splits;
+    const MxParts o = mx_parts(p, splits);
+    note_launch(reinterpret_cast<const void *>(&mx_codes_kernel<T, F16>), MXC_NT);
+    hipLaunchKernelGGL((mx_codes_kernel<T, F16>), dim3((unsigned)((int64_t)tiles_m * tiles_n * splits)), dim3(MXC_NT), 0, s,
+                       p.M, p.N, p.K, o.alpha, (const uint16_t *)p.A, p.lda, p.Q, p.ldq, p.S, p.lds, o.beta, o.C, o.ldc,
+                       tiles_m, tiles_n, per, o.stride);
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess && splits > 1 ? launch_mx_join(p, s, splits) : e;
 }
 
 }  // namespace
 
-// Takes (and launches, status in *err) fp4 products that the DMA kernel would run on 256x256 tiles, with
-// B stored N x K, rows aligned for the DMA (mx_rows_aligned) and K in whole units; returns false,
-// launching nothing, for any other.
+// Takes (and launches, status in *err) fp4 products that the DMA kernel would run, with B stored N x K,
+// rows aligned for the DMA (mx_rows_aligned) and K in whole units; returns false, launching nothing, for
+// any other.
 bool launch_mx_codes(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err) {
-    if (!p.fp4 || p.ta || !p.tb || p.K % 128 != 0 || !mx_rows_aligned(p) || addr::dma_tile(p.M, p.N) != 256 ||
+    if (!p.fp4 || p.ta || !p.tb || p.K % 128 != 0 || !mx_rows_aligned(p) ||
         !addr::mx_dma_takes(false, true, p.M, p.N, p.K, p.lda, p.ldc))
         return false;
-    *name = p.f16 ? "f16_fp4_codes_256x256x128_nt" : "bf16_fp4_codes_256x256x128_nt";
-    *err = p.f16 ? launch_codes<true>(p, s) : launch_codes<false>(p, s);
+    const bool small = addr::dma_tile(p.M, p.N) == 128;
+    static const char *const names[2][2] = {{"bf16_fp4_codes_256x256x128_nt", "bf16_fp4_codes_128x128x128_nt"},
+                                            {"f16_fp4_codes_256x256x128_nt", "f16_fp4_codes_128x128x128_nt"}};
+    *name = names[p.f16][small];
+    if (small) {
+        const int splits = mx_fit_splits(p, p.K / 128);
+        *err = p.f16 ? launch_codes<128, true>(p, s, splits) : launch_codes<128, false>(p, s, splits);
+    } else {
+        *err = p.f16 ? launch_codes<256, true>(p, s, 1) : launch_codes<256, false>(p, s, 1);
+    }
     return true;
 }
 

@@ -103,8 +103,8 @@ bool launch_mx_dma(const MxProblem &p, hipStream_t s, const char **name, hipErro
 // launching nothing, for any other problem.
 bool launch_mx_splitk(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err);
 bool mx_splitk_preferred(int M, int N, int K);
-// The fp4 product on 256x256 tiles with a row-major A and B stored N x K, B in codes in LDS; false,
-// launching nothing, for any other problem.
+// The fp4 product of a row-major A and B stored N x K, B in codes in LDS; false, launching nothing, for
+// any other problem.
 bool launch_mx_codes(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err);
 // Parts of k that the DMA and split-K kernels make of a product when they are given a workspace of one
 // M x N fp32 matrix for each (1: they make no use of one). `aligned`: mx_rows_aligned.

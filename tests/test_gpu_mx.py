@@ -241,16 +241,16 @@ def test_product_dma(fmt, order, M, N, K):
     assert "_dma_" in rt.last_kernel() or "_splitk4_" in rt.last_kernel()
 
 
-@pytest.mark.parametrize("M,N,K", [(3000, 3000, 128), (2304, 4096 + 40, 256), (4100, 2304, 640), (33 * 128, 2200, 384)])
+@pytest.mark.parametrize("M,N,K", [(3000, 3000, 128), (2304, 4096 + 40, 256), (4100, 2304, 640), (33 * 128, 2200, 384), (70, 40, 128), (1300, 2000, 256), (2048, 2048, 4096), (300, 300, 9 * 1024 + 128)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_product_codes_in_lds(dtype, M, N, K):
-    """256x256 tiles with 4-bit codes in LDS: one unit of K, an odd and an even number of them, tiles that
-    end anywhere."""
+    """256- and 128-wide tiles with 4-bit codes in LDS: one unit of K, an odd and an even number of them,
+    tiles that end anywhere, K split over workgroups."""
     rng = np.random.default_rng(M + N + K)
     product(rng, mx.FP4, dtype, "nt", M, N, K, label="codes", aligned=True)
-    assert "_codes_" in rt.last_kernel()
+    assert "_codes_" in rt.last_kernel() or M * N < 2**17
     product(rng, mx.FP4, dtype, "nt", M, N, K, alpha=0.5, beta=-1.0, c_pad=1, label="codes", aligned=True)
-    assert "_codes_" in rt.last_kernel()
+    assert "_codes_" in rt.last_kernel() or M * N < 2**17
 
 
 @pytest.mark.parametrize("M,N,K", [(72, 96, 2048), (128, 288, 4096 + 32), (264, 136 + 24, 8192)])
