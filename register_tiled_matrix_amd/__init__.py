@@ -331,12 +331,16 @@ def _check_format(format):
 
 
 _torch = None  # torch, once the first of these calls needs it
+_get_device = _get_stream = None  # the current device's index; the current stream's handle on a device
 
 
 def _import_torch():
-    global _torch
+    global _torch, _get_device, _get_stream
     import torch
 
+    # the plain numbers, without Device and Stream objects around them
+    _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _get_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
     _torch = torch
     return torch
 
@@ -405,7 +409,7 @@ class MXMatrix:
 class _Launch:
     """Makes `device` the current device and `stream` (None: that device's current one) its current
     stream for what is allocated and launched inside, so that the allocator knows where the memory
-    is used; entering gives the stream's handle. Most calls switch nothing and skip it (_current)."""
+    is used; entering gives the stream's handle."""
 
     __slots__ = ("_device", "_stream")
 
@@ -430,24 +434,12 @@ class _Launch:
         self._device.__exit__(*exc)
 
 
-def _current(device, stream):
-    """The handle of the current stream, where the call is to run on the current device and stream;
-    None where _Launch has to switch."""
-    torch = _torch or _import_torch()
-    index = device.index
-    if stream is not None or torch.cuda.current_device() != index:
-        return None
-    try:  # the plain handle, without a Stream object around it
-        return torch._C._cuda_getCurrentRawStream(index)
-    except AttributeError:
-        return torch.cuda.current_stream(device).cuda_stream
-
-
 def _launched(run, device, stream, *args):
-    """run(*args, handle) on `device` and `stream`, as _Launch arranges it."""
-    handle = _current(device, stream)
-    if handle is not None:
-        return run(*args, handle)
+    """run(*args, handle) on `device` and `stream`, as _Launch arranges it where that is not the
+    current device and stream already."""
+    index = device.index
+    if stream is None and _get_device() == index:
+        return run(*args, _get_stream(index))
     with _Launch(device, stream) as handle:
         return run(*args, handle)
 
@@ -530,7 +522,8 @@ def _gemm_mx(name, want, A, B, C, alpha, beta, stream):
         raise ValueError(f"{name} takes device tensors, all on one device")
     ta, lda = _layout(A, "A")
     M, K = A.shape
-    K2, N = B.shape
+    tb = B.transposed
+    K2, N = (B._cols, B._rows) if tb else (B._rows, B._cols)
     if K != K2:
         raise ValueError(f"inner dimensions differ: {K} vs {K2}")
     if C is None:
@@ -539,23 +532,24 @@ def _gemm_mx(name, want, A, B, C, alpha, beta, stream):
         ldc = N if N > 0 else 1
     else:
         ldc = _rows(_out(C, M, N, A), "C")[0]
-    _ints(M, N, K, lda, B._ldq, B._lds, ldc)
-    return _launched(_run_gemm_mx, device, stream, name, A, ta, lda, B, M, N, K, C, ldc, alpha, beta)
+    _ints(M, N, K, lda, ldc, B._ldq, B._lds)
+    return _launched(_run_gemm_mx, device, stream, name, A, ta, lda, B, 1 if tb else 0, M, N, K, C, ldc, alpha, beta)
 
 
-def _run_gemm_mx(name, A, ta, lda, B, M, N, K, C, ldc, alpha, beta, handle):
+def _run_gemm_mx(name, A, ta, lda, B, tb, M, N, K, C, ldc, alpha, beta, handle):
     lib = _lib or load()
     if C is None:
         C = A.new_empty((M, N), dtype=_torch.float32)
-    tb = 1 if B.transposed else 0
     work, at, size = None, None, 0
     if M > 64:  # fewer rows never use a workspace
         size = lib.regtile_gemm_mx_workspace(ta, tb, M, N, K, lda, ldc)
         if size > 0:
             work = A.new_empty(size, dtype=_torch.uint8)  # stays until the launch is queued
             at = work.data_ptr()
-    _check(getattr(lib, name)(B.format, ta, tb, M, N, K, alpha, A.data_ptr(), lda, B.codes.data_ptr(), B._ldq,
-                              B.scales.data_ptr(), B._lds, beta, C.data_ptr(), ldc, at, size, handle))
+    status = getattr(lib, name)(B.format, ta, tb, M, N, K, alpha, A.data_ptr(), lda, B.codes.data_ptr(), B._ldq,
+                                B.scales.data_ptr(), B._lds, beta, C.data_ptr(), ldc, at, size, handle)
+    if status:
+        _check(status)
     return C
 
 
@@ -563,9 +557,9 @@ def gemm_bf16_mx(A, B, C=None, alpha=1.0, beta=0.0, stream=None):
     """C = alpha*A@B + beta*C; bf16 A (M x K), row-major or a transposed view, times a block-scaled B
     (an MXMatrix, K x N; ``W.t()`` for weights stored N x K), fp32 C row-major; returns C (allocated
     when None)."""
-    return _gemm_mx("regtile_gemm_bf16_mx", (_torch or _import_torch()).bfloat16, A, B, C, alpha, beta, stream)
+    return _gemm_mx("regtile_gemm_bf16_mx", (_torch or _import_torch()).bfloat16, A, B, C, float(alpha), float(beta), stream)
 
 
 def gemm_f16_mx(A, B, C=None, alpha=1.0, beta=0.0, stream=None):
     """As gemm_bf16_mx with a float16 A; B's values are taken in float16."""
-    return _gemm_mx("regtile_gemm_f16_mx", (_torch or _import_torch()).float16, A, B, C, alpha, beta, stream)
+    return _gemm_mx("regtile_gemm_f16_mx", (_torch or _import_torch()).float16, A, B, C, float(alpha), float(beta), stream)

@@ -405,7 +405,8 @@ hipError_t launch_batch_rows(const MxProblem &p, hipStream_t s) {
 // N x K: the register kernel up to 8 rows and, up to 32, where rows are not aligned for the LDS
 // kernel, which takes the others. Returns false, launching nothing, for any other problem.
 bool launch_mx_token(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err) {
-    if (p.ta || !p.tb) return false;
+    // (a launch's threads are counted in 32 bits: at most 512 for 4 rows of B here)
+    if (p.ta || !p.tb || p.N >= (1 << 24)) return false;
     const bool lds = p.M > 8 && p.M <= 64 && mx_rows_aligned(p);
     if (!lds && p.M > 32) return false;
 #define REGTILE_TOKEN_SET(elt, fmt)                                                                            \

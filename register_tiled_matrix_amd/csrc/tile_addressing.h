@@ -182,8 +182,10 @@ REGTILE_HD bool rows_dma_takes(bool nn, int M, int N, int K, int64_t lda, int64_
 // The block-scaled kernel (gemm_mx_dma.hip): A as above in either storage order (K-contiguous:
 // whole 16-byte chunks of k; M-contiguous: of m); B in whole groups of 32 along its rows.
 REGTILE_HD bool mx_dma_takes(bool ta, bool tb, int M, int N, int K, int64_t lda, int64_t ldc) {
-    const int64_t t = dma_tile(M, N), lim = int64_t(1) << 31;
-    if (K <= 0 || (tb ? K : N) % 32 != 0 || t * ldc * 4 >= lim) return false;
+    const int64_t lim = int64_t(1) << 31;
+    if (K <= 0 || (tb ? K : N) % 32 != 0 || M > (1 << 30) || N > (1 << 30)) return false;  // (tile counts in 32 bits)
+    const int64_t t = dma_tile(M, N);
+    if (t * ldc * 4 >= lim) return false;
     return ta ? runs_fit(M, lda, 8) && ((int64_t)K + 64) * lda * 2 + 512 < lim
               : K % 8 == 0 && lda % 8 == 0 && t * lda * 2 < lim;
 }

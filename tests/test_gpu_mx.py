@@ -455,6 +455,42 @@ def test_side_stream_and_allocation():
     assert torch.equal(y, want)
 
 
+def test_two_streams_at_once():
+    """Calls that use a workspace, and one token's, running together on two streams: each call has its own
+    workspace, and the results are those of one stream."""
+    X = rt.quantize_mx(torch.randn(4096, 256, device="cuda"), mx.INT8)
+    dy = [torch.randn(4096, 192, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    assert rt.regtile_gemm_mx_workspace(1, 0, 192, 256, 4096, 192, 256) > 0
+    want = [rt.gemm_bf16_mx(d.t(), X) for d in dy]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(rt.gemm_bf16_mx(dy[i].t(), X))
+                rt.gemm_bf16_mx(dy[i][:1], rt.quantize_mx(dy[i], mx.FP4).t())
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in outs[i])
+
+
+def test_many_columns_of_few_tokens():
+    """More columns of C than the token kernels' launches can count threads for."""
+    N, K = (1 << 24) + 40, 32
+    rng = np.random.default_rng(9)
+    codes, scales = random_codes(rng, mx.FP4, 64, K)
+    Q = torch.from_numpy(codes).cuda().repeat(N // 64 + 1, 1)[:N].contiguous()
+    S = torch.from_numpy(scales).cuda().repeat(N // 64 + 1, 1)[:N].contiguous()
+    A = half_matrix(rng, 2, K, "bf16")
+    got = rt.gemm_bf16_mx(A.cuda(), rt.MXMatrix(mx.FP4, Q, S, K).t())
+    a, b = A.double().numpy(), mx.decode(codes, scales, mx.FP4, K).T
+    assert_close(got[:, :64], a @ b, np.abs(a) @ np.abs(b), "many columns")
+    whole = N // 64 * 64
+    assert torch.equal(got[:, :whole].reshape(2, -1, 64), got[:, None, :64].expand(2, N // 64, 64))
+    assert torch.equal(got[:, whole:], got[:, : N - whole])
+
+
 def test_graph_of_a_linear_layer():
     """Forward, checkpoint and both gradients captured together; every replay on new inputs equals the
     eager calls."""
