@@ -90,8 +90,9 @@ def _special_rows(dtype):
     for scale in (1.0, 2.0**-9, 2.0**9):
         for lead in (4.0, 7.75, 6.0):
             ties = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.5, 0.0, -0.0])
-            v = np.concatenate([[lead], ties, -ties, ties * (1 + 2.0**-7)])[:32]
-            rows.append(np.pad(v, (0, 32 - len(v))) * scale)
+            for off in (2.0**-7, 2.0**-20, -(2.0**-20)):
+                v = np.concatenate([[lead], ties, -ties, ties * (1 + off)])[:32]
+                rows.append(np.pad(v, (0, 32 - len(v))) * scale)
         i8 = np.concatenate([[1.0], (np.arange(-8, 8) + 0.5) / 64, [127.5 / 64, -127.5 / 64, 126.5 / 64, -1.0]])
         rows.append(np.pad(i8, (0, 32 - len(i8))) * scale)
     rows += [np.zeros(32), np.full(32, tiny), np.full(32, tiny / 4), np.linspace(-top, top, 32), np.full(32, top)]
