@@ -276,16 +276,17 @@ bool launch_mx_codes(const MxProblem &p, hipStream_t s, const char **name, hipEr
     if (!p.fp4 || p.ta || !p.tb || p.K % 128 != 0 || !mx_rows_aligned(p) ||
         !addr::mx_dma_takes(false, true, p.M, p.N, p.K, p.lda, p.ldc))
         return false;
-    const bool small = addr::dma_tile(p.M, p.N) == 128;
+    const int parts = mx_wide_parts(p.M, p.N, p.K);
+    const bool wide = parts > 1 && mx_fit_splits(p, p.K / 128) == parts;
+    const bool small = !wide && addr::dma_tile(p.M, p.N) == 128;
+    const int splits = wide || (small && parts == 1) ? mx_fit_splits(p, p.K / 128) : 1;
     static const char *const names[2][2] = {{"bf16_fp4_codes_256x256x128_nt", "bf16_fp4_codes_128x128x128_nt"},
                                             {"f16_fp4_codes_256x256x128_nt", "f16_fp4_codes_128x128x128_nt"}};
     *name = names[p.f16][small];
-    if (small) {
-        const int splits = mx_fit_splits(p, p.K / 128);
+    if (small)
         *err = p.f16 ? launch_codes<128, true>(p, s, splits) : launch_codes<128, false>(p, s, splits);
-    } else {
-        *err = p.f16 ? launch_codes<256, true>(p, s, 1) : launch_codes<256, false>(p, s, 1);
-    }
+    else
+        *err = p.f16 ? launch_codes<256, true>(p, s, splits) : launch_codes<256, false>(p, s, splits);
     return true;
 }
 

@@ -254,6 +254,32 @@ def test_product_codes_in_lds(dtype, M, N, K):
     assert "_codes_" in rt.last_kernel() or M * N < 2**17
 
 
+@pytest.mark.parametrize("order", ["nt", "nn", "tn"])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_product_wide_tiles_in_parts(fmt, order):
+    """256x256 tiles in parts of a long K, with the workspace and, on narrower tiles, without."""
+    rng = np.random.default_rng(10)
+    M, N, K = 1040, 1824, 8192 + 96
+    assert rt.regtile_gemm_mx_workspace(int(order[0] == "t"), int(order[1] == "t"), M, N, K, M if order[0] == "t" else K, N) > 0
+    A = half_matrix(rng, *((K, M) if order[0] == "t" else (M, K)), "bf16").cuda()
+    rows, cols = (N, K) if order[1] == "t" else (K, N)
+    codes, scales = random_codes(rng, fmt, rows, cols)
+    B = rt.MXMatrix(fmt, dev_aligned(codes), dev_aligned(scales), cols)
+    ta, tb = int(order[0] == "t"), int(order[1] == "t")
+    C = rt.gemm_bf16_mx(A.t() if ta else A, B.t() if tb else B)
+    assert "256x256" in rt.last_kernel()
+    D = torch.empty_like(C)
+    assert rt.regtile_gemm_bf16_mx(fmt, ta, tb, M, N, K, 1.0, A.data_ptr(), A.stride(0), B.codes.data_ptr(), B.codes.stride(0),
+                                   B.scales.data_ptr(), B.scales.stride(0), 0.0, D.data_ptr(), N, 0, 0,
+                                   torch.cuda.current_stream().cuda_stream) == 0
+    assert "128x128" in rt.last_kernel()
+    a, b = A.double(), torch.from_numpy(mx.decode(codes, scales, fmt, cols)).cuda()
+    a, b = (a.t() if ta else a), (b.t() if tb else b)
+    ref, mag = (a @ b).cpu().numpy(), (a.abs() @ b.abs()).cpu().numpy()
+    assert_close(C, ref, mag, "wide parts")
+    assert_close(D, ref, mag, "128-wide")
+
+
 @pytest.mark.parametrize("M,N,K", [(72, 96, 2048), (128, 288, 4096 + 32), (264, 136 + 24, 8192)])
 @pytest.mark.parametrize("order", ORDERS)
 @pytest.mark.parametrize("fmt", FORMATS)
