@@ -332,6 +332,7 @@ def _check_format(format):
 
 _torch = None  # torch, once the first of these calls needs it
 _get_device = _get_stream = None  # the current device's index; the current stream's handle on a device
+_mx_dtypes = {}  # regtile_mx_dtype by torch dtype
 
 
 def _import_torch():
@@ -341,6 +342,7 @@ def _import_torch():
     # the plain numbers, without Device and Stream objects around them
     _get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _get_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _mx_dtypes.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
     _torch = torch
     return torch
 
@@ -395,11 +397,16 @@ class MXMatrix:
     def device(self):
         return self.codes.device
 
-    def t(self):
-        v = object.__new__(MXMatrix)
-        v.format, v.codes, v.scales, v.transposed = self.format, self.codes, self.scales, not self.transposed
-        v._rows, v._cols, v._ldq, v._lds = self._rows, self._cols, self._ldq, self._lds
+    @classmethod
+    def _of(cls, format, codes, scales, rows, cols, ldq, lds, transposed):
+        """A matrix of parts that are known to fit."""
+        v = object.__new__(cls)
+        v.format, v.codes, v.scales, v.transposed = format, codes, scales, transposed
+        v._rows, v._cols, v._ldq, v._lds = rows, cols, ldq, lds
         return v
+
+    def t(self):
+        return self._of(self.format, self.codes, self.scales, self._rows, self._cols, self._ldq, self._lds, not self.transposed)
 
     def __repr__(self):
         name = "MX_FP4" if self.format == MX_FP4 else "MX_INT8"
@@ -450,9 +457,10 @@ def _ints(*values):
 
 
 def _mx_dtype(dtype, name):
-    torch = _torch or _import_torch()
+    if _torch is None:
+        _import_torch()
     try:
-        return {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}[dtype]
+        return _mx_dtypes[dtype]
     except KeyError:
         raise ValueError(f"{name} must be float32, bfloat16 or float16, not {dtype}") from None
 
@@ -473,9 +481,9 @@ def quantize_mx(X, format=MX_INT8, out=None, stream=None):
 
 def _run_quantize(X, format, dt, rows, cols, ldx, Q, handle):
     if Q is None:
-        u8 = _torch.uint8
-        Q = MXMatrix(format, X.new_empty((rows, _row_bytes(format, cols)), dtype=u8),
-                     X.new_empty((rows, -(-cols // MX_GROUP)), dtype=u8), cols)
+        u8, width, groups = _torch.uint8, _row_bytes(format, cols), -(-cols // MX_GROUP)
+        Q = MXMatrix._of(format, X.new_empty((rows, width), dtype=u8), X.new_empty((rows, groups), dtype=u8), rows, cols,
+                         max(width, 1), max(groups, 1), False)
     _ints(rows, cols, ldx, Q._ldq, Q._lds)
     _check((_lib or load()).regtile_quantize_mx(format, dt, rows, cols, X.data_ptr(), ldx, Q.codes.data_ptr(), Q._ldq,
                                                 Q.scales.data_ptr(), Q._lds, handle))
