@@ -215,7 +215,7 @@ __global__ __launch_bounds__(MXD_NT) void mx_dma_kernel(int M, int N, int K, flo
         }
         __builtin_amdgcn_sched_barrier(0);
     };
-    constexpr int NVALU = FP4 ? 18 : (F16 ? 84 : 84);  // of a group's expansion
+    constexpr int NVALU = FP4 ? 18 : 84;  // of a group's expansion
 
     // One barrier to the next: the last k step of slab s - 1 (its fragments are in registers), then the
     // first three of slab s, whose parts are `ra` and `rb`. Freed by the barrier: `wa`, which takes the
