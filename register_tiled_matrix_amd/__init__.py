@@ -474,7 +474,8 @@ def quantize_mx(X, format=MX_INT8, out=None, stream=None):
     if not X.is_cuda:
         raise ValueError("quantize_mx takes a device tensor")
     ldx, rows, cols = _rows(X, "X")
-    if out is not None and (out.format != format or out.transposed or out.shape != (rows, cols) or out.device != X.device):
+    if out is not None and (not isinstance(out, MXMatrix) or out.format != format or out.transposed or
+                            out.shape != (rows, cols) or out.device != X.device):
         raise ValueError(f"out must be an untransposed MXMatrix of format {format}, shape {(rows, cols)} on {X.device}")
     return _launched(_run_quantize, X.device, stream, X, format, dt, rows, cols, ldx, out)
 

@@ -144,3 +144,18 @@ def test_workspace_sizes():
     assert f(0, 1, 8192, 8192, 8192, 8192, 8192) == 0   # the tiles fill the chip
     assert f(0, 1, 128, 128, 64, 64, 128) == 0          # nothing to split
     assert f(0, 1, 0, 128, 64, 64, 128) == 0 and f(2, 1, 128, 128, 64, 64, 128) == 0
+
+
+def test_quantize_refuses_an_out_that_is_no_matrix():
+    class OnDevice:  # what the checks look at, without a device
+        dtype, is_cuda, device = torch.float32, True, torch.device("cuda", 0)
+        shape = (2, 32)
+
+        def dim(self):
+            return 2
+
+        def stride(self):
+            return (32, 1)
+
+    with pytest.raises(ValueError, match="out must be"):
+        rt.quantize_mx(OnDevice(), rt.MX_INT8, out=torch.empty(2, 32, dtype=torch.uint8))
