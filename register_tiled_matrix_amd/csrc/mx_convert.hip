@@ -88,7 +88,7 @@ __device__ __forceinline__ void encode8(const float (&x)[8], int E, uint32_t (&q
 constexpr int CV_NT = 256;
 
 // u / d for u < 2^31 as a product: m = ceil(2^(31 + l) / d) with 2^l >= d > 2^(l - 1) fits 32 bits and
-// errs by less than u / 2^31 / d < 1 / d. Unit indices past 2^31 divide (`m` 0).
+// errs by less than u / 2^31 / d < 1 / d. 64-bit unit indices divide.
 struct RowOf {
     uint32_t m, l;
     template <typename IDX>
