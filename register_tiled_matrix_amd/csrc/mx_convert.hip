@@ -13,6 +13,7 @@
 // that: comparing with the borders of fp4 one by one took 59.7 us where the conversion instruction takes 34.4.
 #include "mx_common.h"
 #include "regtile_internal.h"
+#include "tile_addressing.h"
 
 namespace regtile {
 
@@ -147,7 +148,7 @@ __global__ __launch_bounds__(CV_NT) void mx_dequantize_kernel(int rows, int cols
                                                               int64_t ldq, const uint8_t *__restrict__ S, int64_t lds,
                                                               char *__restrict__ X, int64_t ldx, RowOf row_of_unit) {
     constexpr int ES = DT == 0 ? 4 : 2;
-    const IDX per_row = (IDX)((cols + 7) / 8), total = per_row * (IDX)rows;
+    const IDX per_row = (IDX)addr::mx_units(cols), total = per_row * (IDX)rows;
     for (IDX u = (IDX)blockIdx.x * CV_NT + threadIdx.x; u < total; u += (IDX)gridDim.x * CV_NT) {
         const IDX row = row_of_unit(u, per_row);
         const int64_t unit = (int64_t)(u - row * per_row);
@@ -213,8 +214,8 @@ hipError_t quantize_cfg(const MxConvert &p, hipStream_t s) {
 
 template <bool FP4, int DT>
 hipError_t dequantize_cfg(const MxConvert &p, hipStream_t s) {
-    const int64_t units = ((int64_t)p.cols + 7) / 8 * p.rows;
-    const RowOf r = row_of(((int64_t)p.cols + 7) / 8);
+    const int64_t units = addr::mx_units(p.cols) * p.rows;
+    const RowOf r = row_of(addr::mx_units(p.cols));
 #define REGTILE_MX_D(IDX_)                                                                                          \
     do {                                                                                                            \
         note_launch(reinterpret_cast<const void *>(&mx_dequantize_kernel<FP4, DT, IDX_>), CV_NT);                    \

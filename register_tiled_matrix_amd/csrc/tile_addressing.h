@@ -189,6 +189,9 @@ REGTILE_HD bool mx_dma_takes(bool ta, bool tb, int M, int N, int K, int64_t lda,
     return ta ? runs_fit(M, lda, 8) && ((int64_t)K + 64) * lda * 2 + 512 < lim
               : K % 8 == 0 && lda % 8 == 0 && t * lda * 2 < lim;
 }
+// Units of 8 columns in a row of the conversion kernels, in 64 bits: cols goes up to 2^31 - 1. The
+// launch and the kernel both count with it.
+REGTILE_HD int64_t mx_units(int64_t cols) { return (cols + 7) / 8; }
 // The register-staged kernel's gather of an M/N-contiguous operand with `cols` columns goes
 // through a per-slab descriptor (8-byte runs) when this holds, else through predicated loads.
 REGTILE_HD bool gather_desc_takes(int64_t cols, int64_t ld) { return runs_fit(cols, ld, 4); }

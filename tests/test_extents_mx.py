@@ -1,0 +1,41 @@
+"""Sizes and extents of the block-scaled kernels, checked on the CPU through the functions that the
+kernels and their launchers call (csrc/tile_addressing.h; `extent_check_mx.cpp`)."""
+from __future__ import annotations
+
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+SRC = os.path.join(ROOT, "tests", "extent_check_mx.cpp")
+CSRC = os.path.join(ROOT, "register_tiled_matrix_amd", "csrc")
+
+
+@pytest.fixture(scope="module")
+def checker(tmp_path_factory):
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("g++ not available")
+    out = str(tmp_path_factory.mktemp("extent_mx") / "extent_check_mx")
+    subprocess.run([gxx, "-O2", "-std=c++17", "-Wall", "-Werror", "-Wno-unused-function", f"-I{CSRC}", SRC, "-o", out],
+                   check=True, capture_output=True, text=True)
+    return out
+
+
+def _run(exe, *args):
+    r = subprocess.run([exe, *map(str, args)], capture_output=True, text=True, timeout=300)
+    return r.returncode, r.stdout
+
+
+@pytest.mark.parametrize("cols", [1, 7, 8, 9, 777, 2**31 - 9, 2**31 - 8, 2**31 - 7, 2**31 - 1])
+def test_units_of_a_converted_row(checker, cols):
+    rc, out = _run(checker, "units", cols)
+    assert rc == 0 and out == f"{-(-cols // 8)} units\n", out
+
+
+def test_kernel_and_launch_count_units_alike():
+    # nothing in the conversions rounds columns up to units by itself
+    text = open(os.path.join(CSRC, "mx_convert.hip")).read()
+    assert "+ 7) / 8" not in text and text.count("addr::mx_units(") == 3
