@@ -82,7 +82,7 @@ __global__ __launch_bounds__(MXT_NT *KS, KS == 1 ? 2 : 4) void mx_mfma_kernel(in
         constexpr int PF = T == 128 ? 1 : 2;  // register sets: slabs loaded ahead
     uint32_t ra[PF][JA][4], rq[PF][JB][HB / 4], rs[PF][JB];
     const int a_cols = A_K ? K : M, b_cols = B_K ? K : N;
-    const int b_bytes = FP4 ? (b_cols + 1) / 2 : b_cols;
+    const int b_bytes = (int)mx::row_bytes(FP4, b_cols);
     auto load_edge = [&](int64_t slab, int set) {
         const int64_t k0 = slab * MXT_BK;
 #pragma unroll

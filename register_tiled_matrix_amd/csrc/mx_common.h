@@ -15,13 +15,15 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "tile_addressing.h"
+
 namespace regtile {
 namespace mx {
 
 constexpr int GROUP = 32;
 
 __host__ __device__ inline int64_t groups(int64_t cols) { return (cols + GROUP - 1) / GROUP; }
-__host__ __device__ inline int64_t row_bytes(bool fp4, int64_t cols) { return fp4 ? (cols + 1) / 2 : cols; }
+__host__ __device__ inline int64_t row_bytes(bool fp4, int64_t cols) { return addr::mx_row_bytes(fp4, cols); }
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));

@@ -13,7 +13,6 @@
 // that: comparing with the borders of fp4 one by one took 59.7 us where the conversion instruction takes 34.4.
 #include "mx_common.h"
 #include "regtile_internal.h"
-#include "tile_addressing.h"
 
 namespace regtile {
 

@@ -189,8 +189,9 @@ REGTILE_HD bool mx_dma_takes(bool ta, bool tb, int M, int N, int K, int64_t lda,
     return ta ? runs_fit(M, lda, 8) && ((int64_t)K + 64) * lda * 2 + 512 < lim
               : K % 8 == 0 && lda % 8 == 0 && t * lda * 2 < lim;
 }
-// Units of 8 columns in a row of the conversion kernels, in 64 bits: cols goes up to 2^31 - 1. The
-// launch and the kernel both count with it.
+// Bytes of a block-scaled row's codes, and units of 8 columns in a row of the conversion kernels, in 64
+// bits: cols goes up to 2^31 - 1. Argument checks, launches and kernels all count with these.
+REGTILE_HD int64_t mx_row_bytes(bool fp4, int64_t cols) { return fp4 ? (cols + 1) / 2 : cols; }
 REGTILE_HD int64_t mx_units(int64_t cols) { return (cols + 7) / 8; }
 // The register-staged kernel's gather of an M/N-contiguous operand with `cols` columns goes
 // through a per-slab descriptor (8-byte runs) when this holds, else through predicated loads.

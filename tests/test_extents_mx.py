@@ -39,3 +39,16 @@ def test_kernel_and_launch_count_units_alike():
     # nothing in the conversions rounds columns up to units by itself
     text = open(os.path.join(CSRC, "mx_convert.hip")).read()
     assert "+ 7) / 8" not in text and text.count("addr::mx_units(") == 3
+
+
+@pytest.mark.parametrize("fp4", [0, 1])
+@pytest.mark.parametrize("cols", [1, 2, 33, 2**31 - 2, 2**31 - 1])
+def test_bytes_of_a_row_of_codes(checker, fp4, cols):
+    rc, out = _run(checker, "bytes", fp4, cols)
+    assert rc == 0 and out == f"{-(-cols // 2) if fp4 else cols} bytes\n", out
+
+
+@pytest.mark.parametrize("source", sorted(n for n in os.listdir(CSRC) if "mx_" in n and n.endswith(".hip")))
+def test_no_kernel_rounds_a_row_up_in_32_bits(source):
+    # cols + 1 passes 2^31 at the widest rows; the sizes come from the functions above
+    assert "cols + 1) / 2" not in open(os.path.join(CSRC, source)).read()
