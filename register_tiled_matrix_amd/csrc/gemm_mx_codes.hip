@@ -276,7 +276,7 @@ bool launch_mx_codes(const MxProblem &p, hipStream_t s, const char **name, hipEr
     if (!p.fp4 || p.ta || !p.tb || p.K % 128 != 0 || !mx_rows_aligned(p) ||
         !addr::mx_dma_takes(false, true, p.M, p.N, p.K, p.lda, p.ldc))
         return false;
-    const int parts = mx_wide_parts(p.M, p.N, p.K);
+    const int parts = addr::mx_wide_parts(p.ta, p.M, p.N, p.K, p.lda);
     const bool wide = parts > 1 && mx_fit_splits(p, p.K / 128) == parts;
     const bool small = !wide && addr::dma_tile(p.M, p.N) == 128;
     const int splits = wide || (small && parts == 1) ? mx_fit_splits(p, p.K / 128) : 1;

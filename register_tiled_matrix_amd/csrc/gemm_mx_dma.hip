@@ -416,19 +416,14 @@ hipError_t launch_mx_join(const MxProblem &p, hipStream_t s, int splits) {
 // of at least 512 k, and none where the tiles do that. us by number of parts, fp4 / int8, 128-wide:
 // tn 1024 x 1024 x 16384: 1 315, 2 163, 4 88, 8 57, 16 66; nn 1024 x 1024 x 4096: 1 68, 2 40, 4 30, 6 27,
 // 8 29, 16 35; nt 1024 x 1024 x 1024: 1 15.7, 2 16.8, 4 18.8.
-// Between 33 and 128 tiles of 256x256 with K from 8192 on, those tiles in parts that fill the chip (one
-// workgroup to a CU) rather than whole 128-wide ones: tn int8 2048 x 4096 x 8192 157 us, 181; 2048 x 2048 x
+// Between 33 and 128 tiles of 256x256 with K from 8192 on, those tiles in parts that fill the chip
+// (addr::mx_wide_parts) rather than whole 128-wide ones: tn int8 2048 x 4096 x 8192 157 us, 181; 2048 x 2048 x
 // 8192 89, 98; tn fp4 1024 x 4096 x 16384 136, 164; nt fp4 1024 x 8192 x 8192 130, 135. (K = 4096: 92, 89 at
 // tn int8 2048 x 4096; 32 tiles: 57.6, 55.3 at 1024 x 2048 x 8192.)
-int mx_wide_parts(int M, int N, int K) {
-    const int64_t tiles = (int64_t)((M + 255) / 256) * ((N + 255) / 256);
-    return K >= 8192 && tiles > 32 && tiles <= 128 ? (int)(256 / tiles) : 1;
-}
-
 int mx_splits(bool ta, bool tb, int M, int N, int K, int64_t lda, int64_t ldc) {
     const bool sk = !ta && tb && mx_splitk_preferred(M, N, K);
     if (!sk && !addr::mx_dma_takes(ta, tb, M, N, K, lda, ldc)) return 1;
-    if (!sk && mx_wide_parts(M, N, K) > 1) return mx_wide_parts(M, N, K);
+    if (const int wide = addr::mx_wide_parts(ta, M, N, K, lda); !sk && wide > 1) return wide;
     const int64_t t = sk ? 64 : 128, tiles = ((M + t - 1) / t) * ((N + t - 1) / t);
     const int64_t want = (sk ? 256 : 512) / tiles, most = K / 512;  // workgroups: what LDS lets run at once
     if (!sk && tiles > 128) return 1;
@@ -451,7 +446,7 @@ int mx_fit_splits(const MxProblem &p, int slabs) {
 // returns false, launching nothing, for any other.
 bool launch_mx_dma(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err) {
     if (!addr::mx_dma_takes(p.ta, p.tb, p.M, p.N, p.K, p.lda, p.ldc) || !aligned16(p.A)) return false;
-    const int slabs = (p.K + MXD_BK - 1) / MXD_BK, parts = mx_wide_parts(p.M, p.N, p.K);
+    const int slabs = (p.K + MXD_BK - 1) / MXD_BK, parts = addr::mx_wide_parts(p.ta, p.M, p.N, p.K, p.lda);
     const bool wide = parts > 1 && mx_fit_splits(p, slabs) == parts;
     const int t = wide ? 256 : addr::dma_tile(p.M, p.N);
     const int splits = wide || (t == 128 && parts == 1) ? mx_fit_splits(p, slabs) : 1;

@@ -109,7 +109,6 @@ bool launch_mx_codes(const MxProblem &p, hipStream_t s, const char **name, hipEr
 // Parts of k that the DMA and split-K kernels make of a product when they are given a workspace of one
 // M x N fp32 matrix for each (1: they make no use of one). `aligned`: mx_rows_aligned.
 int mx_splits(bool ta, bool tb, int M, int N, int K, int64_t lda, int64_t ldc);
-int mx_wide_parts(int M, int N, int K);
 // The parts that the workspace of `p` has room for, each with at least one of the `slabs`.
 int mx_fit_splits(const MxProblem &p, int slabs);
 // Where a launch of `splits` parts writes: C itself, or the workspace's M x N parts, unscaled.

@@ -189,6 +189,16 @@ REGTILE_HD bool mx_dma_takes(bool ta, bool tb, int M, int N, int K, int64_t lda,
     return ta ? runs_fit(M, lda, 8) && ((int64_t)K + 64) * lda * 2 + 512 < lim
               : K % 8 == 0 && lda % 8 == 0 && t * lda * 2 < lim;
 }
+// 256-wide tiles in parts of k for the problems that mx_dma_takes with 33 to 128 such tiles and a long K
+// (gemm_mx_dma.hip has the measurements): the number of parts, which fill the chip with one workgroup to a
+// CU, or 1 where the problem does not go that way. mx_dma_takes has checked the descriptors of 128-wide
+// tiles here, so a K-contiguous A has to keep 256 of its rows below 2^31 bytes as well (the parts'
+// outputs are M x N).
+REGTILE_HD int mx_wide_parts(bool ta, int M, int N, int K, int64_t lda) {
+    const int64_t tiles = (((int64_t)M + 255) / 256) * (((int64_t)N + 255) / 256);
+    if (K < 8192 || tiles <= 32 || tiles > 128 || (!ta && 256 * lda * 2 >= int64_t(1) << 31)) return 1;
+    return (int)(256 / tiles);
+}
 // Bytes of a block-scaled row's codes, and units of 8 columns in a row of the conversion kernels, in 64
 // bits: cols goes up to 2^31 - 1. Argument checks, launches and kernels all count with these.
 REGTILE_HD int64_t mx_row_bytes(bool fp4, int64_t cols) { return fp4 ? (cols + 1) / 2 : cols; }

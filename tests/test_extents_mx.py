@@ -52,3 +52,32 @@ def test_bytes_of_a_row_of_codes(checker, fp4, cols):
 def test_no_kernel_rounds_a_row_up_in_32_bits(source):
     # cols + 1 passes 2^31 at the widest rows; the sizes come from the functions above
     assert "cols + 1) / 2" not in open(os.path.join(CSRC, source)).read()
+
+
+# (order, M, N, K, lda, ldc); 256-wide tiles in parts where 33 to 128 of them meet K >= 8192
+WIDE = [
+    ("nt", 300, 8448, 8288, 8288, 8448),
+    ("nt", 300, 8448, 8288, 2**22 - 8, 8448),        # the longest rows that leave 256 of them below 2^31 bytes
+    ("nt", 300, 8448, 8288, 5 * 2**20, 8448),        # 128-wide tiles from there on
+    ("nn", 300, 8448, 8296, 2**23 - 8, 8448),
+    ("tn", 1040, 1824, 8288, 1040, 1824),
+    ("tt", 1040, 1824, 8288, 1048, 1830),
+]
+
+
+@pytest.mark.parametrize("case", WIDE, ids=lambda c: "-".join(map(str, c)))
+def test_descriptor_accesses_stay_inside_the_operands(checker, case):
+    rc, out = _run(checker, "one", *case)
+    assert rc == 0 and out.startswith("taken 1 "), out
+
+
+@pytest.mark.parametrize("case", WIDE[2:4], ids=lambda c: "-".join(map(str, c)))
+def test_wide_tiles_do_not_reach_that_far(checker, case):
+    # why these stay on 128-wide tiles: the offsets that stand for "past K" wrap on 256-wide ones
+    rc, out = _run(checker, "force", *case)
+    assert rc == 1 and "wraps past 2^32" in out, out
+
+
+def test_seeded_sweep(checker):
+    rc, out = _run(checker, "sweep", 20261206, 120)
+    assert rc == 0 and int(out.split()[1]) > 20, out

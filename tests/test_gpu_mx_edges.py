@@ -22,6 +22,36 @@ def _device():
     torch.cuda.empty_cache()
 
 
+def dev_rows(x, row, fill):
+    """`x` on the GPU with rows that start `row` elements apart, `fill` behind them."""
+    x = torch.as_tensor(x)
+    full = torch.full((x.shape[0], row), fill, dtype=x.dtype, device="cuda")
+    full[:, :x.shape[1]] = x.cuda()
+    return full[:, :x.shape[1]]
+
+
+def random_matrix(rng, fmt, rows, cols, aligned=True):
+    """(MXMatrix, its values in 64 bits on the GPU); rows aligned for DMA, or close together."""
+    w, g = mx.widths(fmt, cols)
+    codes = rng.integers(0, 256, (rows, w), dtype=np.uint8)
+    scales = rng.integers(120, 131, (rows, g)).astype(np.uint8)
+    B = rt.MXMatrix(fmt, dev_rows(codes, -(-w // 16) * 16 if aligned else w, 255),
+                    dev_rows(scales, -(-g // 4) * 4 if aligned else g, 255), cols)
+    return B, torch.from_numpy(mx.decode(codes, scales, fmt, cols)).cuda()
+
+
+def assert_close(C, a, b, what, alpha=1.0, beta=0.0, C0=None):
+    """Within 1e-5 of the sum of the magnitudes that an output is made of: the library's bound for fp32 sums
+    of exact products. a and b are in 64 bits."""
+    a, b = a.contiguous(), b.contiguous()
+    ref, mag = alpha * (a @ b), abs(alpha) * (a.abs() @ b.abs())
+    if beta:
+        ref, mag = ref + beta * C0.double(), mag + (beta * C0.double()).abs()
+    assert bool(C.isfinite().all()), what
+    worst = ((C.double() - ref).abs() / (1e-5 * mag).clamp(min=1e-30)).max()
+    assert float(worst) <= 1.0, f"{what}: |err| / bound {float(worst):.3g}"
+
+
 @pytest.mark.parametrize("cols", [2**31 - 1, 2**31 - 7])
 def test_dequantize_the_widest_rows(cols):
     """One row of as many columns as an int holds, where rounding up to whole units passes it: every value,
@@ -45,3 +75,18 @@ def test_dequantize_the_widest_rows(cols):
         scale = torch.exp2(S[0, c // 32:-(-(c + n) // 32)].float() - 133)
         want = (Q[0, c:c + n].view(torch.int8).float() * scale.repeat_interleave(32)[:n]).to(torch.bfloat16)
         assert torch.equal(X[0, c:c + n], want), c
+
+
+@pytest.mark.parametrize("fmt,order", [(mx.FP4, "nt"), (mx.INT8, "nt"), (mx.INT8, "nn")])
+def test_long_k_on_rows_too_far_apart_for_wide_tiles(fmt, order):
+    """256 rows of A pass 2^31 bytes, and what lies behind each of them is NaN."""
+    M, N, K, lda = 300, 8448, 8288, 5 * 2**20
+    if torch.cuda.mem_get_info()[0] < 20 << 30:
+        pytest.skip("needs 20 GB of free memory")
+    rng = np.random.default_rng(11)
+    A = dev_rows(torch.from_numpy(rng.standard_normal((M, K))).bfloat16(), lda, float("nan"))
+    B, b = random_matrix(rng, fmt, *((N, K) if order[1] == "t" else (K, N)))
+    announce(f"gemm_mx {fmt} {order} {M}x{N}x{K} lda {lda}")
+    C = rt.gemm_bf16_mx(A, B.t() if order[1] == "t" else B)
+    assert "_dma_128x128" in rt.last_kernel(), rt.last_kernel()
+    assert_close(C, A.double(), b.t() if order[1] == "t" else b, "far rows")
