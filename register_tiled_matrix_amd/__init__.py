@@ -426,7 +426,8 @@ class _Launch:
         if stream is None:
             stream = torch.cuda.current_stream(device)
         elif isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=device)
+            # (an ExternalStream of handle 0 would be another stream than the default one)
+            stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the operands on {device}")
         self._device, self._stream = torch.cuda.device(device), torch.cuda.stream(stream)

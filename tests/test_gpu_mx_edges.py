@@ -90,3 +90,30 @@ def test_long_k_on_rows_too_far_apart_for_wide_tiles(fmt, order):
     C = rt.gemm_bf16_mx(A, B.t() if order[1] == "t" else B)
     assert "_dma_128x128" in rt.last_kernel(), rt.last_kernel()
     assert_close(C, A.double(), b.t() if order[1] == "t" else b, "far rows")
+
+
+def test_handle_of_the_default_stream():
+    """Handle 0 is the default stream, as in the other entry points: work queued there before a call has run
+    before it, work queued after it waits for it."""
+    default = torch.cuda.default_stream()
+    assert default.cuda_stream == 0
+    with rt._Launch(torch.device("cuda", 0), 0) as handle:
+        assert handle == 0 and torch.cuda.current_stream() == default
+    spin = torch.randn(4096, 4096, device="cuda")
+    x = torch.zeros(64, 2048, device="cuda", dtype=torch.bfloat16)
+    W = rt.quantize_mx(torch.randn(512, 2048, device="cuda"), rt.MX_FP4)
+    new = torch.randn(64, 2048, device="cuda", dtype=torch.bfloat16)
+    want, kept = rt.gemm_bf16_mx(new, W.t()), rt.quantize_mx(new, rt.MX_INT8)
+    back = rt.dequantize_mx(kept)
+    torch.cuda.synchronize()
+    for _ in range(4):
+        x.zero_()
+        for _ in range(8):
+            spin = spin @ spin * 1e-3  # keeps the default stream busy while the calls below are queued
+        x.copy_(new)
+        y = rt.gemm_bf16_mx(x, W.t(), stream=0).clone()
+        q = rt.quantize_mx(x, rt.MX_INT8, stream=0)
+        d = rt.dequantize_mx(q, stream=0).clone()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(d, back)
+        assert torch.equal(q.codes, kept.codes) and torch.equal(q.scales, kept.scales)
