@@ -117,3 +117,45 @@ def test_handle_of_the_default_stream():
         torch.cuda.synchronize()
         assert torch.equal(y, want) and torch.equal(d, back)
         assert torch.equal(q.codes, kept.codes) and torch.equal(q.scales, kept.scales)
+
+
+def run_with_workspace(dtype, A, B, C, alpha, beta, work, parts):
+    """The C call with a workspace of `parts` M x N parts at the start of `work` (0: none)."""
+    ta = A.stride(0) == 1 and A.shape[0] > 1
+    (M, K), N = A.shape, B.shape[1]
+    fn = rt.regtile_gemm_bf16_mx if dtype == torch.bfloat16 else rt.regtile_gemm_f16_mx
+    assert fn(B.format, int(ta), int(B.transposed), M, N, K, alpha, A.data_ptr(), A.stride(1 if ta else 0), B.codes.data_ptr(),
+              B.codes.stride(0), B.scales.data_ptr(), B.scales.stride(0), beta, C.data_ptr(), C.stride(0),
+              work.data_ptr() if parts else 0, parts * M * N * 4, torch.cuda.current_stream().cuda_stream) == 0
+
+
+# (M, N, K, tile, parts): the last part shorter than the others in both
+@pytest.mark.parametrize("M,N,K,tile,parts", [(1000, 1000, 129 * 128, 128, 8), (1040, 1824, 65 * 128, 256, 6)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_codes_in_lds_in_parts_of_k(dtype, M, N, K, tile, parts):
+    """K split over workgroups where B stays in codes in LDS: the parts that the binding asks for, fewer (which
+    256-wide tiles do not make), and none."""
+    rng = np.random.default_rng(M + N)
+    A = torch.from_numpy(rng.standard_normal((M, K))).to(dtype).cuda()
+    B, b = random_matrix(rng, mx.FP4, N, K)
+    C0 = torch.randn(M, N + 4, device="cuda")
+    announce(f"gemm_mx fp4 nt {M}x{N}x{K} {dtype} in parts")
+    assert rt.regtile_gemm_mx_workspace(0, 1, M, N, K, K, N + 4) == parts * M * N * 4
+    gemm = rt.gemm_bf16_mx if dtype == torch.bfloat16 else rt.gemm_f16_mx
+    full = C0.clone()
+    C = gemm(A, B.t(), full[:, :N], alpha=-0.5, beta=2.0)
+    assert f"_codes_{tile}x{tile}" in rt.last_kernel(), rt.last_kernel()
+    assert torch.equal(full[:, N:], C0[:, N:])
+    a = A.double()
+    assert_close(C, a, b.t(), "binding", -0.5, 2.0, C0[:, :N])
+    work = torch.empty(parts * M * N + 64, device="cuda")
+    for n in (0, 1, 3, parts):
+        work.fill_(float("nan"))
+        D = C0[:, :N].contiguous()
+        run_with_workspace(dtype, A, B.t(), D, -0.5, 2.0, work, n)
+        narrow = tile == 128 or n < parts
+        assert ("_codes_128x128" if narrow else "_codes_256x256") in rt.last_kernel(), (n, rt.last_kernel())
+        assert_close(D, a, b.t(), f"{n} parts", -0.5, 2.0, C0[:, :N])
+        assert bool(work[max(n, 1) * M * N:].isnan().all())
+        if n == parts:
+            assert torch.equal(D, C)
