@@ -236,10 +236,13 @@ int regtile_dequantize_mx(int format, int dtype, int rows, int cols, const uint8
  *   work, work_bytes (17-18) a workspace, or NULL and 0: device memory, 16-byte aligned, that nothing
  *            else uses until the call has run. Products with few output tiles and a long K use it to
  *            spread K over more of the chip, one M x N fp32 part for each split; with less than
- *            regtile_gemm_mx_workspace() bytes they make fewer splits. Its contents need no
+ *            regtile_gemm_mx_workspace_ex() bytes they make fewer splits. Its contents need no
  *            preparation and mean nothing afterwards.
  *   stream   (arg 19)
- * regtile_gemm_mx_workspace -- the bytes that such a call makes use of, 0 for most.
+ * regtile_gemm_mx_workspace -- the most bytes that such a call of these sizes makes use of, whatever its
+ * format and its operands' alignment; 0 for most sizes, and wherever K is below 1024.
+ * regtile_gemm_mx_workspace_ex -- the bytes that the call with exactly these arguments makes use of (of
+ * pointers the alignment counts; nothing is read).
  * Every output is summed in a fixed order: repeated calls (with the same workspace size) give
  * identical bits.
  */
@@ -250,6 +253,9 @@ int regtile_gemm_f16_mx(int format, int trans_a, int trans_b, int M, int N, int 
                         const uint16_t *A, int lda, const uint8_t *Q, int ldq, const uint8_t *S,
                         int lds, float beta, float *C, int ldc, void *work, int64_t work_bytes, void *stream);
 int64_t regtile_gemm_mx_workspace(int trans_a, int trans_b, int M, int N, int K, int lda, int ldc);
+int64_t regtile_gemm_mx_workspace_ex(int format, int trans_a, int trans_b, int M, int N, int K,
+                                     const uint16_t *A, int lda, const uint8_t *Q, int ldq,
+                                     const uint8_t *S, int lds, int ldc);
 
 /* Name of the kernel the calling thread launched last ("none" before the first launch,
  * "quick-return" when nothing was launched). Static storage; do not free. */

@@ -47,7 +47,7 @@ __all__ = [
     "regtile_gemm_f32_ex", "regtile_gemm_bf16_ex", "regtile_gemm_f16_ex",
     "MX_FP4", "MX_INT8", "MX_GROUP", "MXMatrix", "quantize_mx", "dequantize_mx", "gemm_bf16_mx", "gemm_f16_mx",
     "regtile_quantize_mx", "regtile_dequantize_mx", "regtile_gemm_bf16_mx", "regtile_gemm_f16_mx",
-    "regtile_gemm_mx_workspace", "last_kernel", "last_kernel_info", "strerror", "version", "EXPORTED_SYMBOLS",
+    "regtile_gemm_mx_workspace", "regtile_gemm_mx_workspace_ex", "last_kernel", "last_kernel_info", "strerror", "version", "EXPORTED_SYMBOLS",
 ]
 
 ALGO_F32_AUTO, ALGO_F32_NAIVE, ALGO_F32_LDS, ALGO_F32_REGTILE, ALGO_F32_SPLITK = 0, 1, 2, 3, 4
@@ -60,7 +60,7 @@ EXPORTED_SYMBOLS = ("gemm_f32", "gemm_bf16", "gemm_f16", "regtile_gemm_f32_algo"
                     "regtile_gemm_bf16_algo", "regtile_gemm_f16_algo", "regtile_gemm_f32_ex",
                     "regtile_gemm_bf16_ex", "regtile_gemm_f16_ex",
                     "regtile_quantize_mx", "regtile_dequantize_mx", "regtile_gemm_bf16_mx",
-                    "regtile_gemm_f16_mx", "regtile_gemm_mx_workspace",
+                    "regtile_gemm_f16_mx", "regtile_gemm_mx_workspace", "regtile_gemm_mx_workspace_ex",
                     "regtile_last_kernel", "regtile_last_kernel_info", "regtile_strerror",
                     "regtile_version")
 
@@ -119,6 +119,8 @@ def load():
             f.restype = I
         lib.regtile_gemm_mx_workspace.argtypes = [I] * 7
         lib.regtile_gemm_mx_workspace.restype = ctypes.c_int64
+        lib.regtile_gemm_mx_workspace_ex.argtypes = [I, I, I, I, I, I, P, I, P, I, P, I, I]
+        lib.regtile_gemm_mx_workspace_ex.restype = ctypes.c_int64
         lib.regtile_last_kernel.argtypes = []
         lib.regtile_last_kernel.restype = ctypes.c_char_p
         lib.regtile_last_kernel_info.argtypes = [ctypes.POINTER(KernelInfo)]
@@ -215,6 +217,10 @@ def regtile_gemm_f16_mx(format, trans_a, trans_b, M, N, K, alpha, A, lda, Q, ldq
 
 def regtile_gemm_mx_workspace(trans_a, trans_b, M, N, K, lda, ldc) -> int:
     return load().regtile_gemm_mx_workspace(trans_a, trans_b, M, N, K, lda, ldc)
+
+
+def regtile_gemm_mx_workspace_ex(format, trans_a, trans_b, M, N, K, A, lda, Q, ldq, S, lds, ldc) -> int:
+    return load().regtile_gemm_mx_workspace_ex(format, trans_a, trans_b, M, N, K, A, lda, Q, ldq, S, lds, ldc)
 
 
 def regtile_quantize_mx(format, dtype, rows, cols, X, ldx, Q, ldq, S, lds, stream=0) -> int:
@@ -550,14 +556,15 @@ def _run_gemm_mx(name, A, ta, lda, B, tb, M, N, K, C, ldc, alpha, beta, handle):
     lib = _lib or load()
     if C is None:
         C = A.new_empty((M, N), dtype=_torch.float32)
+    a, q, s = A.data_ptr(), B.codes.data_ptr(), B.scales.data_ptr()
     work, at, size = None, None, 0
-    if M > 64:  # fewer rows never use a workspace
-        size = lib.regtile_gemm_mx_workspace(ta, tb, M, N, K, lda, ldc)
+    if M > 64 and K >= 1024:  # (no part is shorter than 512 k)
+        size = lib.regtile_gemm_mx_workspace_ex(B.format, ta, tb, M, N, K, a, lda, q, B._ldq, s, B._lds, ldc)
         if size > 0:
             work = A.new_empty(size, dtype=_torch.uint8)  # stays until the launch is queued
             at = work.data_ptr()
-    status = getattr(lib, name)(B.format, ta, tb, M, N, K, alpha, A.data_ptr(), lda, B.codes.data_ptr(), B._ldq,
-                                B.scales.data_ptr(), B._lds, beta, C.data_ptr(), ldc, at, size, handle)
+    status = getattr(lib, name)(B.format, ta, tb, M, N, K, alpha, a, lda, q, B._ldq, s, B._lds, beta, C.data_ptr(), ldc,
+                                at, size, handle)
     if status:
         _check(status)
     return C

@@ -269,25 +269,20 @@ hipError_t launch_codes(const MxProblem &p, hipStream_t s, int splits) {
 
 }  // namespace
 
-// Takes (and launches, status in *err) fp4 products that the DMA kernel would run, with B stored N x K,
-// rows aligned for the DMA (mx_rows_aligned) and K in whole units; returns false, launching nothing, for
-// any other.
-bool launch_mx_codes(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err) {
-    if (!p.fp4 || p.ta || !p.tb || p.K % 128 != 0 || !mx_rows_aligned(p) ||
-        !addr::mx_dma_takes(false, true, p.M, p.N, p.K, p.lda, p.ldc))
-        return false;
-    const int parts = addr::mx_wide_parts(p.ta, p.M, p.N, p.K, p.lda);
-    const bool wide = parts > 1 && mx_fit_splits(p, p.K / 128) == parts;
-    const bool small = !wide && addr::dma_tile(p.M, p.N) == 128;
-    const int splits = wide || (small && parts == 1) ? mx_fit_splits(p, p.K / 128) : 1;
+// fp4 products that the DMA kernel would run, with B stored N x K, rows aligned for the DMA and K in
+// whole units
+bool mx_codes_takes(const MxProblem &p) {
+    return p.fp4 && !p.ta && p.tb && p.K % 128 == 0 && mx_rows_aligned(p) && mx_dma_takes(p);
+}
+
+hipError_t launch_mx_codes(const MxProblem &p, const MxPlan &plan, hipStream_t s, const char **name) {
+    const int splits = mx_fit_parts(p, plan);
+    const bool small = (splits == plan.parts ? plan.tile : plan.narrow) == 128;
     static const char *const names[2][2] = {{"bf16_fp4_codes_256x256x128_nt", "bf16_fp4_codes_128x128x128_nt"},
                                             {"f16_fp4_codes_256x256x128_nt", "f16_fp4_codes_128x128x128_nt"}};
     *name = names[p.f16][small];
-    if (small)
-        *err = p.f16 ? launch_codes<128, true>(p, s, splits) : launch_codes<128, false>(p, s, splits);
-    else
-        *err = p.f16 ? launch_codes<256, true>(p, s, splits) : launch_codes<256, false>(p, s, splits);
-    return true;
+    if (small) return p.f16 ? launch_codes<128, true>(p, s, splits) : launch_codes<128, false>(p, s, splits);
+    return p.f16 ? launch_codes<256, true>(p, s, splits) : launch_codes<256, false>(p, s, splits);
 }
 
 }  // namespace regtile

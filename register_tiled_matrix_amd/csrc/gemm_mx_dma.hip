@@ -412,44 +412,62 @@ hipError_t launch_mx_join(const MxProblem &p, hipStream_t s, int splits) {
     return hipGetLastError();
 }
 
-// Enough parts to fill the chip (two 128-wide workgroups, or one of the split-K kernel's, to a CU), each
-// of at least 512 k, and none where the tiles do that. us by number of parts, fp4 / int8, 128-wide:
+// How many parts of k: enough to fill the chip (two 128-wide workgroups, or one of the split-K kernel's,
+// to a CU), each of at least 512 k, and none where the tiles do that. us by number of parts, fp4 / int8, 128-wide:
 // tn 1024 x 1024 x 16384: 1 315, 2 163, 4 88, 8 57, 16 66; nn 1024 x 1024 x 4096: 1 68, 2 40, 4 30, 6 27,
 // 8 29, 16 35; nt 1024 x 1024 x 1024: 1 15.7, 2 16.8, 4 18.8.
 // Between 33 and 128 tiles of 256x256 with K from 8192 on, those tiles in parts that fill the chip
 // (addr::mx_wide_parts) rather than whole 128-wide ones: tn int8 2048 x 4096 x 8192 157 us, 181; 2048 x 2048 x
 // 8192 89, 98; tn fp4 1024 x 4096 x 16384 136, 164; nt fp4 1024 x 8192 x 8192 130, 135. (K = 4096: 92, 89 at
 // tn int8 2048 x 4096; 32 tiles: 57.6, 55.3 at 1024 x 2048 x 8192.)
-int mx_splits(bool ta, bool tb, int M, int N, int K, int64_t lda, int64_t ldc) {
-    const bool sk = !ta && tb && mx_splitk_preferred(M, N, K);
-    if (!sk && !addr::mx_dma_takes(ta, tb, M, N, K, lda, ldc)) return 1;
-    if (const int wide = addr::mx_wide_parts(ta, M, N, K, lda); !sk && wide > 1) return wide;
-    const int64_t t = sk ? 64 : 128, tiles = ((M + t - 1) / t) * ((N + t - 1) / t);
-    const int64_t want = (sk ? 256 : 512) / tiles, most = K / 512;  // workgroups: what LDS lets run at once
-    if (!sk && tiles > 128) return 1;
-    const int64_t n = want < most ? want : most;
+static int parts_of(int64_t tiles, int64_t workgroups, int K) {
+    const int64_t want = workgroups / tiles, most = K / 512, n = want < most ? want : most;
     return n < 1 ? 1 : n > 16 ? 16 : (int)n;
 }
 
-int mx_fit_splits(const MxProblem &p, int slabs) {
-    int64_t n = mx_splits(p.ta, p.tb, p.M, p.N, p.K, p.lda, p.ldc);
-    const int64_t room = p.work_bytes / ((int64_t)p.M * p.N * 4);
-    if (n > room) n = room;
-    if (n > slabs) n = slabs;
-    if (n < 1) return 1;
-    const int64_t per = (slabs + n - 1) / n;
-    return (int)((slabs + per - 1) / per);
+MxPlan mx_plan(const MxProblem &p) {
+    if (mx_token_takes(p)) return {MxPlan::TOKEN, 0, 0, 1, 1};
+    auto tiles = [&](int64_t t) { return ((p.M + t - 1) / t) * ((p.N + t - 1) / t); };
+    MxPlan plan = {MxPlan::MFMA, 0, 0, 1, 1};
+    if (mx_splitk_takes(p)) {
+        plan = {MxPlan::SPLITK, 64, 64, parts_of(tiles(64), 256, p.K), (p.K + 127) / 128};
+    } else if (mx_dma_takes(p)) {
+        const bool codes = mx_codes_takes(p);
+        plan.kernel = codes ? MxPlan::CODES : MxPlan::DMA;
+        plan.slabs = codes ? p.K / 128 : (p.K + MXD_BK - 1) / MXD_BK;
+        plan.tile = plan.narrow = addr::dma_tile(p.M, p.N);
+        const int wide = addr::mx_wide_parts(p.ta, p.M, p.N, p.K, p.lda);
+        if (wide > 1) {
+            plan.tile = 256;
+            plan.parts = wide;
+        } else if (plan.tile == 128 && tiles(128) <= 128) {
+            plan.parts = parts_of(tiles(128), 512, p.K);
+        }
+    }
+    // as many as there are when each takes the same number of slabs
+    const int per = (plan.slabs + plan.parts - 1) / plan.parts;
+    plan.parts = (plan.slabs + per - 1) / per;
+    return plan;
 }
 
-// Takes (and launches, status in *err) a problem whose A meets the 16-bit kernels' DMA conditions
-// in its storage order (addr::mx_dma_takes) with 16-byte aligned rows and whose B has whole groups;
-// returns false, launching nothing, for any other.
-bool launch_mx_dma(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err) {
-    if (!addr::mx_dma_takes(p.ta, p.tb, p.M, p.N, p.K, p.lda, p.ldc) || !aligned16(p.A)) return false;
-    const int slabs = (p.K + MXD_BK - 1) / MXD_BK, parts = addr::mx_wide_parts(p.ta, p.M, p.N, p.K, p.lda);
-    const bool wide = parts > 1 && mx_fit_splits(p, slabs) == parts;
-    const int t = wide ? 256 : addr::dma_tile(p.M, p.N);
-    const int splits = wide || (t == 128 && parts == 1) ? mx_fit_splits(p, slabs) : 1;
+int mx_fit_parts(const MxProblem &p, const MxPlan &plan) {
+    if (plan.parts == 1) return 1;
+    const int64_t room = p.work_bytes / ((int64_t)p.M * p.N * 4);
+    if (room >= plan.parts) return plan.parts;
+    if (room < 2 || plan.tile != plan.narrow) return 1;
+    const int per = (plan.slabs + (int)room - 1) / (int)room;
+    return (plan.slabs + per - 1) / per;
+}
+
+// A meets the 16-bit kernels' DMA conditions in its storage order with 16-byte aligned rows, and B has
+// whole groups
+bool mx_dma_takes(const MxProblem &p) {
+    return addr::mx_dma_takes(p.ta, p.tb, p.M, p.N, p.K, p.lda, p.ldc) && aligned16(p.A);
+}
+
+hipError_t launch_mx_dma(const MxProblem &p, const MxPlan &plan, hipStream_t s, const char **name) {
+    const int splits = mx_fit_parts(p, plan);
+    const int t = splits == plan.parts ? plan.tile : plan.narrow;
 #define REGTILE_MXD_NAMES(elt, fmt, t) \
     {{elt "_" fmt "_dma_" t "_nn", elt "_" fmt "_dma_" t "_nt"}, {elt "_" fmt "_dma_" t "_tn", elt "_" fmt "_dma_" t "_tt"}}
 #define REGTILE_MXD_SIZES(elt, fmt) {REGTILE_MXD_NAMES(elt, fmt, "256x256x64"), REGTILE_MXD_NAMES(elt, fmt, "128x128x64")}
@@ -458,11 +476,8 @@ bool launch_mx_dma(const MxProblem &p, hipStream_t s, const char **name, hipErro
 #undef REGTILE_MXD_SIZES
 #undef REGTILE_MXD_NAMES
     *name = names[p.f16][p.fp4][t == 128][p.ta][p.tb];
-    if (p.fp4)
-        *err = p.f16 ? launch_mxd_order<true, true>(p, s, t, splits) : launch_mxd_order<true, false>(p, s, t, splits);
-    else
-        *err = p.f16 ? launch_mxd_order<false, true>(p, s, t, splits) : launch_mxd_order<false, false>(p, s, t, splits);
-    return true;
+    if (p.fp4) return p.f16 ? launch_mxd_order<true, true>(p, s, t, splits) : launch_mxd_order<true, false>(p, s, t, splits);
+    return p.f16 ? launch_mxd_order<false, true>(p, s, t, splits) : launch_mxd_order<false, false>(p, s, t, splits);
 }
 
 }  // namespace regtile

@@ -271,25 +271,19 @@ hipError_t launch_mxs(const MxProblem &p, hipStream_t s, int splits) {
 // A and B from L2 more than 128-wide ones, split over workgroups, lose. us, this kernel against that one
 // (fp4): 1024 x 2048 x 1024 14.9, 21.2; 256 x 4096 x 4096 19.0, 27.1; 1024 x 1024 x 8192 34.0, 33.8;
 // 512 x 8192 x 4096 47.5, 46.6; past it 1024 x 1024 x 16384 62.9, 56.6; 256 x 8192 x 8192 60.9, 53.2.
-bool mx_splitk_preferred(int M, int N, int K) {
-    const int64_t tiles = (((int64_t)M + MXS_T - 1) / MXS_T) * (((int64_t)N + MXS_T - 1) / MXS_T);
-    return M > 64 && K >= 512 && tiles <= 512 && tiles * K <= (int64_t(1) << 21);
+bool mx_splitk_takes(const MxProblem &p) {
+    if (p.ta || !p.tb || !mx_rows_aligned(p)) return false;
+    const int64_t tiles = (((int64_t)p.M + MXS_T - 1) / MXS_T) * (((int64_t)p.N + MXS_T - 1) / MXS_T);
+    return p.M > 64 && p.K >= 512 && tiles <= 512 && tiles * p.K <= (int64_t(1) << 21);
 }
 
-// Takes (and launches, status in *err) products with a row-major A and B stored N x K whose rows are
-// aligned for the DMA (mx_rows_aligned) and that mx_splitk_preferred chooses; returns false,
-// launching nothing, for any other.
-bool launch_mx_splitk(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err) {
-    if (p.ta || !p.tb || !mx_rows_aligned(p) || !mx_splitk_preferred(p.M, p.N, p.K)) return false;
+hipError_t launch_mx_splitk(const MxProblem &p, const MxPlan &plan, hipStream_t s, const char **name) {
     static const char *const names[2][2] = {{"bf16_int8_splitk4_64x64x128", "bf16_fp4_splitk4_64x64x128"},
                                             {"f16_int8_splitk4_64x64x128", "f16_fp4_splitk4_64x64x128"}};
     *name = names[p.f16][p.fp4];
-    const int splits = mx_fit_splits(p, (p.K + MXS_BK - 1) / MXS_BK);
-    if (p.fp4)
-        *err = p.f16 ? launch_mxs<true, true>(p, s, splits) : launch_mxs<true, false>(p, s, splits);
-    else
-        *err = p.f16 ? launch_mxs<false, true>(p, s, splits) : launch_mxs<false, false>(p, s, splits);
-    return true;
+    const int splits = mx_fit_parts(p, plan);
+    if (p.fp4) return p.f16 ? launch_mxs<true, true>(p, s, splits) : launch_mxs<true, false>(p, s, splits);
+    return p.f16 ? launch_mxs<false, true>(p, s, splits) : launch_mxs<false, false>(p, s, splits);
 }
 
 }  // namespace regtile

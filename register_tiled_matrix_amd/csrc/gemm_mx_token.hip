@@ -401,14 +401,16 @@ hipError_t launch_batch_rows(const MxProblem &p, hipStream_t s) {
 
 }  // namespace
 
-// Takes (and launches, status in *err) products of at most 64 rows of A, row-major, with B stored
-// N x K: the register kernel up to 8 rows and, up to 32, where rows are not aligned for the LDS
-// kernel, which takes the others. Returns false, launching nothing, for any other problem.
-bool launch_mx_token(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err) {
+// Products of at most 64 rows of A, row-major, with B stored N x K: the register kernel up to 8 rows
+// and, up to 32, where rows are not aligned for the LDS kernel, which takes the others.
+bool mx_token_takes(const MxProblem &p) {
     // (a launch's threads are counted in 32 bits: at most 512 for 4 rows of B here)
     if (p.ta || !p.tb || p.N >= (1 << 24)) return false;
-    const bool lds = p.M > 8 && p.M <= 64 && mx_rows_aligned(p);
-    if (!lds && p.M > 32) return false;
+    return p.M <= 32 || (p.M <= 64 && mx_rows_aligned(p));
+}
+
+hipError_t launch_mx_token(const MxProblem &p, hipStream_t s, const char **name) {
+    const bool lds = p.M > 8 && mx_rows_aligned(p);
 #define REGTILE_TOKEN_SET(elt, fmt)                                                                            \
     {{elt "_" fmt "_token4", elt "_" fmt "_token8", elt "_" fmt "_token16", elt "_" fmt "_token32"},          \
      {elt "_" fmt "_batch16", elt "_" fmt "_batch32", elt "_" fmt "_batch48", elt "_" fmt "_batch64"}}
@@ -417,15 +419,11 @@ bool launch_mx_token(const MxProblem &p, hipStream_t s, const char **name, hipEr
 #undef REGTILE_TOKEN_SET
     if (lds) {
         *name = names[p.f16][p.fp4][1][(p.M - 1) / 16];
-        *err = p.f16 ? launch_batch_rows<true>(p, s) : launch_batch_rows<false>(p, s);
-        return true;
+        return p.f16 ? launch_batch_rows<true>(p, s) : launch_batch_rows<false>(p, s);
     }
     *name = names[p.f16][p.fp4][0][p.M <= 4 ? 0 : p.M <= 8 ? 1 : p.M <= 16 ? 2 : 3];
-    if (p.fp4)
-        *err = p.f16 ? launch_token_rows<true, true>(p, s) : launch_token_rows<true, false>(p, s);
-    else
-        *err = p.f16 ? launch_token_rows<false, true>(p, s) : launch_token_rows<false, false>(p, s);
-    return true;
+    if (p.fp4) return p.f16 ? launch_token_rows<true, true>(p, s) : launch_token_rows<true, false>(p, s);
+    return p.f16 ? launch_token_rows<false, true>(p, s) : launch_token_rows<false, false>(p, s);
 }
 
 }  // namespace regtile

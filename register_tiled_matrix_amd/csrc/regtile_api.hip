@@ -209,9 +209,14 @@ int run_mx(bool f16, int format, int trans_a, int trans_b, int M, int N, int K, 
         return status;
     const char *name = "none";
     hipError_t err;
-    if (!regtile::launch_mx_token(p, s, &name, &err) && !regtile::launch_mx_splitk(p, s, &name, &err) &&
-        !regtile::launch_mx_codes(p, s, &name, &err) && !regtile::launch_mx_dma(p, s, &name, &err))
-        err = regtile::launch_mx_mfma(p, s, &name);
+    const regtile::MxPlan plan = regtile::mx_plan(p);
+    switch (plan.kernel) {
+        case regtile::MxPlan::TOKEN: err = regtile::launch_mx_token(p, s, &name); break;
+        case regtile::MxPlan::SPLITK: err = regtile::launch_mx_splitk(p, plan, s, &name); break;
+        case regtile::MxPlan::CODES: err = regtile::launch_mx_codes(p, plan, s, &name); break;
+        case regtile::MxPlan::DMA: err = regtile::launch_mx_dma(p, plan, s, &name); break;
+        default: err = regtile::launch_mx_mfma(p, s, &name); break;
+    }
     return finish(err, name);
 }
 
@@ -358,10 +363,35 @@ int regtile_gemm_f16_mx(int format, int trans_a, int trans_b, int M, int N, int 
                   stream);
 }
 
-int64_t regtile_gemm_mx_workspace(int trans_a, int trans_b, int M, int N, int K, int lda, int ldc) {
-    if (bad_flag(trans_a) || bad_flag(trans_b) || M <= 0 || N <= 0 || K <= 0) return 0;
-    const int n = regtile::mx_splits(trans_a != 0, trans_b != 0, M, N, K, lda, ldc);
+int64_t regtile_gemm_mx_workspace_ex(int format, int trans_a, int trans_b, int M, int N, int K, const uint16_t *A, int lda,
+                                     const uint8_t *Q, int ldq, const uint8_t *S, int lds, int ldc) {
+    if (bad_format(format) || bad_flag(trans_a) || bad_flag(trans_b) || M <= 0 || N <= 0 || K <= 0) return 0;
+    regtile::MxProblem p = {};
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.A = A;
+    p.lda = lda;
+    p.Q = Q;
+    p.ldq = ldq;
+    p.S = S;
+    p.lds = lds;
+    p.ldc = ldc;
+    p.ta = trans_a != 0;
+    p.tb = trans_b != 0;
+    p.fp4 = format == REGTILE_MX_FP4;
+    const int n = regtile::mx_plan(p).parts;
     return n > 1 ? (int64_t)n * M * N * 4 : 0;
+}
+
+int64_t regtile_gemm_mx_workspace(int trans_a, int trans_b, int M, int N, int K, int lda, int ldc) {
+    int64_t most = 0;  // over the formats, and B's rows aligned for DMA or not
+    for (int i = 0; i < 4; ++i) {
+        const int64_t n = regtile_gemm_mx_workspace_ex(i & 1 ? REGTILE_MX_FP4 : REGTILE_MX_INT8, trans_a, trans_b, M, N, K,
+                                                       nullptr, lda, nullptr, i & 2 ? 16 : 1, nullptr, i & 2 ? 4 : 1, ldc);
+        most = n > most ? n : most;
+    }
+    return most;
 }
 
 const char *regtile_last_kernel(void) { return g_last_kernel; }

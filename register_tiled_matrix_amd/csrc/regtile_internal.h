@@ -92,25 +92,32 @@ bool launch_bf16_mfma_splitk(const Problem &p, hipStream_t s, const char **name,
 // Block-scaled operands: conversions, and the product on MFMA tiles.
 hipError_t launch_mx_quantize(const MxConvert &p, hipStream_t s, const char **name);
 hipError_t launch_mx_dequantize(const MxConvert &p, hipStream_t s, const char **name);
+// Register-staged tiles: any product
 hipError_t launch_mx_mfma(const MxProblem &p, hipStream_t s, const char **name);
-// The product for a few rows of A (row-major) with B stored N x K; false, launching nothing, for
-// any other problem.
-bool launch_mx_token(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err);
-// The product on DMA-fed tiles for aligned A and whole groups of B (addr::mx_dma_takes); false,
-// launching nothing, for any other problem.
-bool launch_mx_dma(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err);
-// The product of few tiles with a row-major aligned A and B stored N x K, k split over waves; false,
-// launching nothing, for any other problem.
-bool launch_mx_splitk(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err);
-bool mx_splitk_preferred(int M, int N, int K);
-// The fp4 product of a row-major A and B stored N x K, B in codes in LDS; false, launching nothing, for
-// any other problem.
-bool launch_mx_codes(const MxProblem &p, hipStream_t s, const char **name, hipError_t *err);
-// Parts of k that the DMA and split-K kernels make of a product when they are given a workspace of one
-// M x N fp32 matrix for each (1: they make no use of one). `aligned`: mx_rows_aligned.
-int mx_splits(bool ta, bool tb, int M, int N, int K, int64_t lda, int64_t ldc);
-// The parts that the workspace of `p` has room for, each with at least one of the `slabs`.
-int mx_fit_splits(const MxProblem &p, int slabs);
+// How a product runs: which of the kernels below takes it (mx_plan chooses; the launches and the
+// workspace queries follow), and what the DMA, codes and split-K kernels make of a workspace.
+struct MxPlan {
+    enum Kernel { TOKEN, SPLITK, CODES, DMA, MFMA } kernel;
+    int tile;    // tile width, if the workspace holds every part
+    int narrow;  // tile width otherwise; where it differs from `tile`, k is then not split at all
+    int parts;   // of k, one M x N fp32 matrix of workspace for each; 1: no workspace is used
+    int slabs;   // that the parts are made of
+};
+MxPlan mx_plan(const MxProblem &p);
+// The parts that the workspace of `p` has room for
+int mx_fit_parts(const MxProblem &p, const MxPlan &plan);
+// A few rows of A (row-major) with B stored N x K
+bool mx_token_takes(const MxProblem &p);
+hipError_t launch_mx_token(const MxProblem &p, hipStream_t s, const char **name);
+// Few tiles with a row-major aligned A and B stored N x K, k split over waves
+bool mx_splitk_takes(const MxProblem &p);
+hipError_t launch_mx_splitk(const MxProblem &p, const MxPlan &plan, hipStream_t s, const char **name);
+// DMA-fed tiles for aligned A and whole groups of B (addr::mx_dma_takes)
+bool mx_dma_takes(const MxProblem &p);
+hipError_t launch_mx_dma(const MxProblem &p, const MxPlan &plan, hipStream_t s, const char **name);
+// Among those, fp4 with a row-major A and B stored N x K: B in codes in LDS
+bool mx_codes_takes(const MxProblem &p);
+hipError_t launch_mx_codes(const MxProblem &p, const MxPlan &plan, hipStream_t s, const char **name);
 // Where a launch of `splits` parts writes: C itself, or the workspace's M x N parts, unscaled.
 struct MxParts {
     float *C;

@@ -159,3 +159,40 @@ def test_codes_in_lds_in_parts_of_k(dtype, M, N, K, tile, parts):
         assert bool(work[max(n, 1) * M * N:].isnan().all())
         if n == parts:
             assert torch.equal(D, C)
+
+
+def workspace_of(A, B, ldc):
+    """regtile_gemm_mx_workspace_ex of a product's operands."""
+    ta = A.stride(0) == 1 and A.shape[0] > 1
+    (M, K), N = A.shape, B.shape[1]
+    return rt.regtile_gemm_mx_workspace_ex(B.format, int(ta), int(B.transposed), M, N, K, A.data_ptr(), A.stride(1 if ta else 0),
+                                           B.codes.data_ptr(), B.codes.stride(0), B.scales.data_ptr(), B.scales.stride(0), ldc)
+
+
+# (order, M, N, K, rows of codes and scales aligned): few rows of A, 64-wide tiles' sizes on rows that are not
+# aligned for them (90 and 91 scale bytes), and those that split nothing
+IN_PARTS = [("nn", 1, 1024, 4096, True, 8), ("nn", 16, 1024, 8320, False, 15), ("tn", 16, 1024, 4160, True, 8), ("tt", 48, 520, 2880, False, 5),
+            ("nt", 48, 600, 2880, False, 5), ("nt", 256, 1024, 2880, False, 5), ("nt", 130, 264, 2912, False, 5),
+            ("nt", 48, 600, 2944, True, 0), ("nt", 16, 600, 2880, False, 0), ("nt", 256, 4096, 1024, True, 0)]
+
+
+@pytest.mark.parametrize("order,M,N,K,aligned,parts", IN_PARTS)
+@pytest.mark.parametrize("fmt", [mx.FP4, mx.INT8])
+def test_workspace_query_is_what_a_call_uses(fmt, order, M, N, K, aligned, parts):
+    rng = np.random.default_rng(M + N + K)
+    ta, tb = order[0] == "t", order[1] == "t"
+    A = torch.from_numpy(rng.standard_normal((K, M) if ta else (M, K))).bfloat16().cuda()
+    A = A.t() if ta else A
+    B, b = random_matrix(rng, fmt, *((N, K) if tb else (K, N)), aligned)
+    B, b = (B.t(), b.t()) if tb else (B, b)
+    size = workspace_of(A, B, N)
+    assert size % (4 * M * N) == 0
+    n = size // (4 * M * N)
+    assert n == parts
+    for given in {n, n + 3}:
+        work = torch.full(((n + 3) * M * N,), float("nan"), device="cuda")
+        C = torch.empty(M, N, device="cuda")
+        announce(f"gemm_mx {fmt} {order} {M}x{N}x{K}, workspace of {given} parts")
+        run_with_workspace(torch.bfloat16, A, B, C, 1.0, 0.0, work, given)
+        assert_close(C, A.double(), b, rt.last_kernel())
+        assert bool(work[:n * M * N].isfinite().all()) and bool(work[n * M * N:].isnan().all())
