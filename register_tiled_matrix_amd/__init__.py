@@ -558,7 +558,10 @@ def _run_gemm_mx(name, A, ta, lda, B, tb, M, N, K, C, ldc, alpha, beta, handle):
         C = A.new_empty((M, N), dtype=_torch.float32)
     a, q, s = A.data_ptr(), B.codes.data_ptr(), B.scales.data_ptr()
     work, at, size = None, None, 0
-    if M > 64 and K >= 1024:  # (no part is shorter than 512 k)
+    # K is split into parts of 512 at least, and not at all by the kernels for a few rows of A: those take
+    # row-major A and B stored N x K, up to 32 rows, and up to 64 where the rows are aligned for DMA
+    if K >= 1024 and (M > 64 or ta or not tb or
+                      (M > 32 and ((a | q) & 15 or lda & 7 or B._ldq & 15 or s & 3 or B._lds & 3))):
         size = lib.regtile_gemm_mx_workspace_ex(B.format, ta, tb, M, N, K, a, lda, q, B._ldq, s, B._lds, ldc)
         if size > 0:
             work = A.new_empty(size, dtype=_torch.uint8)  # stays until the launch is queued

@@ -196,3 +196,65 @@ def test_workspace_query_is_what_a_call_uses(fmt, order, M, N, K, aligned, parts
         run_with_workspace(torch.bfloat16, A, B, C, 1.0, 0.0, work, given)
         assert_close(C, A.double(), b, rt.last_kernel())
         assert bool(work[:n * M * N].isfinite().all()) and bool(work[n * M * N:].isnan().all())
+
+
+class Spy:
+    """The library, with the last workspace that a product was given on record."""
+
+    def __init__(self, lib):
+        self.lib, self.given = lib, None
+
+    def __getattr__(self, name):
+        f = getattr(self.lib, name)
+        if name not in ("regtile_gemm_bf16_mx", "regtile_gemm_f16_mx"):
+            return f
+
+        def call(*args):
+            self.given = args[17]
+            return f(*args)
+
+        return call
+
+
+@pytest.mark.parametrize("order,M,N,K,aligned,parts", IN_PARTS + [
+    ("nn", 16, 8192, 8192, True, 8), ("nn", 64, 4096, 4096, True, 8), ("tn", 16, 4096, 8192, True, 16), ("nt", 33, 2880, 2880, False, 5),
+    ("nt", 64, 600, 2944, True, 0), ("nt", 32, 600, 2880, False, 0), ("nn", 64, 1024, 1000, True, 0), ("tn", 300, 512, 2048, True, 0), ("tn", 304, 512, 2048, True, 4)])
+@pytest.mark.parametrize("fmt", [mx.FP4, mx.INT8])
+def test_binding_gives_each_call_its_workspace(monkeypatch, fmt, order, M, N, K, aligned, parts):
+    """dx and dW of a few rows among them: K in parts, as the library's query says, and the same bits as the C
+    call with that workspace."""
+    rng = np.random.default_rng(M + N + K)
+    ta, tb = order[0] == "t", order[1] == "t"
+    A = torch.from_numpy(rng.standard_normal((K, M) if ta else (M, K))).bfloat16().cuda()
+    A = A.t() if ta else A
+    B, b = random_matrix(rng, fmt, *((N, K) if tb else (K, N)), aligned)
+    B, b = (B.t(), b.t()) if tb else (B, b)
+    spy = Spy(rt.load())
+    monkeypatch.setattr(rt, "_lib", spy)
+    announce(f"gemm_mx {fmt} {order} {M}x{N}x{K}, the binding's workspace")
+    C = rt.gemm_bf16_mx(A, B)
+    assert spy.given == workspace_of(A, B, N) == parts * M * N * 4, spy.given
+    assert_close(C, A.double(), b, rt.last_kernel())
+    D = torch.empty_like(C)
+    run_with_workspace(torch.bfloat16, A, B, D, 1.0, 0.0, torch.empty(parts * M * N + 4, device="cuda"), parts)
+    assert torch.equal(C, D)
+
+
+def test_binding_and_misaligned_rows(monkeypatch):
+    """33 to 64 rows whose codes or scales start off the alignment of the token kernel."""
+    rng = np.random.default_rng(12)
+    M, N, K = 48, 600, 2944
+    A = torch.from_numpy(rng.standard_normal((M, K))).bfloat16().cuda()
+    w, g = mx.widths(mx.INT8, K)
+    codes = rng.integers(0, 256, (N, w), dtype=np.uint8)
+    scales = rng.integers(120, 131, (N, g)).astype(np.uint8)
+    b = torch.from_numpy(mx.decode(codes, scales, mx.INT8, K)).cuda().t()
+    spy = Spy(rt.load())
+    monkeypatch.setattr(rt, "_lib", spy)
+    for q_off, s_off, parts in ((0, 0, 0), (16, 4, 0), (8, 0, 5), (0, 1, 5)):
+        Q = dev_rows(np.pad(codes, ((0, 0), (q_off, 0))), w + 16, 255)[:, q_off:]
+        S = dev_rows(np.pad(scales, ((0, 0), (s_off, 0))), g + 4, 255)[:, s_off:]
+        B = rt.MXMatrix(mx.INT8, Q, S, K).t()
+        C = rt.gemm_bf16_mx(A, B)
+        assert spy.given == workspace_of(A, B, N) == parts * M * N * 4, (q_off, s_off, spy.given)
+        assert_close(C, A.double(), b, rt.last_kernel())
