@@ -232,7 +232,8 @@ int regtile_dequantize_mx(int format, int dtype, int rows, int cols, const uint8
  *   trans_a  (arg 2) as in regtile_gemm_bf16_ex;  trans_b (arg 3) 0: B stored K x N, groups along N;
  *            1: B stored N x K, groups along K
  *   M, N, K, alpha, A, lda (args 4-9), Q, ldq, S, lds (10-13), beta, C, ldc (14-16), as above:
- *            0 sizes, alpha == 0 and beta == 0 as for gemm_bf16
+ *            0 sizes, alpha == 0 and beta == 0 as for gemm_bf16. M or N above 2^31 - 128 is more than a
+ *            launch can count: hipErrorInvalidConfiguration, C untouched
  *   work, work_bytes (17-18) a workspace, or NULL and 0: device memory, 16-byte aligned, that nothing
  *            else uses until the call has run. Products with few output tiles and a long K use it to
  *            spread K over more of the chip, one M x N fp32 part for each split; with less than

@@ -79,7 +79,7 @@ __global__ __launch_bounds__(MXT_NT *KS, KS == 1 ? 2 : 4) void mx_mfma_kernel(in
     // M/N-contiguous storage every slab of the last tiles) are loaded as the whole run that ends
     // there and moved down when they are written to LDS, so that every load has the same time to
     // land; rows shorter than a run are read by element.
-        constexpr int PF = T == 128 ? 1 : 2;  // register sets: slabs loaded ahead
+    constexpr int PF = T == 128 ? 1 : 2;  // register sets: slabs loaded ahead
     uint32_t ra[PF][JA][4], rq[PF][JB][HB / 4], rs[PF][JB];
     const int a_cols = A_K ? K : M, b_cols = B_K ? K : N;
     const int b_bytes = (int)mx::row_bytes(FP4, b_cols);
