@@ -258,3 +258,60 @@ def test_binding_and_misaligned_rows(monkeypatch):
         C = rt.gemm_bf16_mx(A, B)
         assert spy.given == workspace_of(A, B, N) == parts * M * N * 4, (q_off, s_off, spy.given)
         assert_close(C, A.double(), b, rt.last_kernel())
+
+
+def test_graph_of_few_rows_with_workspaces():
+    """dx and dW of a few rows, each with a workspace, captured one after the other: every replay on new inputs
+    gives the eager calls' bits, with eager calls of other sizes between the replays."""
+    M, I, O = 16, 1024, 2048
+    W = rt.quantize_mx(torch.randn(O, I, device="cuda"), rt.MX_FP4)
+    kept = rt.quantize_mx(torch.randn(O, I, device="cuda", dtype=torch.bfloat16), rt.MX_INT8)
+    dy = torch.empty(M, O, device="cuda", dtype=torch.bfloat16)
+    dz = torch.empty(O, M, device="cuda", dtype=torch.float16)
+    acc = torch.zeros(M, I, device="cuda")
+    assert workspace_of(dy, W, I) > 0 and workspace_of(dz.t(), kept, I) > 0
+
+    def step():
+        dx = rt.gemm_bf16_mx(dy, W)
+        dw = rt.gemm_f16_mx(dz.t(), kept)
+        rt.gemm_f16_mx(dz.t(), kept, acc, alpha=0.5, beta=1.0)
+        return dx, dw, rt.gemm_bf16_mx(dy[:3], W)
+
+    side = torch.cuda.Stream()
+    dy.normal_(), dz.normal_()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for version in range(4):
+        dy.normal_(), dz.normal_(), acc.normal_()
+        before = acc.clone()
+        eager = [t.clone() for t in step()]
+        after = acc.clone()
+        acc.copy_(before)
+        rt.gemm_bf16_mx(dy[:9], W)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(acc, after), version
+        for o, e in zip(outs, eager):
+            assert torch.equal(o, e), version
+
+
+def test_few_rows_on_two_streams_at_once():
+    """Calls of few rows that use workspaces, running together on two streams: the results are those of one."""
+    W = rt.quantize_mx(torch.randn(4096, 1024, device="cuda"), rt.MX_FP4)
+    dy = [torch.randn(16, 4096, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    want = [rt.gemm_bf16_mx(d, W) for d in dy]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for i in range(40):
+        with torch.cuda.stream(streams[i % 2]):
+            outs[i % 2].append(rt.gemm_bf16_mx(dy[i % 2], W))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in outs[i])
