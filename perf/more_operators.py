@@ -34,7 +34,7 @@ def listed():
         # one token through a projection: latency counts
         {"name": "token_4096x4096", "op": "gemm", "pass": "forward", "a": "e4m3", "b": "e4m3", "out": "bf16", "M": 1, "N": 4096, "K": 4096, "beta": 0.0},
         # a long prompt (or a training batch): the largest product
-        {"name": "prompt8192_8192x8192", "op": "gemm", "pass": "forward", "a": "e4m3", "b": "e4m3", "out": "f32", "M": 8192, "N": 8192, "K": 8192, "beta": 0.0},
+        {"name": "prompt8192_8192x8192", "op": "gemm", "pass": "forward", "a": "e4m3", "b": "e4m3", "out": "bf16", "M": 8192, "N": 8192, "K": 8192, "beta": 0.0},
         # the gradient with respect to the layer's input: gradients in e5m2, the weights as the forward pass stores them
         {"name": "dx4096_4096x8192", "op": "gemm", "pass": "dx", "a": "e5m2", "b": "e4m3", "out": "bf16", "M": 4096, "N": 4096, "K": 8192, "beta": 0.0},
         # a weight gradient over a ragged number of tokens, accumulated over micro-batches
