@@ -258,6 +258,153 @@ int64_t regtile_gemm_mx_workspace_ex(int format, int trans_a, int trans_b, int M
                                      const uint16_t *A, int lda, const uint8_t *Q, int ldq,
                                      const uint8_t *S, int lds, int ldc);
 
+/*
+ * Block-scaled 8-bit float matrices: OCP e4m3 or e5m2 codes, one byte each, and one fp32 scale for each
+ * block of 1 x 128 values (activations, gradients: 128 consecutive columns of a row) or of 128 x 128 (weights).
+ * The blocks at the end of a row, and the last rows' blocks, may be short. An element's value is its code
+ * times its block's scale.
+ *   codes, ld               row r at codes + r * ld (bytes)
+ *   scales, scale_row, scale_col  the scale of block (i, j) at scales[i * scale_row + j * scale_col]; any
+ *                           strides >= 0 (consecutive i next to each other load fastest)
+ *   codes_stack, scales_stack  for a stack of matrices of one shape: the distance of one from the next, in
+ *                           bytes and in floats
+ *   rows, cols, stack       sizes; stack is 1 for a single matrix
+ *   type, block_rows        regtile_f8_type; 1 or 128
+ * No alignment is needed; the fast kernels want codes, ld and codes_stack to be multiples of 16. Products read
+ * such rows in aligned chunks of 16 bytes: bytes behind a row's end that share a chunk with its last element may
+ * be read, whatever they hold, and have no influence.
+ */
+enum regtile_f8_type { REGTILE_F8_E4M3 = 0, REGTILE_F8_E5M2 = 1 };
+typedef struct regtile_f8_matrix {
+    const uint8_t *codes;
+    int64_t ld;
+    const float *scales;
+    int64_t scale_row, scale_col;
+    int64_t codes_stack, scales_stack;
+    int rows, cols, stack;
+    int type, block_rows;
+} regtile_f8_matrix;
+
+/*
+ * regtile_quantize_f8 -- X (rows x cols, row-major, of a regtile_mx_dtype) to such a matrix. With a the largest
+ * magnitude of a block and top the type's largest value (448, 57344): s = max(a * (1 / top), 2^-126), 1 / top and
+ * the product rounded to fp32, and each code is the nearest value of the type to x / s, ties to even. A block with a NaN or an infinity gets a NaN
+ * scale and zero codes.
+ *   dtype (arg 1), transpose (2) 0, or 1: Q is the transpose of X, its blocks along X's rows (block_rows 1 only),
+ *   rows, cols (3-4), X, ldx (5-6)
+ *   index (7)  NULL, or one row number of X for each row that is taken (each of Q's rows, or with transpose
+ *              each of Q's columns); a number that is no row of X gives zeros
+ *   Q (8)      the matrix to write (its shape, type and block_rows say what); stack is not used
+ *   stream (9)
+ * regtile_dequantize_f8 -- the values, rounded to `dtype`: Q (arg 1), dtype (2), X, ldx (3-4), stream (5).
+ */
+int regtile_quantize_f8(int dtype, int transpose, int rows, int cols, const void *X, int ldx, const int32_t *index,
+                        const regtile_f8_matrix *Q, void *stream);
+int regtile_dequantize_f8(const regtile_f8_matrix *Q, int dtype, void *X, int ldx, void *stream);
+
+/*
+ * regtile_gemm_f8 -- C = alpha op(A) op(B) + beta C with both operands in 8-bit floats and a row-major C of a
+ * regtile_mx_dtype. A block of 128 k is summed first and enters the fp32 accumulator times the two scales, so
+ * scales have to run along k: a transposed A, and a B that is not transposed, need blocks of 128 x 128. The
+ * product of two scales has to be a finite fp32 number. The three products of a linear layer y = x W^T:
+ *   y  = x W^T    A = x (tokens x in, 1 x 128), B = W (out x in, 128 x 128), trans_b 1;
+ *   dx = dy W     A = dy (tokens x out, 1 x 128), B = W, trans_b 0;
+ *   dW = dy^T x   A = dy^T, B = x^T, both quantised transposed (blocks along the tokens), trans_b 1.
+ * A C in fp32 is made of exact products and fp32 sums. Into a C in 16 bits large products run on the 8-bit
+ * matrix instructions, whose sums of 32 products align to the largest of them and keep about 17 bits: the error
+ * is some 2e-6 of the sum of the magnitudes (1.2e-4 at most seen), before the rounding to 16 bits.
+ *   trans_a, trans_b (args 1-2), alpha (3), A (4), B (5), beta (6), c_dtype (7), C, ldc (8-9),
+ *   work, work_bytes (10-11) a workspace as for regtile_gemm_bf16_mx, of which regtile_gemm_f8_workspace() bytes
+ *   are made use of, stream (12)
+ * alpha == 0 and beta == 0 as for gemm_f32. Every output is summed in a fixed order.
+ */
+int regtile_gemm_f8(int trans_a, int trans_b, float alpha, const regtile_f8_matrix *A, const regtile_f8_matrix *B, float beta,
+                    int c_dtype, void *C, int ldc, void *work, int64_t work_bytes, void *stream);
+int64_t regtile_gemm_f8_workspace(int trans_a, int trans_b, const regtile_f8_matrix *A, const regtile_f8_matrix *B, int c_dtype,
+                                  int ldc);
+
+/*
+ * A mixture of experts. Token t has k slots, t * k + j; each holds an expert (or none). The rows that the experts
+ * work on are the slots in the order of their experts, each expert's from a multiple of `align` on:
+ *   slots     [rows]        the slot of each row, -1 for rows between groups and behind the last
+ *   position  [tokens * k]  the row of each slot, -1 where the slot has no expert
+ *   offsets   [experts + 1] the first row of each group, and the end of the last one's room
+ *   counts    [experts]     its slots
+ *   rows = regtile_expert_rows_size(tokens, k, experts, align): what any choice fits into (-1 for sizes that pass
+ *   2^31 - 1). All arrays on the device.
+ */
+typedef struct regtile_expert_rows {
+    const int32_t *slots, *position, *offsets, *counts;
+    int tokens, k, experts, align, rows;
+} regtile_expert_rows;
+int64_t regtile_expert_rows_size(int tokens, int k, int experts, int align);
+
+/*
+ * regtile_order_experts -- fills `rows` (arg 2; its arrays are written) from the experts of the slots (arg 1,
+ * tokens * k numbers; one that is no expert leaves its slot without a row). The order of slots of one expert is
+ * kept. Up to 1024 experts. work, work_bytes (3-4): regtile_order_experts_workspace() bytes, 16-byte aligned,
+ * that nothing else uses meanwhile; stream (5).
+ */
+int regtile_order_experts(const int32_t *chosen, const regtile_expert_rows *rows, void *work, int64_t work_bytes, void *stream);
+int64_t regtile_order_experts_workspace(int tokens, int k, int experts);
+
+/*
+ * regtile_route_experts -- a router: for each token the k experts with the largest values v, the lowest number among
+ * equals, and their weights. Scores s = softmax(logits) or sigmoid(logits); v = s + bias (or s). With `groups` > 1
+ * the experts fall into groups of equal size, and only the top_groups best are chosen from: a group counts as much
+ * as its best v (group_best 1) or the sum of its two best (2). Weights: s, divided by the sum of the chosen s if
+ * `renormalize`, times `scale`; in the order of the choice.
+ *   An expert with logit -inf (or bias -inf or NaN) is never chosen; slots for which no expert is left hold -1 and
+ *   weight 0 (a token whose logits are all -inf routes nowhere). A row with a NaN or +inf gets experts 0 .. k - 1
+ *   and NaN weights. Where the sum of the chosen s is 0 the weights are 0.
+ *   score (arg 1), dtype (2, of the logits), tokens (3), experts (4, up to 1024), k (5, up to 64), groups (6, up to
+ *   64, a divisor of experts), top_groups (7), group_best (8), renormalize (9), scale (10), logits, ldl (11-12),
+ *   bias (13, experts floats, or NULL), chosen (14, tokens x k), weights (15, the same), stream (16)
+ * regtile_route_experts_grad -- the gradient with respect to the logits (of their dtype) from that with respect to
+ * the weights. The choice is a constant; NaN in rows with a NaN or +inf; slots with no expert add nothing.
+ *   score (1), dtype (2), tokens (3), experts (4), k (5), renormalize (6), scale (7), logits, ldl (8-9),
+ *   chosen (10), dweights (11, tokens x k), dlogits, ldd (12-13), stream (14)
+ */
+enum regtile_score { REGTILE_SCORE_SOFTMAX = 0, REGTILE_SCORE_SIGMOID = 1 };
+int regtile_route_experts(int score, int dtype, int tokens, int experts, int k, int groups, int top_groups, int group_best,
+                          int renormalize, float scale, const void *logits, int ldl, const float *bias, int32_t *chosen,
+                          float *weights, void *stream);
+int regtile_route_experts_grad(int score, int dtype, int tokens, int experts, int k, int renormalize, float scale,
+                               const void *logits, int ldl, const int32_t *chosen, const float *dweights, void *dlogits, int ldd,
+                               void *stream);
+
+/*
+ * regtile_gemm_f8_experts -- the experts' products: row r of C (rows->rows x N) in group e is alpha A[r] op(B_e) +
+ * beta C[r], with A's row r, or with `gather` A's row for the token of slot r (A is then tokens x K). B is a stack
+ * of rows->experts matrices. Rows between groups become 0; rows behind the last group's room stay as they are.
+ *   rows (arg 1), gather (2), trans_b (3), alpha (4), A (5), B (6), beta (7), c_dtype (8), C, ldc (9-10), stream (11)
+ * regtile_gemm_f8_experts_dw -- the gradient of each expert's matrix: C_e = alpha A[:, group e] B[:, group e]^T +
+ * beta C_e, with A (M x rows) and B (N x rows) quantised transposed, blocks along the rows; rows->align has to be a
+ * multiple of 128. Columns behind a group's count are left out, whatever their codes (their blocks' scales have to
+ * be finite).
+ *   rows (arg 1), alpha (2), A (3), B (4), beta (5), c_dtype (6), C, ldc, c_stack (7-9: C_e at C + e * c_stack
+ *   elements), stream (10)
+ * Accuracy as for regtile_gemm_f8.
+ */
+int regtile_gemm_f8_experts(const regtile_expert_rows *rows, int gather, int trans_b, float alpha, const regtile_f8_matrix *A,
+                            const regtile_f8_matrix *B, float beta, int c_dtype, void *C, int ldc, void *stream);
+int regtile_gemm_f8_experts_dw(const regtile_expert_rows *rows, float alpha, const regtile_f8_matrix *A, const regtile_f8_matrix *B,
+                               float beta, int c_dtype, void *C, int ldc, int64_t c_stack, void *stream);
+
+/*
+ * regtile_combine_experts -- out[t] = sum_j w[t, j] Y[position[t, j]], fp32 sums in the order of j; slots without a
+ * row add nothing; weights NULL: all 1.
+ *   rows (arg 1), dtype (2, of Y and out), n (3, columns), Y, ldy (4-5), weights (6), out, ldo (7-8), stream (9)
+ * regtile_combine_experts_grad -- dY[r] = w dout[t] for the slot of row r, 0 for rows without one (those behind the
+ * last group too); dweights[t, j] = <dout[t], Y[position[t, j]]>, 0 for slots without a row.
+ *   rows (1), dtype (2), n (3), dout, ldd (4-5), Y, ldy (6-7; used for dweights only), weights (8, or NULL),
+ *   dY, lddy (9-10), dweights (11, or NULL), stream (12)
+ */
+int regtile_combine_experts(const regtile_expert_rows *rows, int dtype, int n, const void *Y, int ldy, const float *weights, void *out,
+                            int ldo, void *stream);
+int regtile_combine_experts_grad(const regtile_expert_rows *rows, int dtype, int n, const void *dout, int ldd, const void *Y, int ldy,
+                                 const float *weights, void *dY, int lddy, float *dweights, void *stream);
+
 /* Name of the kernel the calling thread launched last ("none" before the first launch,
  * "quick-return" when nothing was launched). Static storage; do not free. */
 const char *regtile_last_kernel(void);

@@ -23,6 +23,11 @@ Entry points (same names as the C ABI):
   (tokens x in): ``dW = gemm_bf16_mx(dy.t(), X)``.
 * ``quantize_mx(X, format)`` -> MXMatrix and ``dequantize_mx(Q, dtype=torch.bfloat16)``; ``MX_FP4`` holds
   weights in 4.25 bits, ``MX_INT8`` activations (a checkpoint for the backward pass) in 8.25.
+* ``gemm_f8(A, B, C=None, alpha=1.0, beta=0.0, dtype=torch.float32)`` with both operands block-scaled 8-bit
+  floats (``F8Matrix``: e4m3 or e5m2, one fp32 scale per 1 x 128 or 128 x 128 values), from ``quantize_f8``.
+* ``route_experts`` (and ``route_experts_grad``), ``expert_rows``, ``gemm_f8_experts`` (and
+  ``gemm_f8_experts_dw``) and ``combine_experts`` (and ``combine_experts_grad``): a mixture of experts, whose rows
+  fall into groups with a matrix each.
 * ``gemm_f32_raw`` / ``gemm_bf16_raw`` / ``gemm_f16_raw`` take the C arguments verbatim
   (integers for pointers).
 * ``last_kernel()``, ``last_kernel_info()`` (registers, LDS, scratch and occupancy of that
@@ -62,7 +67,11 @@ EXPORTED_SYMBOLS = ("gemm_f32", "gemm_bf16", "gemm_f16", "regtile_gemm_f32_algo"
                     "regtile_quantize_mx", "regtile_dequantize_mx", "regtile_gemm_bf16_mx",
                     "regtile_gemm_f16_mx", "regtile_gemm_mx_workspace", "regtile_gemm_mx_workspace_ex",
                     "regtile_last_kernel", "regtile_last_kernel_info", "regtile_strerror",
-                    "regtile_version")
+                    "regtile_version", "regtile_quantize_f8", "regtile_dequantize_f8", "regtile_gemm_f8",
+                    "regtile_gemm_f8_workspace", "regtile_expert_rows_size", "regtile_order_experts",
+                    "regtile_order_experts_workspace", "regtile_gemm_f8_experts", "regtile_gemm_f8_experts_dw",
+                    "regtile_route_experts", "regtile_route_experts_grad", "regtile_combine_experts",
+                    "regtile_combine_experts_grad")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libregtile.so")
@@ -121,6 +130,7 @@ def load():
         lib.regtile_gemm_mx_workspace.restype = ctypes.c_int64
         lib.regtile_gemm_mx_workspace_ex.argtypes = [I, I, I, I, I, I, P, I, P, I, P, I, I]
         lib.regtile_gemm_mx_workspace_ex.restype = ctypes.c_int64
+        _f8.declare(lib)
         lib.regtile_last_kernel.argtypes = []
         lib.regtile_last_kernel.restype = ctypes.c_char_p
         lib.regtile_last_kernel_info.argtypes = [ctypes.POINTER(KernelInfo)]
@@ -583,3 +593,9 @@ def gemm_bf16_mx(A, B, C=None, alpha=1.0, beta=0.0, stream=None):
 def gemm_f16_mx(A, B, C=None, alpha=1.0, beta=0.0, stream=None):
     """As gemm_bf16_mx with a float16 A; B's values are taken in float16."""
     return _gemm_mx("regtile_gemm_f16_mx", (_torch or _import_torch()).float16, A, B, C, float(alpha), float(beta), stream)
+
+
+from . import _f8  # noqa: E402
+from ._f8 import *  # noqa: E402,F401,F403
+
+__all__ += _f8.__all__

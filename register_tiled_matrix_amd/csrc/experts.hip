@@ -1,0 +1,609 @@
+// experts.hip -- what a mixture of experts needs around its products: the router's choice and weights with
+// their gradient, the order of the tokens' rows by expert, and the weighted sum of each token's rows with its
+// gradient.
+//
+// route: one wave a token, experts i * 64 + lane in registers. The choice is made of exact comparisons: of the
+// logits themselves where softmax or sigmoid only grow with them (no bias, groups by their best), and otherwise
+// of score + bias in 64 bits, since in 32 two experts whose values differ by less than a rounding change places
+// about once in 5000 tokens. Each of the k steps takes the largest key over the wave with 6 DPP maxima of its
+// high word; ties are settled by the low word, then by the lowest index. Only the chosen experts' weights are
+// computed, by the lane that holds the choice, in 64 bits.
+//
+// order: a stable counting sort. A wave finds the lanes with its own expert by ballots over the index's bits,
+// so that counts and ranks need no atomics and come out the same every time.
+#include "f8_common.h"
+
+namespace regtile {
+namespace {
+
+constexpr int NT = 256;  // 4 waves
+typedef unsigned long long u64;
+
+__device__ __forceinline__ float load_value(const void *p, int dtype, int64_t at) {
+    if (dtype == 0) return static_cast<const float *>(p)[at];
+    if (dtype == 1) return (float)static_cast<const __bf16 *>(p)[at];
+    return (float)static_cast<const _Float16 *>(p)[at];
+}
+__device__ __forceinline__ void store_value(void *p, int dtype, int64_t at, float x) {
+    if (dtype == 0)
+        static_cast<float *>(p)[at] = x;
+    else if (dtype == 1)
+        static_cast<__bf16 *>(p)[at] = (__bf16)x;
+    else
+        static_cast<_Float16 *>(p)[at] = (_Float16)x;
+}
+
+// The largest x of the wave, in every lane
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+#if defined(__HIP_DEVICE_COMPILE__)
+#define REGTILE_STEP(ctrl) x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, ctrl, 0xF, 0xF, false))
+    REGTILE_STEP(0x111);  // row_shr 1, 2, 4, 8: lane 15 of each row of 16 has its maximum
+    REGTILE_STEP(0x112);
+    REGTILE_STEP(0x114);
+    REGTILE_STEP(0x118);
+    REGTILE_STEP(0x142);  // row_bcast 15 and 31: lane 63 has them all
+    REGTILE_STEP(0x143);
+#undef REGTILE_STEP
+    return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+#else
+    return x;
+#endif
+}
+template <typename T>
+__device__ __forceinline__ T wave_sum(T x) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
+    return x;
+}
+
+// Keys that compare as the values do; 0 for what is not to be chosen (-inf, NaN), which is below every other
+__device__ __forceinline__ u64 key_of(float v) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);  // (-0 and 0 are equal)
+    const uint32_t k = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+    return v > -INFINITY ? (u64)k << 32 : 0;
+}
+__device__ __forceinline__ u64 key_of(double v) {
+    const u64 b = __builtin_bit_cast(u64, v + 0.0);
+    const u64 k = b ^ ((u64)((int64_t)b >> 63) | 0x8000000000000000ull);
+    return v > -(double)INFINITY ? k : 0;
+}
+
+// A logit's score, up to softmax's total: 64 bits
+__device__ __forceinline__ double score_of(bool sigmoid, float logit, float top) {
+    return sigmoid ? 1.0 / (1.0 + exp(-(double)logit)) : exp((double)logit - (double)top);
+}
+
+// R: experts a lane; WIDE: choose by score + bias in 64 bits, else by the logits
+template <int R, bool WIDE>
+__global__ __launch_bounds__(NT) void route_kernel(RouteProblem p) {
+    // values by expert, a group's experts one slot further on than the last's: the lanes that read a group each
+    // then meet different banks
+    __shared__ u64 by_expert[WIDE ? 4 : 1][WIDE ? 64 * R + 64 : 1];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t token = (int64_t)blockIdx.x * 4 + wave;
+    if (token >= p.tokens) return;
+    float x[R];
+    bool poison = false;
+    uint32_t top_key = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int e = i * 64 + lane;
+        x[i] = e < p.experts ? load_value(p.logits, p.dtype, token * p.ldl + e) : -INFINITY;
+        poison |= x[i] != x[i] || x[i] == INFINITY;
+        top_key = max(top_key, (uint32_t)(key_of(x[i]) >> 32));
+    }
+    int32_t *chosen = p.chosen + token * p.k;
+    float *weights = p.weights + token * p.k;
+    if (__ballot(poison) != 0) {
+        if (lane < p.k) {
+            chosen[lane] = lane;
+            weights[lane] = __builtin_nanf("");
+        }
+        return;
+    }
+    top_key = wave_max(top_key);  // the largest logit
+    const float top = top_key == 0 ? 0.0f
+                                   : __builtin_bit_cast(float, top_key & 0x80000000u ? top_key ^ 0x80000000u : ~top_key);
+    double total = 1.0;
+    u64 key[R];
+    if constexpr (WIDE) {
+        double s[R];
+        total = 0.0;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            s[i] = score_of(p.sigmoid, x[i], top);
+            total += s[i];
+        }
+        total = p.sigmoid ? 1.0 : wave_sum(total);
+        const double unit = total > 0.0 ? 1.0 / total : 0.0;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int e = i * 64 + lane;
+            const double b = p.bias != nullptr && e < p.experts ? (double)p.bias[e] : 0.0;
+            key[i] = x[i] > -INFINITY ? key_of(s[i] * unit + b) : 0;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i) key[i] = key_of(x[i]);
+        if (!p.sigmoid && !p.renormalize) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < R; ++i) sum += expf(x[i] - top);
+            total = wave_sum((double)sum);
+        }
+    }
+    if (p.groups > 1) {
+        const int per = p.experts / p.groups;
+        u64 open;
+        if constexpr (WIDE) {
+            u64 *mine = by_expert[wave];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int e = i * 64 + lane;
+                if (e < p.experts) mine[e + e / per] = key[i];
+            }
+            __builtin_amdgcn_wave_barrier();
+            u64 first = 0, second = 0;  // the two best of group `lane`
+            if (lane < p.groups)
+                for (int i = 0; i < per; ++i) {
+                    const u64 k = mine[lane * (per + 1) + i];
+                    second = max(second, min(first, k));
+                    first = max(first, k);
+                }
+            auto value = [](u64 k) { return __builtin_bit_cast(double, k >> 63 ? k ^ 0x8000000000000000ull : ~k); };
+            u64 rank = first;
+            if (p.group_best == 2 && second != 0) rank = key_of(value(first) + value(second));
+            // groups before this one: better, or as good with a lower number
+            int before = 0;
+            for (int g = 0; g < p.groups; ++g) {
+                const u64 other = __shfl(rank, g);
+                before += other > rank || (other == rank && g < lane);
+            }
+            open = __ballot(lane < p.groups && before < p.top_groups);
+        } else {
+            // by their best logit: the best of the groups that are left, top_groups times
+            u64 left = p.groups == 64 ? ~0ull : (1ull << p.groups) - 1;
+            for (int n = 0; n < p.top_groups; ++n) {
+                uint32_t best = 0;
+                int in = 0x7FFFFFFF;
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const int e = i * 64 + lane, g = e / per;
+                    if (e < p.experts && (left >> g & 1) && (uint32_t)(key[i] >> 32) > best) {
+                        best = (uint32_t)(key[i] >> 32);
+                        in = g;
+                    }
+                }
+                const uint32_t m = wave_max(best);
+                if (m == 0) break;  // nothing to choose in any of them
+                const uint32_t low = ~wave_max(best == m ? ~(uint32_t)in : 0u);
+                left &= ~(1ull << low);
+            }
+            open = ~left;
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int e = i * 64 + lane;
+            if (e < p.experts && !(open >> (e / per) & 1)) key[i] = 0;
+        }
+    }
+    // the k best
+    int my_expert = -1;
+    float my_logit = -INFINITY;
+    for (int j = 0; j < p.k; ++j) {
+        u64 best = 0;
+        int at = 0;
+        float l = 0.0f;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
+                l = x[i];
+            }
+        const uint32_t high = wave_max((uint32_t)(best >> 32));
+        if (high == 0) break;
+        u64 who = __ballot((uint32_t)(best >> 32) == high);
+        if (who & (who - 1)) {
+            if constexpr (WIDE) {
+                const uint32_t low = wave_max((uint32_t)(best >> 32) == high ? (uint32_t)best : 0u);
+                who = __ballot((uint32_t)(best >> 32) == high && (uint32_t)best == low);
+            }
+            if (who & (who - 1)) {
+                const uint32_t first = wave_max(who >> lane & 1 ? ~(uint32_t)(at * 64 + lane) : 0u);
+                who = __ballot((who >> lane & 1) && ~(uint32_t)(at * 64 + lane) == first);
+            }
+        }
+        const int winner = __ffsll((unsigned long long)who) - 1;
+        const int expert = __builtin_amdgcn_readlane(at, winner) * 64 + winner;
+        const float logit = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, l), winner));
+        if (lane == j) {
+            my_expert = expert;
+            my_logit = logit;
+        }
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (lane == winner && i == at) key[i] = 0;
+    }
+    const double s = my_expert >= 0 ? score_of(p.sigmoid, my_logit, top) : 0.0;
+    if (p.renormalize) total = wave_sum(s);
+    if (lane < p.k) {
+        chosen[lane] = my_expert;
+        weights[lane] = total > 0.0 ? (float)(s / total * (double)p.scale) : 0.0f;
+    }
+}
+
+// The gradient with respect to the logits. With w the weights before `scale` and dot = sum_j dw_j w_j, expert
+// c's is scale times:  softmax, renormalised: w_c (dw_c - dot), and 0 for experts that were not chosen;
+// softmax: p_e (dw_e - dot), dw_e = 0 for those;  sigmoid, renormalised: w_c (1 - s_c) (dw_c - dot);
+// sigmoid: s_c (1 - s_c) dw_c.
+template <int R>
+__global__ __launch_bounds__(NT) void route_grad_kernel(RouteProblem p) {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t token = (int64_t)blockIdx.x * 4 + wave;
+    if (token >= p.tokens) return;
+    float x[R], d[R];
+    bool poison = false;
+    uint32_t top_key = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int e = i * 64 + lane;
+        x[i] = e < p.experts ? load_value(p.logits, p.dtype, token * p.ldl + e) : -INFINITY;
+        poison |= x[i] != x[i] || x[i] == INFINITY;
+        top_key = max(top_key, (uint32_t)(key_of(x[i]) >> 32));
+        d[i] = 0.0f;
+    }
+    poison = __ballot(poison) != 0;
+    top_key = wave_max(top_key);
+    const float top = top_key == 0 ? 0.0f
+                                   : __builtin_bit_cast(float, top_key & 0x80000000u ? top_key ^ 0x80000000u : ~top_key);
+    int expert = lane < p.k ? p.chosen[token * p.k + lane] : -1;
+    if (expert >= p.experts || expert < 0) expert = -1;
+    const double dw = expert >= 0 ? (double)p.dweights[token * p.k + lane] : 0.0;
+    const float logit = expert >= 0 ? load_value(p.logits, p.dtype, token * p.ldl + expert) : -INFINITY;
+    const double s = expert >= 0 && !poison ? score_of(p.sigmoid, logit, top) : 0.0;
+    double total = 1.0;
+    if (p.renormalize) {
+        total = wave_sum(s);
+    } else if (!p.sigmoid) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < R; ++i) sum += expf(x[i] - top);
+        total = wave_sum((double)sum);
+    }
+    const double w = total > 0.0 ? s / total : 0.0, dot = wave_sum(dw * w);
+    double mine = w * (dw - (p.renormalize || !p.sigmoid ? dot : 0.0)) * (double)p.scale;
+    if (p.sigmoid) mine *= 1.0 - s;
+    if (!p.sigmoid && !p.renormalize) {
+        mine = w * dw * (double)p.scale;  // the other part goes to every expert
+        const float all = total > 0.0 ? (float)(dot / total * (double)p.scale) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < R; ++i) d[i] = -all * expf(x[i] - top);
+    }
+    const float value = (float)mine;
+    for (int j = 0; j < p.k; ++j) {
+        const int e = __builtin_amdgcn_readlane(expert, j);
+        if (e < 0) continue;
+        const float v = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, value), j));
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+            if (e == i * 64 + lane) d[i] += v;
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int e = i * 64 + lane;
+        if (e < p.experts) store_value(p.dlogits, p.dtype, token * p.ldd + e, poison ? __builtin_nanf("") : d[i]);
+    }
+}
+
+// ---- order -------------------------------------------------------------------------------------
+constexpr int ORDER_NT = 1024, ORDER_WAVES = 16, CHUNK = 4096, MOST_EXPERTS = 1024;
+
+// The lanes of the wave whose e is this lane's
+__device__ __forceinline__ u64 same(int e, int bits) {
+    u64 m = ~0ull;
+    for (int b = 0; b < bits; ++b) {
+        const u64 set = __ballot(e >> b & 1);
+        m &= e >> b & 1 ? set : ~set;
+    }
+    return m;
+}
+__device__ __forceinline__ int expert_of(const OrderProblem &p, int64_t slot, int64_t end) {
+    if (slot >= end) return p.experts;
+    const int e = p.chosen[slot];
+    return e >= 0 && e < p.experts ? e : p.experts;
+}
+
+// counts[wave][expert] of a chunk's slots, each wave's own part of `per` slots from `first` on
+__device__ __forceinline__ void count_chunk(const OrderProblem &p, int *counts, int64_t first, int64_t end, int per, int bits) {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    for (int i = threadIdx.x; i < ORDER_WAVES * p.experts; i += ORDER_NT) counts[i] = 0;
+    __syncthreads();
+    int *mine = counts + wave * p.experts;
+    for (int i = 0; i < per; i += 64) {
+        const int e = expert_of(p, first + wave * per + i + lane, end);
+        const u64 m = same(e, bits);
+        if (e < p.experts && __ffsll((unsigned long long)m) - 1 == lane) mine[e] += __popcll(m);
+        __builtin_amdgcn_wave_barrier();
+    }
+    __syncthreads();
+}
+
+__global__ __launch_bounds__(ORDER_NT) void order_count_kernel(OrderProblem p, int bits) {
+    __shared__ int counts[ORDER_WAVES * MOST_EXPERTS];
+    const int64_t n = (int64_t)p.tokens * p.k, first = (int64_t)blockIdx.x * CHUNK;
+    count_chunk(p, counts, first, min(n, first + CHUNK), CHUNK / ORDER_WAVES, bits);
+    const int e = threadIdx.x;
+    if (e < p.experts) {
+        int sum = 0;
+        for (int w = 0; w < ORDER_WAVES; ++w) sum += counts[w * p.experts + e];
+        p.work[(int64_t)blockIdx.x * p.experts + e] = sum;
+    }
+}
+
+__global__ __launch_bounds__(ORDER_NT) void order_place_kernel(OrderProblem p, int bits) {
+    __shared__ int counts[ORDER_WAVES * MOST_EXPERTS];
+    __shared__ int wave_room[ORDER_WAVES];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, groups = gridDim.x;
+    const int64_t n = (int64_t)p.tokens * p.k, first = (int64_t)blockIdx.x * CHUNK, end = min(n, first + CHUNK);
+    // a wave's part of the chunk, in whole 64s
+    const int per = ((int)((end - first + ORDER_WAVES - 1) / ORDER_WAVES) + 63) / 64 * 64;
+    count_chunk(p, counts, first, end, per, bits);
+    int before = 0, all = 0;
+    if (tid < p.experts) {
+        if (groups == 1) {
+            for (int w = 0; w < ORDER_WAVES; ++w) all += counts[w * p.experts + tid];
+        } else {
+            for (int g = 0; g < groups; ++g) {
+                const int c = p.work[(int64_t)g * p.experts + tid];
+                before += g < (int)blockIdx.x ? c : 0;
+                all += c;
+            }
+        }
+    }
+    const int room = (all + p.align - 1) / p.align * p.align;
+    int upto = room;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int v = __shfl_up(upto, d);
+        if (lane >= d) upto += v;
+    }
+    if (lane == 63) wave_room[wave] = upto;
+    __syncthreads();
+    int start = upto - room, used = 0;
+    for (int w = 0; w < ORDER_WAVES; ++w) {
+        if (w < wave) start += wave_room[w];
+        used += wave_room[w];
+    }
+    if (tid < p.experts) {
+        int at = start + before;
+        for (int w = 0; w < ORDER_WAVES; ++w) {
+            const int c = counts[w * p.experts + tid];
+            counts[w * p.experts + tid] = at;
+            at += c;
+        }
+        if (blockIdx.x == 0) {
+            p.offsets[tid] = start;
+            p.counts[tid] = all;
+            if (tid == 0) p.offsets[p.experts] = used;
+        }
+        if (tid % groups == (int)blockIdx.x)
+            for (int r = start + all; r < start + room; ++r) p.slots[r] = -1;
+    }
+    for (int64_t r = used + (int64_t)blockIdx.x * ORDER_NT + tid; r < p.rows; r += (int64_t)groups * ORDER_NT) p.slots[r] = -1;
+    __syncthreads();
+    int *mine = counts + wave * p.experts;
+    for (int i = 0; i < per; i += 64) {
+        const int64_t slot = first + wave * per + i + lane;
+        const int e = expert_of(p, slot, end);
+        const u64 m = same(e, bits);
+        int at = -1;
+        if (e < p.experts) at = mine[e] + __popcll(m & ((1ull << lane) - 1));
+        __builtin_amdgcn_wave_barrier();
+        if (e < p.experts && 63 - __clzll((long long)m) == lane) mine[e] = at + 1;
+        __builtin_amdgcn_wave_barrier();
+        if (slot < end) {
+            p.position[slot] = at;
+            if (at >= 0) p.slots[at] = (int32_t)slot;
+        }
+    }
+}
+
+// ---- combine -----------------------------------------------------------------------------------
+template <int DT>
+struct Elem;
+template <>
+struct Elem<0> {
+    typedef float T;
+};
+template <>
+struct Elem<1> {
+    typedef __bf16 T;
+};
+template <>
+struct Elem<2> {
+    typedef _Float16 T;
+};
+// V consecutive values (V elements: one aligned load, or 1)
+template <int DT, int V>
+__device__ __forceinline__ void load_v(const void *p, int64_t at, float (&x)[V]) {
+    typedef typename Elem<DT>::T T;
+    const T *q = static_cast<const T *>(p) + at;
+    if constexpr (V == 1) {
+        x[0] = (float)q[0];
+    } else {
+        T t[V];
+        __builtin_memcpy(t, __builtin_assume_aligned(q, V * sizeof(T)), V * sizeof(T));
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = (float)t[i];
+    }
+}
+template <int DT, int V>
+__device__ __forceinline__ void store_v(void *p, int64_t at, const float (&x)[V]) {
+    typedef typename Elem<DT>::T T;
+    T *q = static_cast<T *>(p) + at;
+    T t[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) t[i] = (T)x[i];
+    __builtin_memcpy(__builtin_assume_aligned(q, V * sizeof(T)), t, V * sizeof(T));
+}
+__device__ __forceinline__ int position_of(const CombineProblem &p, int64_t slot) {
+    const int r = p.position[slot];
+    return r < p.rows ? r : -1;
+}
+
+// out[t] = sum_j w[t, j] Y[position[t, j]], in the order of j: a workgroup's threads along a token's columns.
+template <int DT, int V>
+__global__ __launch_bounds__(NT) void combine_kernel(CombineProblem p, int threads_x) {
+    const int tx = threadIdx.x % threads_x, ty = threadIdx.x / threads_x;
+    for (int64_t t = (int64_t)blockIdx.x * (NT / threads_x) + ty; t < p.tokens; t += (int64_t)gridDim.x * (NT / threads_x))
+        for (int64_t c = ((int64_t)blockIdx.y * threads_x + tx) * V; c < p.n; c += (int64_t)gridDim.y * threads_x * V) {
+            float sum[V] = {};
+            for (int j0 = 0; j0 < p.k; j0 += 4) {  // 4 rows under way
+                float y[4][V], w[4];
+                bool some[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int64_t slot = t * p.k + j0 + j;
+                    const int r = j0 + j < p.k ? position_of(p, slot) : -1;
+                    some[j] = r >= 0;
+                    w[j] = some[j] && p.weights != nullptr ? p.weights[slot] : 1.0f;
+                    if (some[j]) load_v<DT, V>(p.Y, r * p.ldy + c, y[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (some[j]) {
+#pragma unroll
+                        for (int v = 0; v < V; ++v) sum[v] = fmaf(w[j], y[j][v], sum[v]);
+                    }
+            }
+            store_v<DT, V>(p.out, t * p.ldo + c, sum);
+        }
+}
+
+// A wave to a row r of Y: with t = slots[r] / k, dY[r] = w dout[t] and dw = <dout[t], Y[r]>; zeros where the row
+// is nobody's. Slots without a row have dw = 0.
+template <int DT, int V>
+__global__ __launch_bounds__(NT) void combine_grad_kernel(CombineProblem p) {
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t n = (int64_t)p.tokens * p.k;
+    for (int64_t r = (int64_t)blockIdx.x * 4 + wave; r < max((int64_t)p.rows, n); r += (int64_t)gridDim.x * 4) {
+        if (p.dweights != nullptr && r < n && lane == 0 && position_of(p, r) < 0) p.dweights[r] = 0.0f;
+        if (r >= p.rows) continue;
+        const int slot = p.slots[r];
+        const bool some = slot >= 0 && slot < n;
+        const int64_t t = some ? slot / p.k : 0;
+        const float w = !some ? 0.0f : p.weights != nullptr ? p.weights[slot] : 1.0f;
+        float sum = 0.0f;
+        for (int64_t c = lane * V; c < p.n; c += 64 * V) {
+            float d[V] = {}, y[V];
+            if (some) {
+                load_v<DT, V>(p.dout, t * p.ldd + c, d);
+                if (p.dweights != nullptr) {
+                    load_v<DT, V>(p.Y, r * p.ldy + c, y);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) sum = fmaf(d[v], y[v], sum);
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v) d[v] *= w;
+            }
+            store_v<DT, V>(p.dY, r * p.lddy + c, d);
+        }
+        if (some && p.dweights != nullptr) {
+            sum = wave_sum(sum);
+            if (lane == 0) p.dweights[slot] = sum;
+        }
+    }
+}
+
+bool rows16(const void *p, int64_t ld, int size) { return aligned16(p) && ld * size % 16 == 0; }
+
+template <typename F>
+hipError_t go(F f, dim3 grid, unsigned threads, hipStream_t s, void **args) {
+    note_launch(reinterpret_cast<const void *>(f), threads);
+    return hipLaunchKernel(reinterpret_cast<const void *>(f), grid, dim3(threads), args, 0, s);
+}
+
+}  // namespace
+
+hipError_t launch_route(const RouteProblem &p, hipStream_t s, const char **name) {
+    // by the logits where the scores grow with them and nothing is added to them
+    const bool wide = p.bias != nullptr || (p.groups > 1 && p.group_best == 2);
+    *name = wide ? "route_scores" : "route_logits";
+    RouteProblem q = p;
+    void *args[] = {&q};
+    const dim3 grid((unsigned)(((int64_t)p.tokens + 3) / 4));
+    auto pick = [&](auto narrow_f, auto wide_f) { return go(wide ? wide_f : narrow_f, grid, NT, s, args); };
+    if (p.experts <= 64) return pick(route_kernel<1, false>, route_kernel<1, true>);
+    if (p.experts <= 128) return pick(route_kernel<2, false>, route_kernel<2, true>);
+    if (p.experts <= 256) return pick(route_kernel<4, false>, route_kernel<4, true>);
+    if (p.experts <= 512) return pick(route_kernel<8, false>, route_kernel<8, true>);
+    return pick(route_kernel<16, false>, route_kernel<16, true>);
+}
+
+hipError_t launch_route_grad(const RouteProblem &p, hipStream_t s, const char **name) {
+    *name = "route_grad";
+    RouteProblem q = p;
+    void *args[] = {&q};
+    const dim3 grid((unsigned)(((int64_t)p.tokens + 3) / 4));
+    if (p.experts <= 64) return go(route_grad_kernel<1>, grid, NT, s, args);
+    if (p.experts <= 128) return go(route_grad_kernel<2>, grid, NT, s, args);
+    if (p.experts <= 256) return go(route_grad_kernel<4>, grid, NT, s, args);
+    if (p.experts <= 512) return go(route_grad_kernel<8>, grid, NT, s, args);
+    return go(route_grad_kernel<16>, grid, NT, s, args);
+}
+
+// One workgroup orders a chunk by itself; more of them count first, through the workspace.
+int64_t order_work_bytes(int64_t slots, int experts) {
+    const int64_t groups = (slots + CHUNK - 1) / CHUNK;
+    return groups > 1 ? groups * experts * 4 : 0;
+}
+
+hipError_t launch_order(const OrderProblem &p, hipStream_t s, const char **name) {
+    const int64_t n = (int64_t)p.tokens * p.k;
+    const unsigned groups = (unsigned)(n > CHUNK ? (n + CHUNK - 1) / CHUNK : 1);
+    int bits = 1;
+    while ((p.experts >> bits) != 0) ++bits;  // 0 .. experts
+    OrderProblem q = p;
+    void *args[] = {&q, &bits};
+    *name = "order_experts";
+    if (groups > 1) {
+        const hipError_t e = go(order_count_kernel, dim3(groups), ORDER_NT, s, args);
+        if (e != hipSuccess) return e;
+    }
+    return go(order_place_kernel, dim3(groups), ORDER_NT, s, args);
+}
+
+hipError_t launch_combine(const CombineProblem &p, hipStream_t s, const char **name) {
+    *name = "combine_experts";
+    const int size = p.dtype == 0 ? 4 : 2, v = 16 / size;
+    const bool wide = p.n % v == 0 && rows16(p.Y, p.ldy, size) && rows16(p.out, p.ldo, size);
+    const int64_t units = wide ? p.n / v : p.n;
+    int threads_x = NT;  // 16 threads at least: the rows of 16 tokens are then under way in a workgroup
+    while (threads_x > 16 && threads_x / 2 >= units) threads_x /= 2;
+    const int64_t gx = ((int64_t)p.tokens * threads_x + NT - 1) / NT, gy = (units + threads_x - 1) / threads_x;
+    CombineProblem q = p;
+    void *args[] = {&q, &threads_x};
+    const dim3 grid((unsigned)(gx < (1 << 20) ? gx : 1 << 20), (unsigned)(gy < 1024 ? gy : 1024));
+    auto pick = [&](auto f, auto f1) { return go(wide ? f : f1, grid, NT, s, args); };
+    if (p.dtype == 0) return pick(combine_kernel<0, 4>, combine_kernel<0, 1>);
+    if (p.dtype == 1) return pick(combine_kernel<1, 8>, combine_kernel<1, 1>);
+    return pick(combine_kernel<2, 8>, combine_kernel<2, 1>);
+}
+
+hipError_t launch_combine_grad(const CombineProblem &p, hipStream_t s, const char **name) {
+    *name = "combine_experts_grad";
+    const int size = p.dtype == 0 ? 4 : 2, v = 16 / size;
+    const bool wide = p.n % v == 0 && (p.dweights == nullptr || rows16(p.Y, p.ldy, size)) && rows16(p.dout, p.ldd, size) &&
+                      rows16(p.dY, p.lddy, size);
+    const int64_t n = (int64_t)p.tokens * p.k, rows = p.rows > n ? p.rows : n, g = (rows + 3) / 4;
+    CombineProblem q = p;
+    void *args[] = {&q};
+    const dim3 grid((unsigned)(g < (1 << 20) ? g : 1 << 20));
+    auto pick = [&](auto f, auto f1) { return go(wide ? f : f1, grid, NT, s, args); };
+    if (p.dtype == 0) return pick(combine_grad_kernel<0, 4>, combine_grad_kernel<0, 1>);
+    if (p.dtype == 1) return pick(combine_grad_kernel<1, 8>, combine_grad_kernel<1, 1>);
+    return pick(combine_grad_kernel<2, 8>, combine_grad_kernel<2, 1>);
+}
+
+}  // namespace regtile

@@ -1,0 +1,205 @@
+// f8_common.h -- block-scaled 8-bit float matrices of include/regtile.h on the device: one validated
+// problem, conversions of codes, the lookup of a group's tile, and the epilogue that the GEMM kernels
+// share.
+//
+// Codes are OCP e4m3 (S.1111.111 is NaN, no infinities) or e5m2 floats. Every code is exact in bf16, so
+// products of bf16 fragments are exact and the sum of a block of 128 is as exact as gemm_bf16's. The
+// 8-bit matrix instructions run at twice that rate but align the products of a group to the largest and
+// drop what falls 17 bits or so below it: against 64 bits the error of one block of normally distributed
+// codes measured 2.0e-6 of the sum of magnitudes (rms; 1.2e-4 at worst on random bits). That is far
+// below a 16-bit C's half step, and above what a 32-bit C should lose.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "mfma_common.h"
+#include "regtile_internal.h"
+
+namespace regtile {
+namespace f8 {
+
+constexpr int BLOCK = 128;
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+// Two codes of a dword (the low half, or the high one) as bf16 values; exact (scale 1).
+template <int TYPE, bool HI>
+__device__ __forceinline__ uint32_t bf16_pair(uint32_t codes) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    if constexpr (TYPE == 0)
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 1.0f, HI));
+    else
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(codes, 1.0f, HI));
+#else
+    (void)codes;
+    return 0;
+#endif
+}
+// 8 codes as the bf16 operand of one lane
+template <int TYPE>
+__device__ __forceinline__ mfma::bf16x8 bf16_of8(uint32_t lo, uint32_t hi) {
+    const mfma::u32x4 v = {bf16_pair<TYPE, false>(lo), bf16_pair<TYPE, true>(lo), bf16_pair<TYPE, false>(hi),
+                           bf16_pair<TYPE, true>(hi)};
+    return __builtin_bit_cast(mfma::bf16x8, v);
+}
+// Two codes as fp32
+template <bool HI>
+__device__ __forceinline__ f32x2 f32_pair(int type, uint32_t codes) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    return type == 0 ? __builtin_amdgcn_cvt_pk_f32_fp8((int)codes, HI) : __builtin_amdgcn_cvt_pk_f32_bf8((int)codes, HI);
+#else
+    (void)type;
+    (void)codes;
+    return f32x2{};
+#endif
+}
+
+// Where group e of `rows` begins, its used rows and its room, kept inside the matrix whatever the arrays hold.
+struct Group {
+    int first, count, room;
+};
+__device__ __forceinline__ Group group_of(const int32_t *offsets, const int32_t *counts, int e, int rows) {
+    Group g;
+    g.first = min(max(offsets[e], 0), rows);
+    g.room = min(max(offsets[e + 1], g.first), rows) - g.first;
+    g.count = min(max(counts[e], 0), g.room);
+    return g;
+}
+
+// The group that row tile `tile` (of `height` rows; groups begin a tile each) belongs to and the tile's
+// number in it; false past the last. Every lane of the wave gets the same answer: 64 groups are counted
+// at a time.
+__device__ __forceinline__ bool find_tile(const int32_t *offsets, int experts, int rows, int height, int tile, int &expert,
+                                          int &in_group) {
+    const int lane = __lane_id();
+    int before = 0;
+    for (int e0 = 0; e0 < experts; e0 += 64) {
+        const int e = e0 + lane;
+        int n = 0;
+        if (e < experts) {
+            const int first = min(max(offsets[e], 0), rows);
+            n = (min(max(offsets[e + 1], first), rows) - first + height - 1) / height;
+        }
+        int upto = n;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(upto, d);
+            if (lane >= d) upto += v;
+        }
+        const uint64_t past = __ballot(before + upto > tile);
+        if (past != 0) {
+            const int l = __ffsll((unsigned long long)past) - 1;
+            expert = __builtin_amdgcn_readfirstlane(e0 + l);
+            in_group = __builtin_amdgcn_readfirstlane(tile - before - (__shfl(upto, l) - __shfl(n, l)));
+            return true;
+        }
+        before += __shfl(upto, 63);
+    }
+    return false;
+}
+
+// What one workgroup computes: rows row0 .. row0 + rows - 1 of C (the tile's), of which the first `used` come
+// from A and the rest are zeros, over K values of depth.
+struct Work {
+    int row0, rows, used, K;
+    F8Operand a, b;
+    F8Out out;
+};
+// Row tile `tile` of `height` rows (DEPTH: of group `part`); false where there is none.
+__device__ __forceinline__ bool work_of(const F8Problem &p, int height, int tile, int part, Work &w) {
+    w.a = p.a;
+    w.b = p.b;
+    w.out = p.out;
+    w.K = p.K;
+    if (p.mode == F8Problem::ROWS) {
+        int e, in_group;
+        if (!find_tile(p.offsets, p.experts, p.M, height, tile, e, in_group)) return false;
+        const Group g = group_of(p.offsets, p.counts, e, p.M);
+        const int at = in_group * height;
+        w.row0 = g.first + at;
+        w.rows = min(height, g.room - at);
+        w.used = min(max(g.count - at, 0), height);
+        w.b.q += e * p.b_stack;
+        w.b.s += e * p.bs_stack;
+        return true;
+    }
+    w.row0 = tile * height;
+    w.rows = w.used = min(height, p.M - w.row0);
+    if (p.mode == F8Problem::DEPTH) {
+        Group g = group_of(p.offsets, p.counts, part, p.K);
+        g.first &= ~(BLOCK - 1);  // (they are multiples of it)
+        w.K = min(g.count, p.K - g.first);
+        w.a.q += g.first;
+        w.b.q += g.first;
+        w.a.s += (g.first / BLOCK) * p.a.s_col;
+        w.b.s += (g.first / BLOCK) * p.b.s_col;
+        w.out.C = static_cast<char *>(w.out.C) + part * p.c_stack * (p.out.dtype == 0 ? 4 : 2);
+    }
+    return true;
+}
+// The row of A that row r of the work (0 .. used - 1) is made from
+__device__ __forceinline__ int64_t a_row(const F8Problem &p, const Work &w, int r) {
+    const int row = w.row0 + r;
+    if (p.slots == nullptr) return row;
+    return min(max(p.slots[row], 0) / p.top_k, p.a_rows - 1);
+}
+// Row tiles that ROWS can have at most: a part of one in each group, and what the rows fill
+inline int64_t most_row_tiles(const F8Problem &p, int height) {
+    if (p.mode != F8Problem::ROWS) return ((int64_t)p.M + height - 1) / height;
+    return (int64_t)p.M / height + (p.experts < p.M ? p.experts : p.M);
+}
+
+// Whether 4 columns from a multiple of 4 on are one aligned store in every row of every C
+inline bool c_wide(const F8Problem &p) {
+    const int size = p.out.dtype == 0 ? 4 : 2;
+    return (reinterpret_cast<uintptr_t>(p.out.C) % (4 * size)) == 0 && p.out.ldc % 4 == 0 && p.c_stack % 4 == 0;
+}
+
+// C elements: 4 consecutive columns of one row, of which the first `count` (at most 4) belong to C. `wide`:
+// C's rows are aligned for one store of 4.
+__device__ __forceinline__ float c_load(const F8Out &o, int64_t at) {
+    if (o.dtype == 0) return static_cast<const float *>(o.C)[at];
+    if (o.dtype == 1) return (float)static_cast<const __bf16 *>(o.C)[at];
+    return (float)static_cast<const _Float16 *>(o.C)[at];
+}
+__device__ __forceinline__ void c_store4(const F8Out &o, int64_t row, int col, int count, float alpha, float beta, mfma::f32x4 v,
+                                         bool wide) {
+    if (count <= 0) return;
+    const int64_t at = row * o.ldc + col;
+    v *= alpha;
+    if (beta != 0.0f) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < count) v[i] = fmaf(beta, c_load(o, at + i), v[i]);
+    }
+    if (o.dtype == 0) {
+        float *c = static_cast<float *>(o.C) + at;
+        if (wide && count >= 4) {
+            *reinterpret_cast<mfma::f32x4 *>(c) = v;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < count) c[i] = v[i];
+        }
+        return;
+    }
+    uint16_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        h[i] = o.dtype == 1 ? __builtin_bit_cast(uint16_t, (__bf16)v[i]) : __builtin_bit_cast(uint16_t, (_Float16)v[i]);
+    uint16_t *c = static_cast<uint16_t *>(o.C) + at;
+    if (wide && count >= 4) {
+        *reinterpret_cast<uint2 *>(c) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < count) c[i] = h[i];
+    }
+}
+
+}  // namespace f8
+}  // namespace regtile

@@ -53,6 +53,41 @@ struct MxConvert {
     int64_t lds;
 };
 
+// One operand of an 8-bit float product: element (i, k) of op(A) (of op(B)^T) at q[i * row + k * step]
+// (one of the two strides is 1), the scale of row i in block b of 128 k at s[(i >> shift) * s_row + b * s_col].
+struct F8Operand {
+    const uint8_t *q;
+    int64_t row, step;
+    const float *s;
+    int64_t s_row, s_col;
+    int shift;  // 0, or 7 for blocks of 128 x 128
+    int type;   // regtile_f8_type
+};
+// C in regtile_mx_dtype
+struct F8Out {
+    void *C;
+    int64_t ldc;
+    int dtype;
+};
+// One validated product of 8-bit float matrices: C (M x N) = alpha A (M x K) B (K x N) + beta C; with
+// `mode` ROWS the rows of C fall into groups, with a B for each (B of group e: q + e * b_stack, s +
+// e * bs_stack), and rows behind a group's count become zeros; with DEPTH the depth does, with a C for each
+// (K is then a group's; A and B begin at the group's column).
+struct F8Problem {
+    enum Mode { DENSE, ROWS, DEPTH } mode;
+    int M, N, K;
+    float alpha, beta;
+    F8Operand a, b;
+    F8Out out;
+    int experts;
+    int64_t b_stack, bs_stack, c_stack;
+    const int32_t *offsets, *counts;
+    const int32_t *slots;  // row r of A is token slots[r] / top_k (of a_rows), or null: row r
+    int top_k, a_rows;
+    void *work;
+    int64_t work_bytes;
+};
+
 // Every launch records the kernel it starts and its workgroup size just before launching it
 // (regtile_last_kernel_info queries that kernel's resources).
 void note_launch(const void *kernel, unsigned threads);
@@ -130,6 +165,74 @@ inline MxParts mx_parts(const MxProblem &p, int splits) {
 }
 // C = alpha (sum of the parts, in order) + beta C
 hipError_t launch_mx_join(const MxProblem &p, hipStream_t s, int splits);
+
+// 8-bit float matrices (f8_common.h). Conversions: X rows x cols of regtile_mx_dtype; with `transpose` the
+// matrix is X's transpose; with `index` row i of what is converted is row index[i] of X, zeros where that is
+// no row. q_rows x q_cols is the matrix's shape.
+struct F8Convert {
+    int dtype, type, block_rows, rows, cols, q_rows, q_cols;
+    bool transpose;
+    void *X;
+    int64_t ldx;
+    const int32_t *index;
+    uint8_t *Q;
+    int64_t ldq;
+    float *S;
+    int64_t s_row, s_col;
+};
+hipError_t launch_f8_quantize(const F8Convert &p, hipStream_t s, const char **name);
+hipError_t launch_f8_dequantize(const F8Convert &p, hipStream_t s, const char **name);
+// Products: the kernel that suits them, and the workspace that it would make use of
+hipError_t launch_f8(const F8Problem &p, hipStream_t s, const char **name);
+int64_t f8_work_bytes(const F8Problem &p);
+// any
+hipError_t launch_f8_any(const F8Problem &p, hipStream_t s, const char **name);
+
+// Routing (experts.hip)
+struct RouteProblem {
+    int tokens, experts, k, groups, top_groups, group_best, dtype;
+    bool sigmoid, renormalize;
+    float scale;
+    const void *logits;
+    int64_t ldl;
+    const float *bias;
+    int32_t *chosen;
+    float *weights;
+    const float *dweights;
+    void *dlogits;
+    int64_t ldd;
+};
+hipError_t launch_route(const RouteProblem &p, hipStream_t s, const char **name);
+hipError_t launch_route_grad(const RouteProblem &p, hipStream_t s, const char **name);
+struct OrderProblem {
+    const int32_t *chosen;
+    int tokens, k, experts, align, rows;
+    int32_t *slots, *position, *offsets, *counts;
+    int32_t *work;
+};
+int64_t order_work_bytes(int64_t slots, int experts);
+hipError_t launch_order(const OrderProblem &p, hipStream_t s, const char **name);
+struct CombineProblem {
+    int tokens, k, rows, n, dtype;
+    const int32_t *slots, *position;
+    const void *Y;
+    int64_t ldy;
+    const float *weights;
+    void *out;  // forward: tokens x n
+    int64_t ldo;
+    const void *dout;  // gradient
+    int64_t ldd;
+    void *dY;
+    int64_t lddy;
+    float *dweights;
+};
+hipError_t launch_combine(const CombineProblem &p, hipStream_t s, const char **name);
+hipError_t launch_combine_grad(const CombineProblem &p, hipStream_t s, const char **name);
+
+// regtile_last_kernel's name, and the status of a launch
+int finish(hipError_t err, const char *name);
+// Nothing was launched
+int quick(void);
 
 // The default 16-bit entry points take the split-K kernel for problems of few 64x64 tiles with
 // enough K per wave: at most 256 tiles (one per CU) with K >= 1024 in any storage order, and at
