@@ -1,0 +1,336 @@
+// gemm_f8_tile.h -- C = alpha A B + beta C for block-scaled 8-bit floats on LDS tiles fed by DMA: a row-major A
+// (rows may be gathered), B stored N x K or K x N, dense or in groups.
+//
+// A stage in LDS is one block of 128 k: BM + BN rows of 128 codes and as many scales. Two stages: while one is
+// multiplied the next is on its way, and one barrier a block hands over. A block's products are summed from
+// zero by the matrix instructions and enter the fp32 accumulators as c += (sa sb) sum, so the scales cost a
+// vector instruction for each of a lane's sums (two where B has a scale for each column), and the other wave
+// of the SIMD keeps the matrix pipe busy meanwhile. B's fragment is the first operand: a lane holds 4
+// consecutive columns of one row of C, and needs one scale of A.
+//
+// EXACT: sums of exact products, four 16x16x32 bf16 MFMAs on codes expanded in registers; else one
+// 16x16x128 8-bit MFMA at twice the rate (f8_common.h has what that loses).
+//
+// LDS: K-contiguous rows of 8 chunks of 16 codes, chunk c of row r at slot c ^ slab_key<8, 16>(r); a lane reads
+// chunks g and 4 + g (g = lane / 16), for both operands the same k. A K x N operand keeps its storage: rows
+// of BN codes at one k, read by transposing reads (8 k of 16 columns for 16 lanes), chunk c of row r at slot
+// c ^ nn_key(r), which spreads the 16 rows that 32 lanes read over all banks.
+//
+// Edges: rows past the last are loaded from the last, chunks past N from the last one that holds an element. What
+// lies past K in the last block (bytes between rows, or zeros from behind the descriptor) is overwritten with
+// zeros in LDS, in both operands: a code there may be a NaN.
+#pragma once
+
+#include <type_traits>
+
+#include "f8_common.h"
+
+namespace regtile {
+namespace f8 {
+using namespace mfma;
+typedef float __attribute__((may_alias)) f32_any;  // as lds_read16: no wait for DMA
+
+template <int BN>
+__device__ __forceinline__ int nn_key(int row) {
+    return BN == 256 ? (row & 7) | ((row >> 4) & 1) << 3 : ((row >> 1) & 3) | ((row >> 4) & 1) << 2;
+}
+
+// Transposing LDS read of 8-bit elements (ds_read_b64_tr_b8): in each group of 16 lanes, lane 2 j + h gives the
+// address of 8 bytes at columns 8 h .. 8 h + 7 of row j, and lane i receives column i of rows 0 .. 7 (measured).
+__device__ __forceinline__ u32x2 lds_read_tr8(const void *lds) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    typedef int v2i32 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) v2i32 *)lds));
+#else
+    (void)lds;
+    return u32x2{};
+#endif
+}
+
+// Two stages that the compiler knows to be apart: without it, it waits for all DMA under way before each
+// transposing read.
+template <typename F>
+__device__ __forceinline__ void apart(const uint8_t *__restrict__ cur, uint8_t *__restrict__ next, F f) {
+    f(cur, next);
+}
+
+// WM x WN waves of MI x NI fragments of 16 x 16. TA: A's type (B is e4m3). NN: B stored K x N. SB: B has a scale
+// for each column, else one for 128.
+template <int WM, int WN, int MI, int NI, bool EXACT, int TA, bool NN, bool SB>
+__global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, int tiles_m, int tiles_n, int per_split,
+                                                                                      bool wide) {
+    constexpr int WAVES = WM * WN, NT = 64 * WAVES, BM = WM * MI * 16, BN = WN * NI * 16;
+    constexpr int JA = BM / 8 / WAVES, JB = BN / 8 / WAVES;       // DMA instructions of a wave
+    constexpr int SC = (BM + BN) / 64;                            // waves' worth of scales
+    constexpr int STAGE = (BM + BN) * BLOCK + (SC > WAVES ? SC : WAVES) * 256;
+    static_assert(JA * 8 * WAVES == BM && JB * 8 * WAVES == BN && SC <= WAVES && NI * 16 <= BLOCK, "whole instructions");
+    __shared__ __align__(16) uint8_t smem[2 * STAGE];
+
+    const int tid = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int wm = wave / WN, wn = wave % WN;
+    int tm, tn;
+    const int id = xcd_contiguous_id(blockIdx.x, gridDim.x), tiles = tiles_m * tiles_n;
+    const int split = id / tiles;  // part of k, per_split blocks
+    grouped_tile<8>(id - split * tiles, tiles_m, tiles_n, tm, tn);
+    Work w;
+    if (!work_of(p, BM, tm, blockIdx.y, w)) return;
+    const int n0 = tn * BN;
+    const int K = w.used > 0 ? w.K : 0, all = (K + BLOCK - 1) / BLOCK;
+    const int first = split * per_split, blocks = min(per_split, all - first);
+    if ((int)gridDim.x > tiles) w.out.C = static_cast<float *>(w.out.C) + (int64_t)split * p.M * p.N;
+
+    f32x4 acc[MI][NI] = {};
+    if (blocks > 0) {
+        // ---- DMA ----
+        // Descriptors begin at the tile's first row (where rows are gathered: at A) and end behind the last chunk
+        // that holds an element; chunks past it arrive as zeros. Lanes hold offsets, the block's is uniform.
+        const bool gather = p.slots != nullptr;
+        auto span = [](int64_t rows, int64_t ld, int width) { return (uint32_t)((rows - 1) * ld + ((width + 15) & ~15)); };
+        const int n_rows = min(BN, p.N - n0);
+        const rsrc_t a_rsrc = make_rsrc(gather ? w.a.q : w.a.q + (int64_t)w.row0 * w.a.row,
+                                        span(gather ? p.a_rows : w.used, w.a.row, K));
+        const rsrc_t b_rsrc = NN ? make_rsrc(w.b.q + n0, span(K, w.b.step, p.N - n0))
+                                 : make_rsrc(w.b.q + (int64_t)n0 * w.b.row, span(n_rows, w.b.row, K));
+        uint32_t av[JA], bv[JB];
+#pragma unroll
+        for (int j = 0; j < JA; ++j) {
+            const int r = (wave * JA + j) * 8 + (lane >> 3), c = (lane & 7) ^ addr::slab_key<8, 16>(r), at = min(r, w.used - 1);
+            av[j] = (uint32_t)((gather ? a_row(p, w, at) : at) * w.a.row) + c * 16;
+        }
+#pragma unroll
+        for (int j = 0; j < JB; ++j) {
+            if constexpr (NN) {
+                constexpr int CH = BN / 16;
+                const int slot = (wave * JB + j) * 64 + lane, r = slot / CH, c = (slot % CH) ^ nn_key<BN>(r);
+                bv[j] = (uint32_t)(r * w.b.step) + min(c * 16, (n_rows - 1) & ~15);
+            } else {
+                const int r = (wave * JB + j) * 8 + (lane >> 3), c = (lane & 7) ^ addr::slab_key<8, 16>(r);
+                bv[j] = (uint32_t)(min(r, n_rows - 1) * w.b.row) + c * 16;
+            }
+        }
+        // scales: a wave brings 64 rows' of A or 64 columns' of B
+        static_assert(BM % 64 == 0, "a wave's scales are all of one operand");
+        const bool sa_wave = wave * 64 < BM || wave >= SC;
+        const int si = sa_wave ? min((wave < SC ? wave * 64 : 0) + lane, w.used - 1) : min(n0 + wave * 64 - BM + lane, p.N - 1);
+        const int64_t s_at = sa_wave ? (a_row(p, w, si) >> w.a.shift) * w.a.s_row : (int64_t)(si >> w.b.shift) * w.b.s_row;
+        const uint32_t sv = (uint32_t)(s_at * 4), s_step = (uint32_t)((sa_wave ? w.a.s_col : w.b.s_col) * 4);
+        const rsrc_t s_rsrc = make_rsrc(sa_wave ? w.a.s : w.b.s, 0x7FFFFFFFu);
+
+        constexpr int PIECES = JA + JB + 1;
+        // instruction n of a block's DMA; past the last block the last again, into the stage that is free then
+        auto dma = [&](int n, int block, uint8_t *to) {
+            const int kb = first + min(block, blocks - 1);
+            if (n < JA)
+                dma16_buf(a_rsrc, av[n], kb * BLOCK, to + (wave * JA + n) * 1024);
+            else if (n < JA + JB)
+                dma16_buf(b_rsrc, bv[n - JA], NN ? (uint32_t)(kb * BLOCK * w.b.step) : kb * BLOCK, to + BM * BLOCK + (wave * JB + n - JA) * 1024);
+            else
+                dma4_buf(s_rsrc, sv, kb * s_step, to + (BM + BN) * BLOCK + wave * 256);
+        };
+
+        // ---- one block ----
+        const int fr = lane & 15, fg = lane >> 4;
+        const int a_key = addr::slab_key<8, 16>(fr);
+        auto row_frag = [&](const uint8_t *s, int row) {
+            const uint8_t *at = s + row * BLOCK;
+            const u32x4 lo = lds_read16(at + (fg ^ a_key) * 16), hi = lds_read16(at + ((fg + 4) ^ a_key) * 16);
+            return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+        };
+        auto column_frag = [&](const uint8_t *s, int chunk) {
+            const int r = fg * 16 + (fr >> 1);
+            const uint8_t *at = s + r * BN + (chunk ^ nn_key<BN>(r)) * 16 + (fr & 1) * 8;
+            u32x2 v[4];
+#pragma unroll
+            for (int h = 0; h < 4; ++h) v[h] = lds_read_tr8(at + ((h >> 1) * 64 + (h & 1) * 8) * BN);
+            return i32x8{(int)v[0][0], (int)v[0][1], (int)v[1][0], (int)v[1][1], (int)v[2][0], (int)v[2][1], (int)v[3][0], (int)v[3][1]};
+        };
+        // A fragment as the matrix instructions take it: the codes, or expanded
+        struct Wide {
+            bf16x8 v[4];
+        };
+        typedef typename std::conditional<EXACT, Wide, i32x8>::type Frag;
+        auto frag = [](i32x8 q, auto type) -> Frag {
+            if constexpr (EXACT) {
+                constexpr int T = decltype(type)::value;
+                return Wide{{bf16_of8<T>(q[0], q[1]), bf16_of8<T>(q[2], q[3]), bf16_of8<T>(q[4], q[5]), bf16_of8<T>(q[6], q[7])}};
+            } else {
+                return q;
+            }
+        };
+        const std::integral_constant<int, TA> type_a{};
+        const std::integral_constant<int, 0> type_b{};
+
+        // Tiles are multiplied in the order of rows and columns of fragments, and each is added to its
+        // accumulator LAG tiles later, when its sum has left the matrix pipe. The sums of the last tiles of a
+        // block are added in the next one's time, with that block's factors.
+        constexpr int LAG = EXACT ? 1 : 2, RING = EXACT ? 2 : 4, TILES = MI * NI;
+        static_assert(TILES % RING == 0 && MI % 2 == 0 && NI > LAG, "a tile has one slot of the ring, a row one of two factors");
+        f32x4 d[RING];
+        i32x8 qa, qb[NI];    // codes that were read last
+        Frag a, b[NI];
+        float fa[2], sb_all; // row i's factor in fa[i % 2]; sb: of the block that is read
+        f32x4 sb[SB ? NI : 1], sb_now[SB ? NI : 1];
+        float sa_next;
+        auto read_a = [&](const uint8_t *s, int i) {
+            const int row = (wm * MI + i) * 16 + fr;
+            qa = row_frag(s, row);
+            sa_next = reinterpret_cast<const f32_any *>(s + (BM + BN) * BLOCK)[row];
+        };
+        auto read_b = [&](const uint8_t *s, int j) {
+            const f32_any *sc = reinterpret_cast<const f32_any *>(s + (BM + BN) * BLOCK) + BM + wn * NI * 16;
+            if constexpr (NN)
+                qb[j] = column_frag(s + BM * BLOCK, wn * NI + j);
+            else
+                qb[j] = row_frag(s + BM * BLOCK, (wn * NI + j) * 16 + fr);
+            if constexpr (SB)
+                sb[j] = __builtin_bit_cast(f32x4, lds_read16(sc + j * 16 + fg * 4));
+            else if (j == 0)
+                sb_all = sc[0];
+        };
+        auto add = [&](int t) {  // tile t of a block's
+            const int i = t / NI, j = t % NI;
+            const f32x4 &v = d[t % RING];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(v[e], SB ? fa[i & 1] * sb_now[j][e] : fa[i & 1], acc[i][j][e]);
+        };
+        auto tile = [&](int t) {
+            const int j = t % NI;
+            f32x4 &v = d[t % RING];
+            v = f32x4{};
+            if constexpr (EXACT) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j].v[q], a.v[q], v, 0, 0, 0);
+            } else {
+                v = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j], a, v, 0, TA, 0, 0, 0, 0);
+            }
+        };
+        // Between two barriers: the last row of fragments of block t - 1 (they are in registers), while block t's
+        // first are read from `cur`, then all rows of block t but the last. The other stage, `next`, takes
+        // block t + 1.
+        auto period = [&](int t, const uint8_t *cur, uint8_t *next, auto first_tag) {
+            constexpr bool FIRST = decltype(first_tag)::value;
+            constexpr int START = FIRST ? NI : 0;
+            if constexpr (FIRST) {
+#pragma unroll
+                for (int j = 0; j < NI; ++j) read_b(cur, j);
+                read_a(cur, 0);
+            }
+#pragma unroll
+            for (int n = START; n < TILES; ++n) {
+                const int i = n / NI - 1, j = n % NI;  // row -1: the last of block t - 1
+                const int id = i < 0 ? (MI - 1) * NI + j : i * NI + j;
+                if (j == 0) {  // the row's fragment has been read, and its factor
+                    a = frag(qa, type_a);
+                    fa[(id / NI) & 1] = SB ? sa_next : sa_next * sb_all;
+                }
+                if (i == 0) b[j] = frag(qb[j], type_b);
+                tile(id);
+                if (!FIRST || n - LAG >= START) add((id + TILES - LAG) % TILES);
+                if (SB && i == 0 && j == LAG - 1) {
+#pragma unroll
+                    for (int c = 0; c < NI; ++c) sb_now[c] = sb[c];
+                }
+                if (j == 0) read_a(cur, i + 1);
+                if (i < 0) read_b(cur, j);
+#pragma unroll
+                for (int m = 0; m < PIECES; ++m)
+                    if (m * (TILES - START) / PIECES + START == n) dma(m, t + 1, next);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        // zeros past K in the stage of the last block
+        auto clear = [&](uint8_t *s, int left) {
+            for (int c = tid; c < (NN ? BM : BM + BN) * 8; c += NT) {
+                const int r = c >> 3, kk = (c & 7) * 16;
+                if (kk + 16 <= left) continue;
+                u32x4 *at = reinterpret_cast<u32x4 *>(s + r * BLOCK + ((c & 7) ^ addr::slab_key<8, 16>(r)) * 16);
+                u32x4 v = *at;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int bytes = min(max(left - kk - 4 * i, 0), 4);
+                    v[i] &= bytes == 4 ? ~0u : (1u << 8 * bytes) - 1;
+                }
+                *at = v;
+            }
+            wait_lgkmcnt0();
+            lds_barrier();
+        };
+
+#pragma unroll
+        for (int n = 0; n < PIECES; ++n) dma(n, 0, smem);
+        auto arrive = [&](int t, uint8_t *cur) {
+            wait_vmcnt<0>();   // block t's DMA (of this wave) has landed,
+            wait_lgkmcnt0();   // and the last row of the block before has been read:
+            lds_barrier();     // of every wave
+            const int left = K - (first + t) * BLOCK;
+            if (left < BLOCK) clear(cur, left);
+        };
+        arrive(0, smem);
+        apart(smem, smem + STAGE, [&](const uint8_t *c, uint8_t *n) { period(0, c, n, std::true_type{}); });
+        for (int t = 1; t < blocks; ++t) {
+            uint8_t *cur = smem + (t & 1) * STAGE, *next = smem + (~t & 1) * STAGE;
+            arrive(t, cur);
+            apart(cur, next, [&](const uint8_t *c, uint8_t *n) { period(t, c, n, std::false_type{}); });
+        }
+        // the last row of the last block
+        a = frag(qa, type_a);
+        fa[(MI - 1) & 1] = SB ? sa_next : sa_next * sb_all;
+#pragma unroll
+        for (int n = 0; n < NI + LAG; ++n) {
+            const int id = (MI - 1) * NI + n;
+            if (n < NI) tile(id);
+            add(id - LAG);
+        }
+        wait_vmcnt<0>();  // no LDS DMA may still be in flight when the workgroup retires
+    }
+
+    // ---- epilogue ----
+    const int row0 = wm * MI * 16 + (lane & 15), col0 = wn * NI * 16 + (lane >> 4) * 4;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const int r = row0 + i * 16;
+        if (r >= w.rows) continue;
+        const bool used = r < w.used;
+#pragma unroll
+        for (int j = 0; j < NI; ++j) {
+            const int c = n0 + col0 + j * 16;
+            const f32x4 zero = {};
+            c_store4(w.out, w.row0 + r, c, min(p.N - c, 4), p.alpha, used ? p.beta : 0.0f, used ? acc[i][j] : zero, wide);
+        }
+    }
+}
+
+template <int WM, int WN, int MI, int NI, bool EXACT, int TA, bool NN, bool SB>
+hipError_t launch_tile(const F8Problem &p, hipStream_t s, int splits) {
+    constexpr int BM = WM * MI * 16, BN = WN * NI * 16, NT = 64 * WM * WN;
+    const int64_t tiles_m = most_row_tiles(p, BM), tiles_n = ((int64_t)p.N + BN - 1) / BN, grid = tiles_m * tiles_n * splits;
+    if (grid * NT > 0xFFFFFFFFll || p.experts > 65535) return hipErrorInvalidConfiguration;
+    const int blocks = (p.K + BLOCK - 1) / BLOCK, per = blocks > 0 ? (blocks + splits - 1) / splits : 1;
+    F8Problem q = p;
+    if (splits > 1) {  // parts of M x N fp32, joined by f8_join
+        q.out.C = p.work;
+        q.out.ldc = p.N;
+        q.out.dtype = 0;
+        q.alpha = 1.0f;
+        q.beta = 0.0f;
+    }
+    auto f = f8_tile_kernel<WM, WN, MI, NI, EXACT, TA, NN, SB>;
+    note_launch(reinterpret_cast<const void *>(f), NT);
+    hipLaunchKernelGGL(f, dim3((unsigned)grid, p.mode == F8Problem::DEPTH ? p.experts : 1), dim3(NT), 0, s, q, (int)tiles_m, (int)tiles_n,
+                       per, c_wide(q));
+    const hipError_t e = hipGetLastError();
+    return e == hipSuccess && splits > 1 ? launch_f8_join(p, s, splits) : e;
+}
+
+// A's type, B's storage and B's scales, from a problem that f8_tile_takes
+template <int WM, int WN, int MI, int NI, bool EXACT>
+hipError_t launch_tile_of(const F8Problem &p, hipStream_t s, int splits) {
+    const bool nn = p.b.step != 1, sb = p.b.shift == 0;
+    if (nn) return p.a.type ? launch_tile<WM, WN, MI, NI, EXACT, 1, true, false>(p, s, splits) : launch_tile<WM, WN, MI, NI, EXACT, 0, true, false>(p, s, splits);
+    if (sb) return p.a.type ? launch_tile<WM, WN, MI, NI, EXACT, 1, false, true>(p, s, splits) : launch_tile<WM, WN, MI, NI, EXACT, 0, false, true>(p, s, splits);
+    return p.a.type ? launch_tile<WM, WN, MI, NI, EXACT, 1, false, false>(p, s, splits) : launch_tile<WM, WN, MI, NI, EXACT, 0, false, false>(p, s, splits);
+}
+
+}  // namespace f8
+}  // namespace regtile

@@ -87,6 +87,19 @@ __device__ __forceinline__ void dma16_buf(rsrc_t r, uint32_t voff, uint32_t soff
 #endif
 }
 
+// 4 bytes per lane likewise, at `dst` + lane * 4
+__device__ __forceinline__ void dma4_buf(rsrc_t r, uint32_t voff, uint32_t soff, void *dst) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)dst, 4,
+                                             (int)voff, (int)soff, 0, 0);
+#else
+    (void)r;
+    (void)voff;
+    (void)soff;
+    (void)dst;
+#endif
+}
+
 // 8 bytes per lane at buffer byte offset voff + soff (soff wave-uniform); zero past the
 // descriptor's end.
 __device__ __forceinline__ uint2 load_b64_buf(rsrc_t r, uint32_t voff, uint32_t soff) {

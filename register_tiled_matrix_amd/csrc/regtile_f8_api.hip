@@ -387,11 +387,3 @@ int regtile_combine_experts_grad(const regtile_expert_rows *rows, int dtype, int
 }
 
 }  // extern "C"
-
-namespace regtile {
-hipError_t launch_f8(const F8Problem &p, hipStream_t s, const char **name) { return launch_f8_any(p, s, name); }
-int64_t f8_work_bytes(const F8Problem &p) {
-    (void)p;
-    return 0;
-}
-}  // namespace regtile
