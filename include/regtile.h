@@ -270,8 +270,9 @@ int64_t regtile_gemm_mx_workspace_ex(int format, int trans_a, int trans_b, int M
  *                           bytes and in floats
  *   rows, cols, stack       sizes; stack is 1 for a single matrix
  *   type, block_rows        regtile_f8_type; 1 or 128
- * No alignment is needed; the fast kernels want codes, ld and codes_stack to be multiples of 16. Products read
- * such rows in aligned chunks of 16 bytes: bytes behind a row's end that share a chunk with its last element may
+ * No alignment is needed; products of more than a few rows want codes, ld and codes_stack to be multiples of 16, and
+ * copy operands that are not into their workspace first (without one they are slow). Products read
+ * aligned rows in aligned chunks of 16 bytes: bytes behind a row's end that share a chunk with its last element may
  * be read, whatever they hold, and have no influence.
  */
 enum regtile_f8_type { REGTILE_F8_E4M3 = 0, REGTILE_F8_E5M2 = 1 };
@@ -377,19 +378,26 @@ int regtile_route_experts_grad(int score, int dtype, int tokens, int experts, in
  * regtile_gemm_f8_experts -- the experts' products: row r of C (rows->rows x N) in group e is alpha A[r] op(B_e) +
  * beta C[r], with A's row r, or with `gather` A's row for the token of slot r (A is then tokens x K). B is a stack
  * of rows->experts matrices. Rows between groups become 0; rows behind the last group's room stay as they are.
- *   rows (arg 1), gather (2), trans_b (3), alpha (4), A (5), B (6), beta (7), c_dtype (8), C, ldc (9-10), stream (11)
+ *   rows (arg 1), gather (2), trans_b (3), alpha (4), A (5), B (6), beta (7), c_dtype (8), C, ldc (9-10),
+ *   work, work_bytes (11-12) as for regtile_gemm_f8, stream (13)
  * regtile_gemm_f8_experts_dw -- the gradient of each expert's matrix: C_e = alpha A[:, group e] B[:, group e]^T +
  * beta C_e, with A (M x rows) and B (N x rows) quantised transposed, blocks along the rows; rows->align has to be a
  * multiple of 128. Columns behind a group's count are left out, whatever their codes (their blocks' scales have to
  * be finite).
  *   rows (arg 1), alpha (2), A (3), B (4), beta (5), c_dtype (6), C, ldc, c_stack (7-9: C_e at C + e * c_stack
- *   elements), stream (10)
+ *   elements), work, work_bytes (10-11), stream (12)
  * Accuracy as for regtile_gemm_f8.
  */
 int regtile_gemm_f8_experts(const regtile_expert_rows *rows, int gather, int trans_b, float alpha, const regtile_f8_matrix *A,
-                            const regtile_f8_matrix *B, float beta, int c_dtype, void *C, int ldc, void *stream);
+                            const regtile_f8_matrix *B, float beta, int c_dtype, void *C, int ldc, void *work, int64_t work_bytes,
+                            void *stream);
 int regtile_gemm_f8_experts_dw(const regtile_expert_rows *rows, float alpha, const regtile_f8_matrix *A, const regtile_f8_matrix *B,
-                               float beta, int c_dtype, void *C, int ldc, int64_t c_stack, void *stream);
+                               float beta, int c_dtype, void *C, int ldc, int64_t c_stack, void *work, int64_t work_bytes,
+                               void *stream);
+int64_t regtile_gemm_f8_experts_workspace(const regtile_expert_rows *rows, int gather, int trans_b, const regtile_f8_matrix *A,
+                                          const regtile_f8_matrix *B, int c_dtype);
+int64_t regtile_gemm_f8_experts_dw_workspace(const regtile_expert_rows *rows, const regtile_f8_matrix *A, const regtile_f8_matrix *B,
+                                             int c_dtype);
 
 /*
  * regtile_combine_experts -- out[t] = sum_j w[t, j] Y[position[t, j]], fp32 sums in the order of j; slots without a

@@ -70,6 +70,7 @@ EXPORTED_SYMBOLS = ("gemm_f32", "gemm_bf16", "gemm_f16", "regtile_gemm_f32_algo"
                     "regtile_version", "regtile_quantize_f8", "regtile_dequantize_f8", "regtile_gemm_f8",
                     "regtile_gemm_f8_workspace", "regtile_expert_rows_size", "regtile_order_experts",
                     "regtile_order_experts_workspace", "regtile_gemm_f8_experts", "regtile_gemm_f8_experts_dw",
+                    "regtile_gemm_f8_experts_workspace", "regtile_gemm_f8_experts_dw_workspace",
                     "regtile_route_experts", "regtile_route_experts_grad", "regtile_combine_experts",
                     "regtile_combine_experts_grad")
 

@@ -38,8 +38,8 @@ def declare(lib):
     for name, args in (("regtile_quantize_f8", [I, I, I, I, P, I, P, P, P]), ("regtile_dequantize_f8", [P, I, P, I, P]),
                        ("regtile_gemm_f8", [I, I, F, P, P, F, I, P, I, P, L, P]),
                        ("regtile_order_experts", [P, P, P, L, P]),
-                       ("regtile_gemm_f8_experts", [P, I, I, F, P, P, F, I, P, I, P]),
-                       ("regtile_gemm_f8_experts_dw", [P, F, P, P, F, I, P, I, L, P]),
+                       ("regtile_gemm_f8_experts", [P, I, I, F, P, P, F, I, P, I, P, L, P]),
+                       ("regtile_gemm_f8_experts_dw", [P, F, P, P, F, I, P, I, L, P, L, P]),
                        ("regtile_route_experts", [I] * 9 + [F, P, I, P, P, P, P]),
                        ("regtile_route_experts_grad", [I] * 6 + [F, P, I, P, P, P, I, P]),
                        ("regtile_combine_experts", [P, I, I, P, I, P, P, I, P]),
@@ -48,6 +48,7 @@ def declare(lib):
         f.argtypes = args
         f.restype = I
     for name, args in (("regtile_gemm_f8_workspace", [I, I, P, P, I, I]), ("regtile_expert_rows_size", [I] * 4),
+                       ("regtile_gemm_f8_experts_workspace", [P, I, I, P, P, I]), ("regtile_gemm_f8_experts_dw_workspace", [P, P, P, I]),
                        ("regtile_order_experts_workspace", [I] * 3)):
         f = getattr(lib, name)
         f.argtypes = args
@@ -264,6 +265,14 @@ def _c_of(C, dtype, beta, shape, device):
     return dtype, dt, ldc
 
 
+def _workspace(A, size):
+    """(tensor, address, bytes): the tensor has to stay until the launch is queued."""
+    if size <= 0:
+        return None, None, 0
+    work = A.codes.new_empty(size, dtype=_torch.uint8)
+    return work, work.data_ptr(), size
+
+
 def gemm_f8(A, B, C=None, alpha=1.0, beta=0.0, dtype=None, stream=None):
     """C = alpha*A@B + beta*C; F8Matrix A (M x K) and B (K x N), a row-major C of ``dtype`` (float32, the default, or
     bfloat16 or float16; C's, if it is given); returns C (allocated when None). Scales have to run along k: with
@@ -281,11 +290,8 @@ def _run_gemm(A, B, C, alpha, beta, dtype, dt, M, N, ldc, handle):
     if C is None:
         C = A.codes.new_empty((M, N), dtype=dtype)
     ta, tb = (1 if A.transposed else 0), (1 if B.transposed else 0)
-    at, work = None, None
-    size = lib.regtile_gemm_f8_workspace(ta, tb, A._at, B._at, dt, ldc)
-    if size > 0:
-        work = A.codes.new_empty(size, dtype=_torch.uint8)  # stays until the launch is queued
-        at = work.data_ptr()
+    # (a few rows go without)
+    work, at, size = _workspace(A, 0 if M <= 16 and tb else lib.regtile_gemm_f8_workspace(ta, tb, A._at, B._at, dt, ldc))
     status = lib.regtile_gemm_f8(ta, tb, alpha, A._at, B._at, beta, dt, C.data_ptr(), ldc, at, size, handle)
     if status:
         _rt._check(status)
@@ -460,8 +466,9 @@ def gemm_f8_experts(A, B, rows, C=None, gather=False, alpha=1.0, beta=0.0, dtype
 def _run_experts(A, B, rows, C, gather, alpha, beta, dtype, dt, N, ldc, handle):
     if C is None:
         C = A.codes.new_empty((rows.rows, N), dtype=dtype)
-    status = _lib().regtile_gemm_f8_experts(rows._at, gather, 1 if B.transposed else 0, alpha, A._at, B._at, beta, dt, C.data_ptr(), ldc,
-                                            handle)
+    lib, tb = _lib(), 1 if B.transposed else 0
+    work, at, size = _workspace(A, lib.regtile_gemm_f8_experts_workspace(rows._at, gather, tb, A._at, B._at, dt))
+    status = lib.regtile_gemm_f8_experts(rows._at, gather, tb, alpha, A._at, B._at, beta, dt, C.data_ptr(), ldc, at, size, handle)
     if status:
         _rt._check(status)
     return C
@@ -489,7 +496,9 @@ def gemm_f8_experts_dw(A, B, rows, C=None, alpha=1.0, beta=0.0, dtype=None, stre
 def _run_experts_dw(A, B, rows, C, alpha, beta, dtype, dt, M, N, ldc, handle):
     if C is None:
         C = A.codes.new_empty((rows.experts, M, N), dtype=dtype)
-    status = _lib().regtile_gemm_f8_experts_dw(rows._at, alpha, A._at, B._at, beta, dt, C.data_ptr(), ldc, C.stride(0), handle)
+    lib = _lib()
+    work, at, size = _workspace(A, lib.regtile_gemm_f8_experts_dw_workspace(rows._at, A._at, B._at, dt))
+    status = lib.regtile_gemm_f8_experts_dw(rows._at, alpha, A._at, B._at, beta, dt, C.data_ptr(), ldc, C.stride(0), at, size, handle)
     if status:
         _rt._check(status)
     return C

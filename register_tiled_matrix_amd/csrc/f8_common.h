@@ -58,6 +58,34 @@ __device__ __forceinline__ f32x2 f32_pair(int type, uint32_t codes) {
 #endif
 }
 
+// 16 codes at `p`, of which the first `left` belong to the row and the rest become 0; `have` codes of the row lie before p
+__device__ __forceinline__ mfma::u32x4 load16(const uint8_t *p, int left, int have) {
+    mfma::u32x4 v = {};
+    if (left >= 16) {
+        __builtin_memcpy(&v, p, 16);
+    } else if (left > 0) {
+        if (have + left >= 16) {  // the 16 that end where the row ends, moved down
+            uint64_t lo, hi;
+            __builtin_memcpy(&lo, p + left - 16, 8);
+            __builtin_memcpy(&hi, p + left - 8, 8);
+            const int s = 8 * (16 - left);
+            if (s >= 64) {
+                lo = hi >> (s - 64);
+                hi = 0;
+            } else {
+                lo = lo >> s | hi << (64 - s);
+                hi >>= s;
+            }
+            v = mfma::u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (i < left) v[i / 4] |= (uint32_t)p[i] << (8 * (i & 3));
+        }
+    }
+    return v;
+}
+
 // Where group e of `rows` begins, its used rows and its room, kept inside the matrix whatever the arrays hold.
 struct Group {
     int first, count, room;

@@ -33,14 +33,62 @@ __global__ __launch_bounds__(JOIN_NT) void f8_join_kernel(F8Problem p, int split
 
 constexpr int64_t SPAN = int64_t(1) << 31;  // bytes that a descriptor's offsets may reach
 
-// What the DMA-fed tiles take: K-contiguous A, e4m3 B, aligned rows, and operands within the reach of a tile's
-// descriptors
+// Rows that DMA reads begin at multiples of 16 bytes; operands that lie otherwise are copied into a workspace first.
+bool a_aligned(const F8Problem &p) { return aligned16(p.a.q) && p.a.row % 16 == 0; }
+bool b_aligned(const F8Problem &p) { return aligned16(p.b.q) && (p.b.step != 1 ? p.b.step : p.b.row) % 16 == 0 && p.b_stack % 16 == 0; }
+
+// A's and B's stored matrices: rows, columns, how many
+struct Stored {
+    int64_t rows, cols, count;
+    int64_t ld() const { return (cols + 15) / 16 * 16; }
+    int64_t bytes() const { return rows * ld() * count; }
+};
+Stored stored_a(const F8Problem &p) { return {p.slots != nullptr ? p.a_rows : p.M, p.K, 1}; }
+Stored stored_b(const F8Problem &p) {
+    const int64_t count = p.mode == F8Problem::ROWS ? p.experts : 1;
+    return p.b.step != 1 ? Stored{p.K, p.N, count} : Stored{p.N, p.K, count};
+}
+
+// One matrix (or stack) to aligned rows: 16 bytes a thread, a row of threads along each row; what lies behind a
+// row's end up to a multiple of 16 becomes 0.
+struct Copy {
+    const uint8_t *from;
+    uint8_t *to;
+    int64_t ld, stack, to_ld;
+    int64_t rows, cols, count;
+};
+constexpr int COPY_NT = 256;
+__global__ __launch_bounds__(COPY_NT) void f8_align_kernel(Copy c0, Copy c1, int z1, int across) {
+    const bool second = (int)blockIdx.z >= z1;
+    const Copy c = second ? c1 : c0;
+    const int z = second ? blockIdx.z - z1 : blockIdx.z, nz = second ? gridDim.z - z1 : z1;
+    const int tx = threadIdx.x % across, ty = threadIdx.x / across;
+    for (int64_t e = z; e < c.count; e += nz)
+        for (int64_t r = (int64_t)blockIdx.x * (COPY_NT / across) + ty; r < c.rows; r += (int64_t)gridDim.x * (COPY_NT / across)) {
+            const uint8_t *from = c.from + e * c.stack + r * c.ld;
+            uint8_t *to = c.to + (e * c.rows + r) * c.to_ld;
+            for (int64_t k = ((int64_t)blockIdx.y * across + tx) * 16; k < c.cols; k += (int64_t)gridDim.y * across * 16)
+                *reinterpret_cast<mfma::u32x4 *>(to + k) = load16(from + k, (int)min(c.cols - k, (int64_t)16), (int)min(k, (int64_t)16));
+        }
+}
+// Copies of one or two operands (count 0: none), in one launch
+hipError_t align_rows(const Copy &a, const Copy &b, hipStream_t s) {
+    const int64_t cols = a.cols > b.cols ? a.cols : b.cols, rows = a.rows > b.rows ? a.rows : b.rows, units = (cols + 15) / 16;
+    int across = COPY_NT;
+    while (across > 8 && across / 2 >= units) across /= 2;
+    const int64_t gx = (rows * across + COPY_NT - 1) / COPY_NT, gy = (units + across - 1) / across;
+    const int za = (int)(a.count < 1024 ? a.count : 1024), zb = (int)(b.count < 1024 ? b.count : 1024);
+    hipLaunchKernelGGL(f8_align_kernel, dim3((unsigned)(gx < (1 << 16) ? gx : 1 << 16), (unsigned)(gy < 64 ? gy : 64), (unsigned)(za + zb)),
+                       dim3(COPY_NT), 0, s, a, b, za, across);
+    return hipGetLastError();
+}
+
+// What the tiles take: K-contiguous A, e4m3 B, and operands within the reach of a tile's 32-bit offsets
 bool tile_takes(const F8Problem &p) {
     const F8Operand &a = p.a, &b = p.b;
     const bool nn = b.step != 1;
     const int64_t ldb = nn ? b.step : b.row, kb = ((int64_t)p.K + BLOCK - 1) / BLOCK;
     if (a.step != 1 || b.type != REGTILE_F8_E4M3) return false;
-    if (!aligned16(a.q) || !aligned16(b.q) || a.row % 16 != 0 || ldb % 16 != 0 || p.b_stack % 16 != 0) return false;
     const int64_t rows_a = p.slots != nullptr ? p.a_rows : 256;
     if (rows_a * a.row + p.K + BLOCK >= SPAN || (nn ? ((int64_t)p.K + BLOCK) * ldb + 256 : 256 * ldb + p.K + BLOCK) >= SPAN) return false;
     const int64_t all_a = p.slots != nullptr ? p.a_rows : p.M;
@@ -48,26 +96,42 @@ bool tile_takes(const F8Problem &p) {
 }
 
 struct Plan {
-    enum { ANY, TILE_128, TILE_WIDE, TILE_256 } kernel;
+    enum { ANY, TILE_128, TILE_WIDE, TILE_256, TOKEN, TILE_DEEP } kernel;
+    int shape;
     bool exact;
-    int parts;  // of k, through the workspace
+    int parts;     // of k, through the workspace
+    bool copy_a, copy_b;  // operands that it needs copies of
+    int64_t copy_bytes;
 };
 
 Plan plan_of(const F8Problem &p) {
-    Plan plan = {Plan::ANY, p.out.dtype == 0, 1};
+    Plan plan = {Plan::ANY, 0, p.out.dtype == 0, 1, false, false, 0};
     if (!tile_takes(p)) return plan;
+    const bool dense = p.mode == F8Problem::DENSE, rows = p.mode == F8Problem::ROWS;
+    // Few rows (in a group, on the average): codes straight to registers
+    const int64_t weights = (int64_t)p.N * p.K, group = rows ? p.M / p.experts : p.M;
+    if (p.b.step == 1 && (dense || rows)) {
+        plan.kernel = Plan::TOKEN;
+        if (dense && p.M <= 16) return plan.shape = 11, plan;
+        if (dense && p.M <= 32 && weights <= 1 << 25) return plan.shape = 21, plan;
+        if (dense && p.M <= 64 && weights <= 1 << 25) return plan.shape = 22, plan;
+        if (rows && group <= (b_aligned(p) ? 12 : 48)) return plan.shape = 12, plan;
+    }
+    plan.copy_a = !a_aligned(p);
+    plan.copy_b = !b_aligned(p);
+    plan.copy_bytes = (plan.copy_a ? stored_a(p).bytes() : 0) + (plan.copy_b ? stored_b(p).bytes() : 0);
     const int64_t tiles256 = most_row_tiles(p, 256) * (((int64_t)p.N + 255) / 256);
-    const int64_t tiles128 = most_row_tiles(p, 128) * (((int64_t)p.N + 127) / 128) * (p.mode == F8Problem::DEPTH ? p.experts : 1);
-    // 256 x 256 tiles run one to a CU: with fewer than 192 too many of the 256 CUs are idle (2048^3, 64 tiles: 35.3 us
-    // against 20.9; 4096 x 4096 x 8192, 256 tiles: 130 against 161)
-    if (!plan.exact && p.b.shift != 0 && tiles256 >= 192 && p.mode != F8Problem::ROWS) {
+    const int64_t tiles128 = most_row_tiles(p, 128) * (((int64_t)p.N + 127) / 128);
+    plan.kernel = Plan::TILE_128;
+    // 256 x 256 tiles run one to a CU: with fewer than 192 too many of the 256 CUs are idle (2048^3, 64 tiles: 35.3
+    // us against 20.9; 4096 x 4096 x 8192, 256 tiles: 130 against 161)
+    if (!plan.exact && p.b.shift != 0 && tiles256 >= 192 && (!rows || group >= 256)) {
         plan.kernel = Plan::TILE_256;
         return plan;
     }
-    plan.kernel = Plan::TILE_128;
     // two 128 x 128 tiles run on a CU: fewer than 512 of them go in parts of at least 1024 k (1024 x 1024 x 8192, 64
     // tiles: 63.9 us whole, 27.4 in 4 parts, 27.2 in 8; 2048 x 2048 x 2048: 20.9 whole, 28.7 in 2)
-    if (p.mode == F8Problem::DENSE) {
+    if (dense) {
         const int64_t blocks = ((int64_t)p.K + BLOCK - 1) / BLOCK, fill = 512 / tiles128;
         plan.parts = (int)(fill < blocks / 8 ? fill : blocks / 8);
         if (plan.parts < 1 || (tiles128 >= 256 && blocks < 32)) plan.parts = 1;
@@ -78,19 +142,48 @@ Plan plan_of(const F8Problem &p) {
 }  // namespace
 
 int64_t f8_work_bytes(const F8Problem &p) {
-    const int parts = plan_of(p).parts;
-    return parts > 1 ? (int64_t)parts * p.M * p.N * 4 : 0;
+    const Plan plan = plan_of(p);
+    return plan.copy_bytes + (plan.parts > 1 ? (int64_t)plan.parts * p.M * p.N * 4 : 0);
 }
 
-hipError_t launch_f8(const F8Problem &p, hipStream_t s, const char **name) {
-    Plan plan = plan_of(p);
+hipError_t launch_f8(const F8Problem &given, hipStream_t s, const char **name) {
+    Plan plan = plan_of(given);
+    F8Problem p = given;
+    if (plan.copy_bytes > p.work_bytes) return launch_f8_any(p, s, name);  // no room for them
+    uint8_t *work = static_cast<uint8_t *>(p.work);
+    Copy copies[2] = {};
+    if (plan.copy_a) {
+        const Stored m = stored_a(p);
+        copies[0] = {p.a.q, work, p.a.row, 0, m.ld(), m.rows, m.cols, 1};
+        p.a.q = work;
+        p.a.row = m.ld();
+        work += m.bytes();
+    }
+    if (plan.copy_b) {
+        const Stored m = stored_b(p);
+        int64_t &ld = p.b.step != 1 ? p.b.step : p.b.row;
+        copies[1] = {p.b.q, work, ld, p.b_stack, m.ld(), m.rows, m.cols, m.count};
+        p.b.q = work;
+        p.b_stack = m.rows * m.ld();
+        ld = m.ld();
+        work += m.bytes();
+    }
+    if (plan.copy_bytes > 0) {
+        const hipError_t e = align_rows(copies[0], copies[1], s);
+        if (e != hipSuccess) return e;
+    }
+    p.work = work;
+    p.work_bytes -= plan.copy_bytes;
     while (plan.parts > 1 && (int64_t)plan.parts * p.M * p.N * 4 > p.work_bytes) --plan.parts;
     static const char *const wide[2] = {"f8_tile_256x128", "f8_tile_256x128_exact"};
     static const char *const small[2] = {"f8_tile_128x128", "f8_tile_128x128_exact"};
+    static const char *const deep[2] = {"f8_tile_128x128_deep", "f8_tile_128x128_deep_exact"};
     switch (plan.kernel) {
         case Plan::TILE_256: *name = "f8_tile_256x256"; return launch_f8_tile_256(p, s);
         case Plan::TILE_WIDE: *name = wide[plan.exact]; return launch_f8_tile_wide(p, plan.exact, s, plan.parts);
         case Plan::TILE_128: *name = small[plan.exact]; return launch_f8_tile_128(p, plan.exact, s, plan.parts);
+        case Plan::TILE_DEEP: *name = deep[plan.exact]; return launch_f8_tile_deep(p, plan.exact, s, plan.parts);
+        case Plan::TOKEN: *name = "f8_token"; return launch_f8_token(p, plan.shape, s);
         default: return launch_f8_any(p, s, name);
     }
 }

@@ -1,8 +1,9 @@
 // gemm_f8_tile.h -- C = alpha A B + beta C for block-scaled 8-bit floats on LDS tiles fed by DMA: a row-major A
 // (rows may be gathered), B stored N x K or K x N, dense or in groups.
 //
-// A stage in LDS is one block of 128 k: BM + BN rows of 128 codes and as many scales. Two stages: while one is
-// multiplied the next is on its way, and one barrier a block hands over. A block's products are summed from
+// A stage in LDS is one block of 128 k: BM + BN rows of 128 codes and as many scales. While one is
+// multiplied the next STAGES - 1 are on their way, and one barrier a block hands over. Two stages let two workgroups of
+// 128 x 128 share a CU; with too few tiles for that, four hide the latency of memory better (DESIGN_FIGURE). A block's products are summed from
 // zero by the matrix instructions and enter the fp32 accumulators as c += (sa sb) sum, so the scales cost a
 // vector instruction for each of a lane's sums (two where B has a scale for each column), and the other wave
 // of the SIMD keeps the matrix pipe busy meanwhile. B's fragment is the first operand: a lane holds 4
@@ -56,7 +57,7 @@ __device__ __forceinline__ void apart(const uint8_t *__restrict__ cur, uint8_t *
 
 // WM x WN waves of MI x NI fragments of 16 x 16. TA: A's type (B is e4m3). NN: B stored K x N. SB: B has a scale
 // for each column, else one for 128.
-template <int WM, int WN, int MI, int NI, bool EXACT, int TA, bool NN, bool SB>
+template <int WM, int WN, int MI, int NI, int STAGES, bool EXACT, int TA, bool NN, bool SB>
 __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, int tiles_m, int tiles_n, int per_split,
                                                                                       bool wide) {
     constexpr int WAVES = WM * WN, NT = 64 * WAVES, BM = WM * MI * 16, BN = WN * NI * 16;
@@ -64,7 +65,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
     constexpr int SC = (BM + BN) / 64;                            // waves' worth of scales
     constexpr int STAGE = (BM + BN) * BLOCK + (SC > WAVES ? SC : WAVES) * 256;
     static_assert(JA * 8 * WAVES == BM && JB * 8 * WAVES == BN && SC <= WAVES && NI * 16 <= BLOCK, "whole instructions");
-    __shared__ __align__(16) uint8_t smem[2 * STAGE];
+    __shared__ __align__(16) uint8_t smem[STAGES * STAGE];
 
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -167,15 +168,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
         constexpr int LAG = EXACT ? 1 : 2, RING = EXACT ? 2 : 4, TILES = MI * NI;
         static_assert(TILES % RING == 0 && MI % 2 == 0 && NI > LAG, "a tile has one slot of the ring, a row one of two factors");
         f32x4 d[RING];
-        i32x8 qa, qb[NI];    // codes that were read last
+        i32x8 qa[2], qb[NI];  // codes that have been read: of the next two rows (row i in qa[i % 2]), of the next block's columns
         Frag a, b[NI];
-        float fa[2], sb_all; // row i's factor in fa[i % 2]; sb: of the block that is read
-        f32x4 sb[SB ? NI : 1], sb_now[SB ? NI : 1];
-        float sa_next;
+        float fa[2], sb_all; // row i's factor in fa[i % 2]; sb_all: of the block that is read, sb: of the one that is added
+        f32x4 sb[SB ? NI : 1];
+        float sa_next[2];
         auto read_a = [&](const uint8_t *s, int i) {
             const int row = (wm * MI + i) * 16 + fr;
-            qa = row_frag(s, row);
-            sa_next = reinterpret_cast<const f32_any *>(s + (BM + BN) * BLOCK)[row];
+            qa[i & 1] = row_frag(s, row);
+            sa_next[i & 1] = reinterpret_cast<const f32_any *>(s + (BM + BN) * BLOCK)[row];
         };
         auto read_b = [&](const uint8_t *s, int j) {
             const f32_any *sc = reinterpret_cast<const f32_any *>(s + (BM + BN) * BLOCK) + BM + wn * NI * 16;
@@ -183,16 +184,18 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
                 qb[j] = column_frag(s + BM * BLOCK, wn * NI + j);
             else
                 qb[j] = row_frag(s + BM * BLOCK, (wn * NI + j) * 16 + fr);
-            if constexpr (SB)
-                sb[j] = __builtin_bit_cast(f32x4, lds_read16(sc + j * 16 + fg * 4));
-            else if (j == 0)
-                sb_all = sc[0];
+            if (!SB && j == 0) sb_all = sc[0];
+        };
+        auto read_sb = [&](const uint8_t *s) {
+            const f32_any *sc = reinterpret_cast<const f32_any *>(s + (BM + BN) * BLOCK) + BM + wn * NI * 16;
+#pragma unroll
+            for (int j = 0; j < (SB ? NI : 0); ++j) sb[j] = __builtin_bit_cast(f32x4, lds_read16(sc + j * 16 + fg * 4));
         };
         auto add = [&](int t) {  // tile t of a block's
             const int i = t / NI, j = t % NI;
             const f32x4 &v = d[t % RING];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(v[e], SB ? fa[i & 1] * sb_now[j][e] : fa[i & 1], acc[i][j][e]);
+            for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(v[e], SB ? fa[i & 1] * sb[j][e] : fa[i & 1], acc[i][j][e]);
         };
         auto tile = [&](int t) {
             const int j = t % NI;
@@ -205,37 +208,37 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
                 v = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b[j], a, v, 0, TA, 0, 0, 0, 0);
             }
         };
-        // Between two barriers: the last row of fragments of block t - 1 (they are in registers), while block t's
-        // first are read from `cur`, then all rows of block t but the last. The other stage, `next`, takes
-        // block t + 1.
+        // Row `id / NI` begins: its fragment and its factor have been read
+        auto begin_row = [&](int i) {
+            a = frag(qa[i & 1], type_a);
+            fa[i & 1] = SB ? sa_next[i & 1] : sa_next[i & 1] * sb_all;
+        };
+        // Between two barriers: the last two rows of fragments of block t - 1 (they are in registers), while block t's
+        // first are read from `cur`, then all rows of block t but the last two. Rows are read two ahead. The other
+        // stage, `next`, takes block t + STAGES - 1.
         auto period = [&](int t, const uint8_t *cur, uint8_t *next, auto first_tag) {
             constexpr bool FIRST = decltype(first_tag)::value;
-            constexpr int START = FIRST ? NI : 0;
+            constexpr int START = FIRST ? 2 * NI : 0;
             if constexpr (FIRST) {
 #pragma unroll
                 for (int j = 0; j < NI; ++j) read_b(cur, j);
                 read_a(cur, 0);
+                read_a(cur, 1);
             }
 #pragma unroll
             for (int n = START; n < TILES; ++n) {
-                const int i = n / NI - 1, j = n % NI;  // row -1: the last of block t - 1
-                const int id = i < 0 ? (MI - 1) * NI + j : i * NI + j;
-                if (j == 0) {  // the row's fragment has been read, and its factor
-                    a = frag(qa, type_a);
-                    fa[(id / NI) & 1] = SB ? sa_next : sa_next * sb_all;
-                }
+                const int i = n / NI - 2, j = n % NI;  // rows -2 and -1: the last of block t - 1
+                const int id = ((i + MI) % MI) * NI + j;
+                if (j == 0) begin_row(id / NI);
                 if (i == 0) b[j] = frag(qb[j], type_b);
                 tile(id);
                 if (!FIRST || n - LAG >= START) add((id + TILES - LAG) % TILES);
-                if (SB && i == 0 && j == LAG - 1) {
-#pragma unroll
-                    for (int c = 0; c < NI; ++c) sb_now[c] = sb[c];
-                }
-                if (j == 0) read_a(cur, i + 1);
-                if (i < 0) read_b(cur, j);
+                if (SB && i == 0 && j == LAG - 1) read_sb(cur);  // (the block before has been added)
+                if (j == 0) read_a(cur, i + 2);
+                if (i == -1) read_b(cur, j);
 #pragma unroll
                 for (int m = 0; m < PIECES; ++m)
-                    if (m * (TILES - START) / PIECES + START == n) dma(m, t + 1, next);
+                    if (m * (TILES - START) / PIECES + START == n) dma(m, t + STAGES - 1, next);
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
@@ -258,28 +261,29 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
         };
 
 #pragma unroll
-        for (int n = 0; n < PIECES; ++n) dma(n, 0, smem);
+        for (int t = 0; t < STAGES - 1; ++t)
+#pragma unroll
+            for (int n = 0; n < PIECES; ++n) dma(n, t, smem + t * STAGE);
         auto arrive = [&](int t, uint8_t *cur) {
-            wait_vmcnt<0>();   // block t's DMA (of this wave) has landed,
-            wait_lgkmcnt0();   // and the last row of the block before has been read:
-            lds_barrier();     // of every wave
+            wait_vmcnt<(STAGES - 2) * PIECES>();  // block t's DMA (of this wave) has landed, STAGES - 2 blocks are younger,
+            wait_lgkmcnt0();                      // and the last rows of the block before have been read:
+            lds_barrier();                        // of every wave
             const int left = K - (first + t) * BLOCK;
             if (left < BLOCK) clear(cur, left);
         };
         arrive(0, smem);
-        apart(smem, smem + STAGE, [&](const uint8_t *c, uint8_t *n) { period(0, c, n, std::true_type{}); });
+        apart(smem, smem + (STAGES - 1) * STAGE, [&](const uint8_t *c, uint8_t *n) { period(0, c, n, std::true_type{}); });
         for (int t = 1; t < blocks; ++t) {
-            uint8_t *cur = smem + (t & 1) * STAGE, *next = smem + (~t & 1) * STAGE;
+            uint8_t *cur = smem + (t % STAGES) * STAGE, *next = smem + ((t - 1) % STAGES) * STAGE;
             arrive(t, cur);
             apart(cur, next, [&](const uint8_t *c, uint8_t *n) { period(t, c, n, std::false_type{}); });
         }
-        // the last row of the last block
-        a = frag(qa, type_a);
-        fa[(MI - 1) & 1] = SB ? sa_next : sa_next * sb_all;
+        // the last two rows of the last block
 #pragma unroll
-        for (int n = 0; n < NI + LAG; ++n) {
-            const int id = (MI - 1) * NI + n;
-            if (n < NI) tile(id);
+        for (int n = 0; n < 2 * NI + LAG; ++n) {
+            const int id = (MI - 2) * NI + n;
+            if (n < 2 * NI && n % NI == 0) begin_row(id / NI);
+            if (n < 2 * NI) tile(id);
             add(id - LAG);
         }
         wait_vmcnt<0>();  // no LDS DMA may still be in flight when the workgroup retires
@@ -301,7 +305,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
     }
 }
 
-template <int WM, int WN, int MI, int NI, bool EXACT, int TA, bool NN, bool SB>
+template <int WM, int WN, int MI, int NI, int STAGES, bool EXACT, int TA, bool NN, bool SB>
 hipError_t launch_tile(const F8Problem &p, hipStream_t s, int splits) {
     constexpr int BM = WM * MI * 16, BN = WN * NI * 16, NT = 64 * WM * WN;
     const int64_t tiles_m = most_row_tiles(p, BM), tiles_n = ((int64_t)p.N + BN - 1) / BN, grid = tiles_m * tiles_n * splits;
@@ -315,7 +319,7 @@ hipError_t launch_tile(const F8Problem &p, hipStream_t s, int splits) {
         q.alpha = 1.0f;
         q.beta = 0.0f;
     }
-    auto f = f8_tile_kernel<WM, WN, MI, NI, EXACT, TA, NN, SB>;
+    auto f = f8_tile_kernel<WM, WN, MI, NI, STAGES, EXACT, TA, NN, SB>;
     note_launch(reinterpret_cast<const void *>(f), NT);
     hipLaunchKernelGGL(f, dim3((unsigned)grid, p.mode == F8Problem::DEPTH ? p.experts : 1), dim3(NT), 0, s, q, (int)tiles_m, (int)tiles_n,
                        per, c_wide(q));
@@ -323,13 +327,17 @@ hipError_t launch_tile(const F8Problem &p, hipStream_t s, int splits) {
     return e == hipSuccess && splits > 1 ? launch_f8_join(p, s, splits) : e;
 }
 
-// A's type, B's storage and B's scales, from a problem that f8_tile_takes
-template <int WM, int WN, int MI, int NI, bool EXACT>
+// A's type, B's storage and B's scales, from a problem that these tiles take
+template <int WM, int WN, int MI, int NI, int STAGES, bool EXACT>
 hipError_t launch_tile_of(const F8Problem &p, hipStream_t s, int splits) {
     const bool nn = p.b.step != 1, sb = p.b.shift == 0;
-    if (nn) return p.a.type ? launch_tile<WM, WN, MI, NI, EXACT, 1, true, false>(p, s, splits) : launch_tile<WM, WN, MI, NI, EXACT, 0, true, false>(p, s, splits);
-    if (sb) return p.a.type ? launch_tile<WM, WN, MI, NI, EXACT, 1, false, true>(p, s, splits) : launch_tile<WM, WN, MI, NI, EXACT, 0, false, true>(p, s, splits);
-    return p.a.type ? launch_tile<WM, WN, MI, NI, EXACT, 1, false, false>(p, s, splits) : launch_tile<WM, WN, MI, NI, EXACT, 0, false, false>(p, s, splits);
+    auto go = [&](auto ta) {
+        constexpr int TA = decltype(ta)::value;
+        if (nn) return launch_tile<WM, WN, MI, NI, STAGES, EXACT, TA, true, false>(p, s, splits);
+        if (sb) return launch_tile<WM, WN, MI, NI, STAGES, EXACT, TA, false, true>(p, s, splits);
+        return launch_tile<WM, WN, MI, NI, STAGES, EXACT, TA, false, false>(p, s, splits);
+    };
+    return p.a.type ? go(std::integral_constant<int, 1>{}) : go(std::integral_constant<int, 0>{});
 }
 
 }  // namespace f8

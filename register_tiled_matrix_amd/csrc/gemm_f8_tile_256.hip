@@ -4,7 +4,7 @@
 
 namespace regtile {
 hipError_t launch_f8_tile_256(const F8Problem &p, hipStream_t s) {
-    if (p.b.step != 1) return p.a.type ? f8::launch_tile<2, 4, 8, 4, false, 1, true, false>(p, s, 1) : f8::launch_tile<2, 4, 8, 4, false, 0, true, false>(p, s, 1);
-    return p.a.type ? f8::launch_tile<2, 4, 8, 4, false, 1, false, false>(p, s, 1) : f8::launch_tile<2, 4, 8, 4, false, 0, false, false>(p, s, 1);
+    if (p.b.step != 1) return p.a.type ? f8::launch_tile<2, 4, 8, 4, 2, false, 1, true, false>(p, s, 1) : f8::launch_tile<2, 4, 8, 4, 2, false, 0, true, false>(p, s, 1);
+    return p.a.type ? f8::launch_tile<2, 4, 8, 4, 2, false, 1, false, false>(p, s, 1) : f8::launch_tile<2, 4, 8, 4, 2, false, 0, false, false>(p, s, 1);
 }
 }  // namespace regtile

@@ -4,6 +4,6 @@
 
 namespace regtile {
 hipError_t launch_f8_tile_wide(const F8Problem &p, bool exact, hipStream_t s, int splits) {
-    return exact ? f8::launch_tile_of<4, 2, 4, 4, true>(p, s, splits) : f8::launch_tile_of<4, 2, 4, 4, false>(p, s, splits);
+    return exact ? f8::launch_tile_of<4, 2, 4, 4, 2, true>(p, s, splits) : f8::launch_tile_of<4, 2, 4, 4, 2, false>(p, s, splits);
 }
 }  // namespace regtile

@@ -95,6 +95,26 @@ bool dense(int ta, int tb, const regtile_f8_matrix *A, const regtile_f8_matrix *
     return (tb ? B->cols : B->rows) == p->K;
 }
 
+// ... with its rows, or its depth, in groups
+void in_rows(const regtile_expert_rows *rows, int gather, const regtile_f8_matrix *A, const regtile_f8_matrix *B, F8Problem *p) {
+    p->mode = F8Problem::ROWS;
+    p->M = rows->rows;
+    p->experts = rows->experts;
+    p->b_stack = B->codes_stack;
+    p->bs_stack = B->scales_stack;
+    p->offsets = rows->offsets;
+    p->counts = rows->counts;
+    p->slots = gather ? rows->slots : nullptr;
+    p->top_k = rows->k;
+    p->a_rows = A->rows;
+}
+void in_depth(const regtile_expert_rows *rows, F8Problem *p) {
+    p->mode = F8Problem::DEPTH;
+    p->experts = rows->experts;
+    p->offsets = rows->offsets;
+    p->counts = rows->counts;
+}
+
 }  // namespace
 
 extern "C" {
@@ -192,7 +212,8 @@ int regtile_order_experts(const int32_t *chosen, const regtile_expert_rows *rows
 }
 
 int regtile_gemm_f8_experts(const regtile_expert_rows *rows, int gather, int trans_b, float alpha, const regtile_f8_matrix *A,
-                            const regtile_f8_matrix *B, float beta, int c_dtype, void *C, int ldc, void *stream) {
+                            const regtile_f8_matrix *B, float beta, int c_dtype, void *C, int ldc, void *work, int64_t work_bytes,
+                            void *stream) {
     if (bad_rows(rows)) return -1;
     if (gather != 0 && gather != 1) return -2;
     if (trans_b != 0 && trans_b != 1) return -3;
@@ -203,27 +224,23 @@ int regtile_gemm_f8_experts(const regtile_expert_rows *rows, int gather, int tra
     if (bad_dtype(c_dtype)) return -8;
     if ((rows->rows > 0 && p.N > 0 && C == nullptr) || misaligned(C, c_dtype)) return -9;
     if (ldc < (p.N > 1 ? p.N : 1)) return -10;
+    if ((reinterpret_cast<uintptr_t>(work) & 15u) != 0) return -11;
+    if (work_bytes < 0 || (work == nullptr && work_bytes != 0)) return -12;
+    in_rows(rows, gather, A, B, &p);
     if (alpha == 0.0f) p.K = 0;
-    p.mode = F8Problem::ROWS;
-    p.M = rows->rows;
     p.alpha = alpha;
     p.beta = beta;
     p.out.C = C;
     p.out.ldc = ldc;
     p.out.dtype = c_dtype;
-    p.experts = rows->experts;
-    p.b_stack = B->codes_stack;
-    p.bs_stack = B->scales_stack;
-    p.offsets = rows->offsets;
-    p.counts = rows->counts;
-    p.slots = gather ? rows->slots : nullptr;
-    p.top_k = rows->k;
-    p.a_rows = A->rows;
+    p.work = work;
+    p.work_bytes = work_bytes;
     return run(p, stream);
 }
 
 int regtile_gemm_f8_experts_dw(const regtile_expert_rows *rows, float alpha, const regtile_f8_matrix *A, const regtile_f8_matrix *B,
-                               float beta, int c_dtype, void *C, int ldc, int64_t c_stack, void *stream) {
+                               float beta, int c_dtype, void *C, int ldc, int64_t c_stack, void *work, int64_t work_bytes,
+                               void *stream) {
     if (bad_rows(rows) || rows->align % regtile::f8::BLOCK != 0) return -1;
     if (bad_matrix(A, alpha != 0.0f, 1) || A->cols != rows->rows || A->block_rows != 1) return -3;
     if (bad_matrix(B, alpha != 0.0f, 1) || B->cols != rows->rows || B->block_rows != 1) return -4;
@@ -233,18 +250,39 @@ int regtile_gemm_f8_experts_dw(const regtile_expert_rows *rows, float alpha, con
     if ((p.M > 0 && p.N > 0 && C == nullptr) || misaligned(C, c_dtype)) return -7;
     if (ldc < (p.N > 1 ? p.N : 1)) return -8;
     if (c_stack < 0 || (rows->experts > 1 && p.M > 0 && p.N > 0 && c_stack < (int64_t)(p.M - 1) * ldc + p.N)) return -9;
+    if ((reinterpret_cast<uintptr_t>(work) & 15u) != 0) return -10;
+    if (work_bytes < 0 || (work == nullptr && work_bytes != 0)) return -11;
+    in_depth(rows, &p);
     if (alpha == 0.0f) p.K = 0;
-    p.mode = F8Problem::DEPTH;
     p.alpha = alpha;
     p.beta = beta;
     p.out.C = C;
     p.out.ldc = ldc;
     p.out.dtype = c_dtype;
-    p.experts = rows->experts;
     p.c_stack = c_stack;
-    p.offsets = rows->offsets;
-    p.counts = rows->counts;
+    p.work = work;
+    p.work_bytes = work_bytes;
     return run(p, stream);
+}
+
+int64_t regtile_gemm_f8_experts_workspace(const regtile_expert_rows *rows, int gather, int trans_b, const regtile_f8_matrix *A,
+                                          const regtile_f8_matrix *B, int c_dtype) {
+    F8Problem p;
+    if (bad_rows(rows) || bad_matrix(A, false, 1) || bad_matrix(B, false, rows->experts) || !dense(0, trans_b != 0, A, B, &p)) return 0;
+    if (rows->rows == 0 || p.N == 0 || A->rows != (gather ? rows->tokens : rows->rows)) return 0;
+    in_rows(rows, gather, A, B, &p);
+    p.out.dtype = c_dtype;
+    return regtile::f8_work_bytes(p);
+}
+
+int64_t regtile_gemm_f8_experts_dw_workspace(const regtile_expert_rows *rows, const regtile_f8_matrix *A, const regtile_f8_matrix *B,
+                                             int c_dtype) {
+    F8Problem p;
+    if (bad_rows(rows) || bad_matrix(A, false, 1) || bad_matrix(B, false, 1) || !dense(0, 1, A, B, &p)) return 0;
+    if (p.M == 0 || p.N == 0 || p.K != rows->rows) return 0;
+    in_depth(rows, &p);
+    p.out.dtype = c_dtype;
+    return regtile::f8_work_bytes(p);
 }
 
 int regtile_route_experts(int score, int dtype, int tokens, int experts, int k, int groups, int top_groups, int group_best,

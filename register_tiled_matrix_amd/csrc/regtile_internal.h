@@ -189,7 +189,10 @@ int64_t f8_work_bytes(const F8Problem &p);
 hipError_t launch_f8_tile_256(const F8Problem &p, hipStream_t s);
 hipError_t launch_f8_tile_wide(const F8Problem &p, bool exact, hipStream_t s, int splits);
 hipError_t launch_f8_tile_128(const F8Problem &p, bool exact, hipStream_t s, int splits);
+hipError_t launch_f8_tile_deep(const F8Problem &p, bool exact, hipStream_t s, int splits);
 hipError_t launch_f8_join(const F8Problem &p, hipStream_t s, int splits);
+// few rows of A (in each group), B stored N x K
+hipError_t launch_f8_token(const F8Problem &p, int shape, hipStream_t s);
 // any
 hipError_t launch_f8_any(const F8Problem &p, hipStream_t s, const char **name);
 

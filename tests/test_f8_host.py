@@ -99,11 +99,11 @@ def test_experts_arguments(lib):
     b = ctypes.byref
     stack = matrix(rows=300, cols=200, block_rows=128, stack=3, codes_stack=60000, scales_stack=6)
 
-    def g(r=R, gather=1, tb=1, A=matrix(rows=4), B=stack, dtype=1, C=DUMMY, ldc=300):
-        return lib.regtile_gemm_f8_experts(b(r), gather, tb, 1.0, b(A), b(B), 0.0, dtype, C, ldc, None)
+    def g(r=R, gather=1, tb=1, A=matrix(rows=4), B=stack, dtype=1, C=DUMMY, ldc=300, work=None, size=0):
+        return lib.regtile_gemm_f8_experts(b(r), gather, tb, 1.0, b(A), b(B), 0.0, dtype, C, ldc, work, size, None)
 
-    def dw(r=R, A=matrix(rows=64, cols=n), B=matrix(rows=32, cols=n), dtype=0, C=DUMMY, ldc=32, stack=2048):
-        return lib.regtile_gemm_f8_experts_dw(b(r), 1.0, b(A), b(B), 0.0, dtype, C, ldc, stack, None)
+    def dw(r=R, A=matrix(rows=64, cols=n), B=matrix(rows=32, cols=n), dtype=0, C=DUMMY, ldc=32, stack=2048, work=None, size=0):
+        return lib.regtile_gemm_f8_experts_dw(b(r), 1.0, b(A), b(B), 0.0, dtype, C, ldc, stack, work, size, None)
 
     for bad in BAD_ROWS:
         r = rows_struct(**bad)
@@ -117,6 +117,8 @@ def test_experts_arguments(lib):
     assert g(dtype=4) == -8 and g(C=0) == -9 and g(ldc=299) == -10
     assert dw(rows_struct(align=64)) == -1 and dw(A=matrix(rows=64, cols=n - 1)) == -3 and dw(B=matrix(rows=32, cols=n + 1)) == -4
     assert dw(A=matrix(rows=64, cols=n, block_rows=128)) == -3 and dw(dtype=7) == -6 and dw(C=0) == -7 and dw(ldc=31) == -8
+    assert g(work=DUMMY + 8, size=64) == -11 and g(work=DUMMY, size=-1) == -12 and g(size=16) == -12
+    assert dw(work=DUMMY + 8, size=64) == -10 and dw(work=DUMMY, size=-1) == -11 and dw(size=16) == -11
     assert dw(stack=2047) == -9 and dw(stack=-1) == -9
     assert lib.regtile_order_experts(None, b(R), None, 0, None) == -1
     assert lib.regtile_order_experts(DUMMY, b(rows_struct(experts=1025)), None, 0, None) == -2
