@@ -145,11 +145,17 @@ class F8Matrix:
 
 
 def _new_matrix(like, dtype, rows, cols, block_rows):
-    ld = max((cols + 15) // 16 * 16, 16)
-    codes = _torch.empty_strided((rows, cols), (ld, 1), dtype=dtype, device=like.device)
+    """A matrix to be written: rows of codes from multiples of 16 bytes on, scales of a block of columns together."""
+    ld = (cols + 15) // 16 * 16 or 16
     br, bc = (rows if block_rows == 1 else _blocks(rows)), _blocks(cols)
-    scales = _torch.empty_strided((br, bc), (1, max(br, 1)), dtype=_torch.float32, device=like.device)
-    return F8Matrix(codes, scales, block_rows)
+    m = object.__new__(F8Matrix)
+    codes = m.codes = like.new_empty_strided((rows, cols), (ld, 1), dtype=dtype)
+    scales = m.scales = like.new_empty_strided((br, bc), (1, br or 1), dtype=_torch.float32)
+    m.block_rows, m.type, m.transposed = block_rows, _types[dtype], False
+    m._rows, m._cols, m._stack = rows, cols, 0
+    m._c = MatrixStruct(codes.data_ptr(), ld, scales.data_ptr(), 1, br or 1, 0, 0, rows, cols, 1, m.type, block_rows)
+    m._at = ctypes.addressof(m._c)
+    return m
 
 
 def quantize_f8(X, dtype=None, block_rows=1, transpose=False, rows=None, out=None, stream=None):
@@ -188,8 +194,10 @@ def _run_quantize(X, dtype, dt, block_rows, transpose, x_rows, x_cols, ldx, rows
         Q = _new_matrix(X, dtype, *shape, block_rows)
     if 0 in shape:  # (an empty tensor of row numbers has no address)
         return Q
-    _rt._check(_lib().regtile_quantize_f8(dt, 1 if transpose else 0, x_rows, x_cols, X.data_ptr(), ldx,
-                                          None if rows is None else rows.data_ptr(), Q._at, handle))
+    status = _lib().regtile_quantize_f8(dt, 1 if transpose else 0, x_rows, x_cols, X.data_ptr(), ldx,
+                                        None if rows is None else rows.data_ptr(), Q._at, handle)
+    if status:
+        _rt._check(status)
     return Q
 
 
@@ -378,7 +386,7 @@ class ExpertRows:
     ``align`` on (include/regtile.h). ``slots`` (rows), ``position`` (tokens x k), ``offsets`` (experts + 1) and
     ``counts`` (experts) are contiguous int32 tensors on one device; they are kept, not copied."""
 
-    __slots__ = ("slots", "position", "offsets", "counts", "tokens", "k", "experts", "align", "rows", "_c", "_at")
+    __slots__ = ("tokens", "k", "experts", "align", "rows", "device", "_parts", "_c", "_at")
 
     def __init__(self, slots, position, offsets, counts, align=1):
         _torch or _import_torch()
@@ -392,18 +400,28 @@ class ExpertRows:
         _int32(position, "position", device, (tokens, k))
         _int32(offsets, "offsets", device, (experts + 1,))
         _int32(counts, "counts", device, (experts,))
-        self._set(slots, position, offsets, counts, tokens, k, experts, align, rows)
+        self._set((slots, position, offsets, counts), [t.data_ptr() for t in (slots, position, offsets, counts)], device, tokens, k, experts,
+                  align, rows)
 
-    def _set(self, slots, position, offsets, counts, tokens, k, experts, align, rows):
-        self.slots, self.position, self.offsets, self.counts = slots, position, offsets, counts
+    def _set(self, parts, at, device, tokens, k, experts, align, rows):
+        self._parts, self.device = parts, device
         self.tokens, self.k, self.experts, self.align, self.rows = tokens, k, experts, align, rows
-        self._c = RowsStruct(slots.data_ptr(), position.data_ptr(), offsets.data_ptr(), counts.data_ptr(), tokens, k, experts, align, rows)
+        self._c = RowsStruct(*at, tokens, k, experts, align, rows)
         self._at = ctypes.addressof(self._c)
         return self
 
-    @property
-    def device(self):
-        return self.slots.device
+    def _part(self, i):
+        """slots, position, offsets or counts; the four lie in one tensor until one of them is asked for."""
+        if type(self._parts) is not tuple:
+            n, E = self.tokens * self.k, self.experts
+            slots, position, offsets, counts = self._parts[:self.rows + n + 2 * E + 1].split((self.rows, n, E + 1, E))
+            self._parts = slots, position.view(self.tokens, self.k), offsets, counts
+        return self._parts[i]
+
+    slots = property(lambda self: self._part(0))
+    position = property(lambda self: self._part(1))
+    offsets = property(lambda self: self._part(2))
+    counts = property(lambda self: self._part(3))
 
     def token_of_row(self):
         """The token of each row (int32), -1 for rows without one: ``quantize_f8``'s ``rows`` for tokens in the
@@ -431,11 +449,18 @@ def expert_rows(experts, n_experts, align=1, stream=None):
 
 def _run_rows(experts, tokens, k, n_experts, align, rows, handle):
     lib = _lib()
-    new = experts.new_empty
-    r = object.__new__(ExpertRows)._set(new(rows), new((tokens, k)), new(n_experts + 1), new(n_experts), tokens, k, n_experts, align, rows)
-    size = lib.regtile_order_experts_workspace(tokens, k, n_experts)
-    work = new((size + 3) // 4) if size else None
-    _rt._check(lib.regtile_order_experts(experts.data_ptr(), r._at, work.data_ptr() if size else None, size, handle))
+    n = tokens * k
+    # one tensor: slots, position, offsets, counts, and behind them (16 bytes aligned) the workspace that many slots need
+    used = rows + n + 2 * n_experts + 1
+    size = lib.regtile_order_experts_workspace(tokens, k, n_experts) if n > 4096 else 0
+    start = (used + 3) // 4 * 4
+    parts = experts.new_empty(start + (size + 3) // 4 if size else used)
+    at = parts.data_ptr()
+    r = object.__new__(ExpertRows)._set(parts, (at, at + 4 * rows, at + 4 * (rows + n), at + 4 * (rows + n + n_experts + 1)), experts.device,
+                                        tokens, k, n_experts, align, rows)
+    status = lib.regtile_order_experts(experts.data_ptr(), r._at, at + 4 * start if size else None, size, handle)
+    if status:
+        _rt._check(status)
     return r
 
 

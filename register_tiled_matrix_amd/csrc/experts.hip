@@ -143,23 +143,35 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteProblem p) {
                 if (e < p.experts) mine[e + e / per] = key[i];
             }
             __builtin_amdgcn_wave_barrier();
-            u64 first = 0, second = 0;  // the two best of group `lane`
-            if (lane < p.groups)
-                for (int i = 0; i < per; ++i) {
-                    const u64 k = mine[lane * (per + 1) + i];
+            // the two best of each group: `sub` lanes to a group, then over those
+            int sub = 64;
+            while (sub * p.groups > 64) sub >>= 1;
+            const int group = lane / sub, part = lane & (sub - 1);
+            u64 first = 0, second = 0;
+            if (group < p.groups)
+                for (int i = part; i < per; i += sub) {
+                    const u64 k = mine[group * (per + 1) + i];
                     second = max(second, min(first, k));
                     first = max(first, k);
                 }
+            for (int d = 1; d < sub; d <<= 1) {
+                const u64 f = __shfl_xor(first, d), n = __shfl_xor(second, d);
+                second = max(max(second, n), min(first, f));
+                first = max(first, f);
+            }
             auto value = [](u64 k) { return __builtin_bit_cast(double, k >> 63 ? k ^ 0x8000000000000000ull : ~k); };
             u64 rank = first;
             if (p.group_best == 2 && second != 0) rank = key_of(value(first) + value(second));
             // groups before this one: better, or as good with a lower number
             int before = 0;
             for (int g = 0; g < p.groups; ++g) {
-                const u64 other = __shfl(rank, g);
-                before += other > rank || (other == rank && g < lane);
+                const u64 other = (u64)(uint32_t)__builtin_amdgcn_readlane((int)(rank >> 32), g * sub) << 32 |
+                                  (uint32_t)__builtin_amdgcn_readlane((int)rank, g * sub);
+                before += other > rank || (other == rank && g < group);
             }
-            open = __ballot(lane < p.groups && before < p.top_groups);
+            const bool kept = group < p.groups && part == 0 && before < p.top_groups;
+            open = 0;  // a bit for each group, from the lanes that begin one
+            for (u64 m = __ballot(kept); m != 0; m &= m - 1) open |= 1ull << ((__ffsll((unsigned long long)m) - 1) / sub);
         } else {
             // by their best logit: the best of the groups that are left, top_groups times
             u64 left = p.groups == 64 ? ~0ull : (1ull << p.groups) - 1;
@@ -314,14 +326,20 @@ __device__ __forceinline__ int expert_of(const OrderProblem &p, int64_t slot, in
     return e >= 0 && e < p.experts ? e : p.experts;
 }
 
-// counts[wave][expert] of a chunk's slots, each wave's own part of `per` slots from `first` on
-__device__ __forceinline__ void count_chunk(const OrderProblem &p, int *counts, int64_t first, int64_t end, int per, int bits) {
+// counts[wave][expert] of a chunk's slots, each wave's own part of `per` slots from `first` on; e: this lane's experts
+constexpr int MOST = CHUNK / ORDER_NT;
+__device__ __forceinline__ void count_chunk(const OrderProblem &p, int *counts, int64_t first, int64_t end, int per, int bits,
+                                            int (&e_of)[MOST]) {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) e_of[i] = i * 64 < per ? expert_of(p, first + wave * per + i * 64 + lane, end) : p.experts;
     for (int i = threadIdx.x; i < ORDER_WAVES * p.experts; i += ORDER_NT) counts[i] = 0;
     __syncthreads();
     int *mine = counts + wave * p.experts;
-    for (int i = 0; i < per; i += 64) {
-        const int e = expert_of(p, first + wave * per + i + lane, end);
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) {
+        if (i * 64 >= per) break;
+        const int e = e_of[i];
         const u64 m = same(e, bits);
         if (e < p.experts && __ffsll((unsigned long long)m) - 1 == lane) mine[e] += __popcll(m);
         __builtin_amdgcn_wave_barrier();
@@ -332,7 +350,8 @@ __device__ __forceinline__ void count_chunk(const OrderProblem &p, int *counts, 
 __global__ __launch_bounds__(ORDER_NT) void order_count_kernel(OrderProblem p, int bits) {
     __shared__ int counts[ORDER_WAVES * MOST_EXPERTS];
     const int64_t n = (int64_t)p.tokens * p.k, first = (int64_t)blockIdx.x * CHUNK;
-    count_chunk(p, counts, first, min(n, first + CHUNK), CHUNK / ORDER_WAVES, bits);
+    int e_of[MOST];
+    count_chunk(p, counts, first, min(n, first + CHUNK), CHUNK / ORDER_WAVES, bits, e_of);
     const int e = threadIdx.x;
     if (e < p.experts) {
         int sum = 0;
@@ -344,11 +363,13 @@ __global__ __launch_bounds__(ORDER_NT) void order_count_kernel(OrderProblem p, i
 __global__ __launch_bounds__(ORDER_NT) void order_place_kernel(OrderProblem p, int bits) {
     __shared__ int counts[ORDER_WAVES * MOST_EXPERTS];
     __shared__ int wave_room[ORDER_WAVES];
+    __shared__ int2 ends[MOST_EXPERTS];  // of a group's rows and of its room
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, groups = gridDim.x;
     const int64_t n = (int64_t)p.tokens * p.k, first = (int64_t)blockIdx.x * CHUNK, end = min(n, first + CHUNK);
     // a wave's part of the chunk, in whole 64s
     const int per = ((int)((end - first + ORDER_WAVES - 1) / ORDER_WAVES) + 63) / 64 * 64;
-    count_chunk(p, counts, first, end, per, bits);
+    int e_of[MOST];
+    count_chunk(p, counts, first, end, per, bits, e_of);
     int before = 0, all = 0;
     if (tid < p.experts) {
         if (groups == 1) {
@@ -387,15 +408,19 @@ __global__ __launch_bounds__(ORDER_NT) void order_place_kernel(OrderProblem p, i
             p.counts[tid] = all;
             if (tid == 0) p.offsets[p.experts] = used;
         }
-        if (tid % groups == (int)blockIdx.x)
-            for (int r = start + all; r < start + room; ++r) p.slots[r] = -1;
+        ends[tid] = make_int2(start + all, start + room);
     }
     for (int64_t r = used + (int64_t)blockIdx.x * ORDER_NT + tid; r < p.rows; r += (int64_t)groups * ORDER_NT) p.slots[r] = -1;
     __syncthreads();
+    // rows between the groups: a wave to a group
+    for (int e = (int)blockIdx.x * ORDER_WAVES + wave; e < p.experts; e += groups * ORDER_WAVES)
+        for (int r = ends[e].x + lane; r < ends[e].y; r += 64) p.slots[r] = -1;
     int *mine = counts + wave * p.experts;
-    for (int i = 0; i < per; i += 64) {
-        const int64_t slot = first + wave * per + i + lane;
-        const int e = expert_of(p, slot, end);
+#pragma unroll
+    for (int i = 0; i < MOST; ++i) {
+        if (i * 64 >= per) break;
+        const int64_t slot = first + wave * per + i * 64 + lane;
+        const int e = e_of[i];
         const u64 m = same(e, bits);
         int at = -1;
         if (e < p.experts) at = mine[e] + __popcll(m & ((1ull << lane) - 1));

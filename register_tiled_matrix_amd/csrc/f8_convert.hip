@@ -3,10 +3,12 @@
 //
 // A block with largest magnitude a gets s = max(a * (1 / top), 2^-126), top the type's largest value (1 / top
 // and the product rounded to fp32), and its codes are the nearest to x / s, ties to even. The quotient is wanted
-// to be right at the borders between codes, and an IEEE division costs 10 instructions and more a value. So:
-// q = x r with r = 1 / s, one correction, which leaves q within a unit of its last place, and the sign of the
-// exact remainder x - q s: where it is not 0 and q's last bit is even, q moves one unit towards it. An odd
-// q is no border (those end in zeros), and it is on the quotient's side of any. 10 instructions a value.
+// to be right at the borders between codes, and an IEEE division costs 10 instructions and more a value. So x is
+// multiplied by two numbers just below and just above 1 / s: the quotient lies between the products, and where both
+// have the same code it is the quotient's. Where they differ a border lies between them or on the quotient (of 16-bit
+// values one in 500 is a tie), and the value takes the long way: q = x r, one correction, which leaves q within a unit
+// of its last place, and the sign of the exact remainder x - q s: where it is not 0 and q's last bit is even, q moves one
+// unit towards it. An odd q is no border (those end in zeros), and it is on the quotient's side of any.
 //
 // Bound by memory: rows, 16 lanes a block, 8 values a lane; columns (transpose), a tile of 128 rows x 64
 // columns through LDS, so that both sides move whole lines.
@@ -18,7 +20,6 @@ using namespace f8;
 using mfma::u32x4;
 
 constexpr int NT = 256;
-__host__ __device__ constexpr float top_of(int type) { return type == 0 ? 448.0f : 57344.0f; }
 __host__ __device__ constexpr float inv_top_of(int type) { return type == 0 ? 1.0f / 448.0f : 1.0f / 57344.0f; }
 
 template <int DT>
@@ -80,6 +81,28 @@ __device__ __forceinline__ void store8(void *row, int64_t col, int count, bool w
     }
 }
 
+// The same 8 values in two steps, so that several loads can be under way: aligned and there (a row's number is kept in
+// range by the caller; `some` says whether the values count)
+template <int DT>
+struct Raw {
+    u32x4 v[DT == 0 ? 2 : 1];
+};
+template <int DT>
+__device__ __forceinline__ Raw<DT> load_raw(const void *row, int64_t col) {
+    const u32x4 *p = reinterpret_cast<const u32x4 *>(static_cast<const typename Elem<DT>::T *>(row) + col);
+    Raw<DT> r;
+    r.v[0] = p[0];
+    if constexpr (DT == 0) r.v[1] = p[1];
+    return r;
+}
+template <int DT>
+__device__ __forceinline__ void values_of(const Raw<DT> &r, bool some, float (&x)[8]) {
+    typename Elem<DT>::T t[8];
+    __builtin_memcpy(t, &r, sizeof t);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = some ? (float)t[i] : 0.0f;
+}
+
 // The larger of magnitudes as bit patterns: NaN above infinity above every number
 __device__ __forceinline__ uint32_t magnitude(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7FFFFFFFu; }
 
@@ -99,10 +122,10 @@ __device__ __forceinline__ Block block_of(uint32_t top_bits, float inv_top) {
     b.s = fmaxf(__builtin_bit_cast(float, top_bits) * inv_top, 0x1p-126f);
     b.mul = b.s < 0x1p-60f ? 0x1p60f : 1.0f;
     b.d = b.s * b.mul;
-    b.r = 1.0f / b.d;
+    b.r = __builtin_amdgcn_rcpf(b.d);  // (off by a unit of its last place at most)
     return b;
 }
-__device__ __forceinline__ float quotient(float x, const Block &b, float top) {
+__device__ __forceinline__ float quotient(float x, const Block &b) {
     x *= b.mul;
     float q = x * b.r;
     q = fmaf(fmaf(-q, b.d, x), b.r, q);
@@ -111,20 +134,37 @@ __device__ __forceinline__ float quotient(float x, const Block &b, float top) {
     const int towards = ((int32_t)(__builtin_bit_cast(uint32_t, e) ^ bits) >> 31) | 1;
     const float moved = __builtin_bit_cast(float, bits + (uint32_t)towards);
     q = e != 0.0f && (bits & 1u) == 0 ? moved : q;
-    return copysignf(fminf(fabsf(q), top), x);  // (-0 stays -0)
+    return copysignf(q, x);  // (-0 stays -0; what passes the largest value by a few units still rounds to it)
 }
-// 4 values as codes
-__device__ __forceinline__ uint32_t codes4(const float *x, const Block &b, int type, float top) {
-    float q[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = b.mul == 0.0f ? 0.0f : quotient(x[i], b, top);
+__device__ __forceinline__ uint32_t pack4(int type, const float *q) {
 #if defined(__HIP_DEVICE_COMPILE__)
     if (type == 0) return __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false), true);
     return __builtin_amdgcn_cvt_pk_bf8_f32(q[2], q[3], __builtin_amdgcn_cvt_pk_bf8_f32(q[0], q[1], 0, false), true);
 #else
     (void)type;
+    (void)q;
     return 0;
 #endif
+}
+// N values (4 or 8) of one block as codes
+template <int N>
+__device__ __forceinline__ void codes(const float (&x)[N], const Block &b, int type, uint32_t (&out)[N / 4]) {
+    const float below = b.r * (1.0f - 0x1p-21f), above = b.r * (1.0f + 0x1p-21f);  // (r, and each product, is off by 2^-23 at most)
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+        float q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = x[i + j] * below;
+        uint32_t code = pack4(type, q);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = x[i + j] * above;
+        if (code != pack4(type, q) || b.mul != 1.0f) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q[j] = quotient(x[i + j], b);
+            code = b.mul == 0.0f ? 0u : pack4(type, q);
+        }
+        out[i / 4] = code;
+    }
 }
 __device__ __forceinline__ void store_codes8(uint8_t *p, int count, bool wide, uint32_t lo, uint32_t hi) {
     if (count >= 8 && wide) {
@@ -143,54 +183,125 @@ __device__ __forceinline__ int64_t source_row(const F8Convert &p, int64_t i) {
     return r >= 0 && r < p.rows ? r : -1;
 }
 
-// Blocks of 1 x 128: 4 of them to a wave, a row to each wave of a workgroup.
+// The largest magnitude of 8 values as its bits. 16-bit values are compared in pairs.
 template <int DT>
+__device__ __forceinline__ uint32_t largest(const Raw<DT> &r) {
+    if constexpr (DT == 0) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, r.v[i / 4][i % 4] & 0x7FFFFFFFu);
+        return m;
+    } else {
+        typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+        u16x2 m = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, r.v[0][i] & 0x7FFF7FFFu));
+        const unsigned short top = max(m[0], m[1]);
+        return __builtin_bit_cast(uint32_t, (float)__builtin_bit_cast(typename Elem<DT>::T, top));
+    }
+}
+// The largest of each row of 16 lanes, in all of them
+__device__ __forceinline__ uint32_t largest_of_16(uint32_t m) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x128, 0xF, 0xF, false));  // row_ror 8, 4, 2, 1
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x124, 0xF, 0xF, false));
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x122, 0xF, 0xF, false));
+    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, 0x121, 0xF, 0xF, false));
+#endif
+    return m;
+}
+
+// Blocks of 1 x 128: a workgroup takes 32 rows of 4 blocks, a wave 8 of the rows, 4 at a time so that their loads are
+// under way together. Scales leave through LDS: those of 32 rows of one block are a line (one by one from the lanes
+// that have them they cost as much as the rest of the kernel). WIDE: rows of X and of codes are aligned for whole
+// accesses, and columns come in eights (a lane behind the last of a row then takes its last 8 values, which are of the
+// same block or of none that is stored).
+constexpr int U = 4, ROWS = 32;
+template <int DT, bool WIDE>
 __global__ __launch_bounds__(NT) void f8_rows_kernel(F8Convert p, bool wide_x, bool wide_q) {
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const float top = top_of(p.type);
-    const int64_t chunks = ((int64_t)p.q_cols + 511) / 512;
-    for (int64_t row = (int64_t)blockIdx.x * 4 + wave; row < p.q_rows; row += (int64_t)gridDim.x * 4) {
-        const int64_t from = source_row(p, row);
-        const char *x_row = static_cast<const char *>(p.X) + from * p.ldx * (int64_t)sizeof(typename Elem<DT>::T);
+    __shared__ float scales[4][ROWS];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const float inv_top = inv_top_of(p.type);
+    const int64_t chunks = ((int64_t)p.q_cols + 511) / 512, row_bytes = p.ldx * (int64_t)sizeof(typename Elem<DT>::T);
+    for (int64_t first = (int64_t)blockIdx.x * ROWS; first < p.q_rows; first += (int64_t)gridDim.x * ROWS)
         for (int64_t chunk = blockIdx.y; chunk < chunks; chunk += gridDim.y) {
             const int64_t col = chunk * 512 + lane * 8;
             const int count = (int)min((int64_t)8, p.q_cols - col);
-            float x[8] = {};
-            if (from >= 0 && count > 0) load8<DT>(x_row, col, count, wide_x, x);
-            uint32_t m = 0;
+            for (int r = wave * 8; r < wave * 8 + 8 && first + r < p.q_rows; r += U) {
+                const int64_t row0 = first + r;
+                int64_t from[U];
+                Raw<DT> raw[WIDE ? U : 1];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = max(m, magnitude(x[i]));
+                for (int u = 0; u < U; ++u) {
+                    from[u] = row0 + u < p.q_rows ? source_row(p, row0 + u) : -1;
+                    if constexpr (WIDE) {
+                        raw[u] = Raw<DT>{};
+                        if (from[u] >= 0) raw[u] = load_raw<DT>(static_cast<const char *>(p.X) + from[u] * row_bytes, min(col, (int64_t)p.q_cols - 8));
+                    }
+                }
 #pragma unroll
-            for (int d = 1; d < 16; d <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, d));
-            if (count <= 0) continue;
-            const Block b = block_of(m, inv_top_of(p.type));
-            store_codes8(p.Q + row * p.ldq + col, count, wide_q, codes4(x, b, p.type, top), codes4(x + 4, b, p.type, top));
-            if ((lane & 15) == 0) p.S[row * p.s_row + (col >> 7) * p.s_col] = b.s;
+                for (int u = 0; u < U; ++u) {
+                    float x[8] = {};
+                    uint32_t m = 0;
+                    if constexpr (WIDE) {
+                        values_of<DT>(raw[u], true, x);
+                        m = largest(raw[u]);
+                    } else {
+                        if (from[u] >= 0 && count > 0) load8<DT>(static_cast<const char *>(p.X) + from[u] * row_bytes, col, count, wide_x, x);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) m = max(m, magnitude(x[i]));
+                    }
+                    const Block b = block_of(largest_of_16(m), inv_top);
+                    uint32_t q[2];
+                    codes(x, b, p.type, q);
+                    const int64_t row = row0 + u;
+                    if ((lane & 15) == 0) scales[lane >> 4][r + u] = b.s;
+                    if (count > 0 && row < p.q_rows) store_codes8(p.Q + row * p.ldq + col, count, WIDE || wide_q, q[0], q[1]);
+                }
+            }
+            __syncthreads();
+            const int block = threadIdx.x / ROWS, r = threadIdx.x % ROWS;
+            if (block < 4 && chunk * 512 + block * 128 < p.q_cols && first + r < p.q_rows)
+                p.S[(first + r) * p.s_row + (chunk * 4 + block) * p.s_col] = scales[block][r];
+            __syncthreads();
         }
-    }
 }
 
 // The transpose: row f of the matrix is column f of X, in blocks of 128 of X's rows. A workgroup takes 128
 // rows and 64 columns; a thread 8 columns of the rows tid / 8 + 32 i. Codes are turned through LDS, whose
 // rows of 128 bytes (one of the matrix) are padded by 4.
-template <int DT>
+template <int DT, bool WIDE>
 __global__ __launch_bounds__(NT) void f8_turn_kernel(F8Convert p, bool wide_x, bool wide_q) {
     __shared__ uint32_t part[4][64];
     __shared__ uint32_t turned[64][33];  // as bytes: [column][row]
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, at = (tid & 7) * 8, r0 = tid >> 3;
-    const float top = top_of(p.type);
     const int64_t tiles_r = ((int64_t)p.q_cols + 127) / 128, tiles_c = ((int64_t)p.q_rows + 63) / 64;
     for (int64_t tc = blockIdx.x; tc < tiles_c; tc += gridDim.x)
         for (int64_t tr = blockIdx.y; tr < tiles_r; tr += gridDim.y) {
             const int64_t col = tc * 64 + at;
             const int count = (int)min((int64_t)8, p.q_rows - col);
             float x[4][8] = {};
+            int64_t from[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int64_t row = tr * 128 + r0 + 32 * i;
-                const int64_t from = row < p.q_cols ? source_row(p, row) : -1;
-                if (from >= 0 && count > 0)
-                    load8<DT>(static_cast<const char *>(p.X) + from * p.ldx * (int64_t)sizeof(typename Elem<DT>::T), col, count, wide_x, x[i]);
+                from[i] = row < p.q_cols ? source_row(p, row) : -1;
+            }
+            if constexpr (WIDE) {
+                Raw<DT> raw[4];
+                if (p.rows > 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        raw[i] = load_raw<DT>(static_cast<const char *>(p.X) + max(from[i], (int64_t)0) * p.ldx * (int64_t)sizeof(typename Elem<DT>::T),
+                                              min(col, (int64_t)p.q_rows - 8));
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) values_of<DT>(raw[i], from[i] >= 0 && count > 0, x[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (from[i] >= 0 && count > 0)
+                        load8<DT>(static_cast<const char *>(p.X) + from[i] * p.ldx * (int64_t)sizeof(typename Elem<DT>::T), col, count, wide_x, x[i]);
             }
             uint32_t m[8];
 #pragma unroll
@@ -209,9 +320,10 @@ __global__ __launch_bounds__(NT) void f8_turn_kernel(F8Convert p, bool wide_x, b
             for (int c = 0; c < 8; ++c) {
                 const Block b = block_of(max(max(part[0][at + c], part[1][at + c]), max(part[2][at + c], part[3][at + c])), inv_top_of(p.type));
                 const float v[4] = {x[0][c], x[1][c], x[2][c], x[3][c]};
-                const uint32_t q = codes4(v, b, p.type, top);
+                uint32_t q[1];
+                codes(v, b, p.type, q);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) bytes[(at + c) * 132 + r0 + 32 * i] = (uint8_t)(q >> (8 * i));
+                for (int i = 0; i < 4; ++i) bytes[(at + c) * 132 + r0 + 32 * i] = (uint8_t)(q[0] >> (8 * i));
                 if (r0 == 0 && c < count) p.S[(col + c) * p.s_row + tr * p.s_col] = b.s;
             }
             __syncthreads();
@@ -228,11 +340,10 @@ __global__ __launch_bounds__(NT) void f8_turn_kernel(F8Convert p, bool wide_x, b
 }
 
 // Blocks of 128 x 128, one to a workgroup: a thread holds 8 columns of the rows tid / 16 + 16 i.
-template <int DT>
+template <int DT, bool WIDE>
 __global__ __launch_bounds__(NT) void f8_square_kernel(F8Convert p, bool wide_x, bool wide_q) {
     __shared__ uint32_t part[4];
     const int tid = threadIdx.x, lane = tid & 63, at = (tid & 15) * 8, r0 = tid >> 4;
-    const float top = top_of(p.type);
     const int64_t tiles_r = ((int64_t)p.q_rows + 127) / 128, tiles_c = ((int64_t)p.q_cols + 127) / 128;
     for (int64_t tr = blockIdx.x; tr < tiles_r; tr += gridDim.x)
         for (int64_t tc = blockIdx.y; tc < tiles_c; tc += gridDim.y) {
@@ -240,11 +351,27 @@ __global__ __launch_bounds__(NT) void f8_square_kernel(F8Convert p, bool wide_x,
             const int count = (int)min((int64_t)8, p.q_cols - col);
             float x[8][8] = {};
             uint32_t m = 0;
+            int64_t from[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int64_t row = tr * 128 + r0 + 16 * i, from = row < p.q_rows ? source_row(p, row) : -1;
-                if (from >= 0 && count > 0)
-                    load8<DT>(static_cast<const char *>(p.X) + from * p.ldx * (int64_t)sizeof(typename Elem<DT>::T), col, count, wide_x, x[i]);
+                const int64_t row = tr * 128 + r0 + 16 * i;
+                from[i] = row < p.q_rows ? source_row(p, row) : -1;
+            }
+            if constexpr (WIDE) {
+                Raw<DT> raw[8];
+                if (p.rows > 0) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        raw[i] = load_raw<DT>(static_cast<const char *>(p.X) + max(from[i], (int64_t)0) * p.ldx * (int64_t)sizeof(typename Elem<DT>::T),
+                                              min(col, (int64_t)p.q_cols - 8));
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) values_of<DT>(raw[i], from[i] >= 0 && count > 0, x[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (from[i] >= 0 && count > 0)
+                        load8<DT>(static_cast<const char *>(p.X) + from[i] * p.ldx * (int64_t)sizeof(typename Elem<DT>::T), col, count, wide_x, x[i]);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -260,8 +387,11 @@ __global__ __launch_bounds__(NT) void f8_square_kernel(F8Convert p, bool wide_x,
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int64_t row = tr * 128 + r0 + 16 * i;
-                    if (row < p.q_rows)
-                        store_codes8(p.Q + row * p.ldq + col, count, wide_q, codes4(x[i], b, p.type, top), codes4(x[i] + 4, b, p.type, top));
+                    if (row < p.q_rows) {
+                        uint32_t q[2];
+                        codes(x[i], b, p.type, q);
+                        store_codes8(p.Q + row * p.ldq + col, count, wide_q, q[0], q[1]);
+                    }
                 }
             }
             __syncthreads();
@@ -307,17 +437,18 @@ unsigned grid_of(int64_t n, int64_t most) { return (unsigned)(n < most ? n : mos
 
 bool wide(const void *p, int64_t ld_bytes, int to) { return (reinterpret_cast<uintptr_t>(p) % to) == 0 && ld_bytes % to == 0; }
 
-template <typename F0, typename F1, typename F2>
-hipError_t launch(F0 f0, F1 f1, F2 f2, const F8Convert &p, dim3 grid, hipStream_t s) {
+template <typename F>
+hipError_t launch(F pick, const F8Convert &p, dim3 grid, hipStream_t s) {
     const int size = p.dtype == 0 ? 4 : 2;
     const bool wx = wide(p.X, p.ldx * size, 16), wq = wide(p.Q, p.ldq, 8);
-    auto go = [&](auto f) {
-        note_launch(reinterpret_cast<const void *>(f), NT);
-        hipLaunchKernelGGL(f, grid, dim3(NT), 0, s, p, wx, wq);
-        return hipGetLastError();
-    };
-    return p.dtype == 0 ? go(f0) : p.dtype == 1 ? go(f1) : go(f2);
+    const auto f = pick(wx && wq && p.cols % 8 == 0);
+    note_launch(reinterpret_cast<const void *>(f), NT);
+    hipLaunchKernelGGL(f, grid, dim3(NT), 0, s, p, wx, wq);
+    return hipGetLastError();
 }
+#define REGTILE_PICK(kernel) \
+    [&](bool w) { return w ? (p.dtype == 0 ? kernel<0, true> : p.dtype == 1 ? kernel<1, true> : kernel<2, true>) \
+                           : (p.dtype == 0 ? kernel<0, false> : p.dtype == 1 ? kernel<1, false> : kernel<2, false>); }
 
 }  // namespace
 
@@ -325,22 +456,22 @@ hipError_t launch_f8_quantize(const F8Convert &p, hipStream_t s, const char **na
     const int64_t rows = p.q_rows, cols = p.q_cols;
     if (p.transpose) {
         *name = "f8_quantize_transposed";
-        return launch(f8_turn_kernel<0>, f8_turn_kernel<1>, f8_turn_kernel<2>, p,
+        return launch(REGTILE_PICK(f8_turn_kernel), p,
                       dim3(grid_of((rows + 63) / 64, 1 << 16), grid_of((cols + 127) / 128, 1 << 15)), s);
     }
     if (p.block_rows == 1) {
         *name = "f8_quantize_rows";
-        return launch(f8_rows_kernel<0>, f8_rows_kernel<1>, f8_rows_kernel<2>, p,
-                      dim3(grid_of((rows + 3) / 4, 1 << 18), grid_of((cols + 511) / 512, 64)), s);
+        return launch(REGTILE_PICK(f8_rows_kernel), p,
+                      dim3(grid_of((rows + ROWS - 1) / ROWS, 1 << 16), grid_of((cols + 511) / 512, 64)), s);
     }
     *name = "f8_quantize_blocks";
-    return launch(f8_square_kernel<0>, f8_square_kernel<1>, f8_square_kernel<2>, p,
+    return launch(REGTILE_PICK(f8_square_kernel), p,
                   dim3(grid_of((rows + 127) / 128, 1 << 16), grid_of((cols + 127) / 128, 1 << 15)), s);
 }
 
 hipError_t launch_f8_dequantize(const F8Convert &p, hipStream_t s, const char **name) {
     *name = "f8_dequantize";
-    return launch(f8_values_kernel<0>, f8_values_kernel<1>, f8_values_kernel<2>, p,
+    return launch([&](bool) { return p.dtype == 0 ? f8_values_kernel<0> : p.dtype == 1 ? f8_values_kernel<1> : f8_values_kernel<2>; }, p,
                   dim3(grid_of(((int64_t)p.q_rows + 3) / 4, 1 << 18), grid_of(((int64_t)p.q_cols + 511) / 512, 64)), s);
 }
 

@@ -136,7 +136,7 @@ Plan plan_of(const F8Problem &p) {
         plan.parts = (int)(fill < blocks / 8 ? fill : blocks / 8);
         if (plan.parts < 1 || (tiles128 >= 256 && blocks < 32)) plan.parts = 1;
     }
-    return plan;  // tuned
+    return plan;
 }
 
 }  // namespace

@@ -76,9 +76,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
     grouped_tile<8>(id - split * tiles, tiles_m, tiles_n, tm, tn);
     Work w;
     if (!work_of(p, BM, tm, blockIdx.y, w)) return;
-    const int n0 = tn * BN;
-    const int K = w.used > 0 ? w.K : 0, all = (K + BLOCK - 1) / BLOCK;
-    const int first = split * per_split, blocks = min(per_split, all - first);
+    // (the same in every lane; where it comes from memory or a division it would stay in vector registers, and an offset
+    // in one costs a loop at each DMA)
+    auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+    w.used = uniform(w.used);
+    w.row0 = uniform(w.row0);
+    const int n0 = uniform(tn * BN);
+    const int K = uniform(w.used > 0 ? w.K : 0), all = (K + BLOCK - 1) / BLOCK;
+    const int first = uniform(split * per_split), blocks = min(per_split, all - first);
     if ((int)gridDim.x > tiles) w.out.C = static_cast<float *>(w.out.C) + (int64_t)split * p.M * p.N;
 
     f32x4 acc[MI][NI] = {};
@@ -115,7 +120,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
         const bool sa_wave = wave * 64 < BM || wave >= SC;
         const int si = sa_wave ? min((wave < SC ? wave * 64 : 0) + lane, w.used - 1) : min(n0 + wave * 64 - BM + lane, p.N - 1);
         const int64_t s_at = sa_wave ? (a_row(p, w, si) >> w.a.shift) * w.a.s_row : (int64_t)(si >> w.b.shift) * w.b.s_row;
-        const uint32_t sv = (uint32_t)(s_at * 4), s_step = (uint32_t)((sa_wave ? w.a.s_col : w.b.s_col) * 4);
+        const uint32_t sv = (uint32_t)(s_at * 4), s_step = uniform((int)((sa_wave ? w.a.s_col : w.b.s_col) * 4));
         const rsrc_t s_rsrc = make_rsrc(sa_wave ? w.a.s : w.b.s, 0x7FFFFFFFu);
 
         constexpr int PIECES = JA + JB + 1;
@@ -132,15 +137,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
 
         // ---- one block ----
         const int fr = lane & 15, fg = lane >> 4;
-        const int a_key = addr::slab_key<8, 16>(fr);
-        auto row_frag = [&](const uint8_t *s, int row) {
-            const uint8_t *at = s + row * BLOCK;
-            const u32x4 lo = lds_read16(at + (fg ^ a_key) * 16), hi = lds_read16(at + ((fg + 4) ^ a_key) * 16);
-            return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+        // A lane's place in the first fragment of its wave's rows (columns, factors); the others are at constant distances
+        const int key = addr::slab_key<8, 16>(fr), lo = (fg ^ key) * 16, hi = ((fg + 4) ^ key) * 16;
+        const int a_at = (wm * MI * 16 + fr) * BLOCK, b_at = BM * BLOCK + (wn * NI * 16 + fr) * BLOCK;
+        const int sa_at = (BM + BN) * BLOCK + (wm * MI * 16 + fr) * 4, sb_at = (BM + BN) * BLOCK + (BM + wn * NI * 16) * 4;
+        const int tr_row = fg * 16 + (fr >> 1), tr_at = BM * BLOCK + tr_row * BN + (fr & 1) * 8, tr_key = nn_key<BN>(tr_row);
+        auto whole = [](u32x4 l, u32x4 h) {
+            return i32x8{(int)l[0], (int)l[1], (int)l[2], (int)l[3], (int)h[0], (int)h[1], (int)h[2], (int)h[3]};
         };
-        auto column_frag = [&](const uint8_t *s, int chunk) {
-            const int r = fg * 16 + (fr >> 1);
-            const uint8_t *at = s + r * BN + (chunk ^ nn_key<BN>(r)) * 16 + (fr & 1) * 8;
+        auto column_frag = [&](const uint8_t *s, int j) {
+            const uint8_t *at = s + tr_at + ((wn * NI + j) ^ tr_key) * 16;
             u32x2 v[4];
 #pragma unroll
             for (int h = 0; h < 4; ++h) v[h] = lds_read_tr8(at + ((h >> 1) * 64 + (h & 1) * 8) * BN);
@@ -174,22 +180,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
         f32x4 sb[SB ? NI : 1];
         float sa_next[2];
         auto read_a = [&](const uint8_t *s, int i) {
-            const int row = (wm * MI + i) * 16 + fr;
-            qa[i & 1] = row_frag(s, row);
-            sa_next[i & 1] = reinterpret_cast<const f32_any *>(s + (BM + BN) * BLOCK)[row];
+            qa[i & 1] = whole(lds_read16(s + a_at + lo + i * 16 * BLOCK), lds_read16(s + a_at + hi + i * 16 * BLOCK));
+            sa_next[i & 1] = *reinterpret_cast<const f32_any *>(s + sa_at + i * 64);
         };
         auto read_b = [&](const uint8_t *s, int j) {
-            const f32_any *sc = reinterpret_cast<const f32_any *>(s + (BM + BN) * BLOCK) + BM + wn * NI * 16;
             if constexpr (NN)
-                qb[j] = column_frag(s + BM * BLOCK, wn * NI + j);
+                qb[j] = column_frag(s, j);
             else
-                qb[j] = row_frag(s + BM * BLOCK, (wn * NI + j) * 16 + fr);
-            if (!SB && j == 0) sb_all = sc[0];
+                qb[j] = whole(lds_read16(s + b_at + lo + j * 16 * BLOCK), lds_read16(s + b_at + hi + j * 16 * BLOCK));
+            if (!SB && j == 0) sb_all = *reinterpret_cast<const f32_any *>(s + sb_at);
         };
         auto read_sb = [&](const uint8_t *s) {
-            const f32_any *sc = reinterpret_cast<const f32_any *>(s + (BM + BN) * BLOCK) + BM + wn * NI * 16;
 #pragma unroll
-            for (int j = 0; j < (SB ? NI : 0); ++j) sb[j] = __builtin_bit_cast(f32x4, lds_read16(sc + j * 16 + fg * 4));
+            for (int j = 0; j < (SB ? NI : 0); ++j) sb[j] = __builtin_bit_cast(f32x4, lds_read16(s + sb_at + fg * 16 + j * 64));
         };
         auto add = [&](int t) {  // tile t of a block's
             const int i = t / NI, j = t % NI;
@@ -232,6 +235,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
                 if (j == 0) begin_row(id / NI);
                 if (i == 0) b[j] = frag(qb[j], type_b);
                 tile(id);
+                if constexpr (!EXACT) __builtin_amdgcn_sched_barrier(0);  // (the sum that is added next needs time)
                 if (!FIRST || n - LAG >= START) add((id + TILES - LAG) % TILES);
                 if (SB && i == 0 && j == LAG - 1) read_sb(cur);  // (the block before has been added)
                 if (j == 0) read_a(cur, i + 2);
