@@ -86,7 +86,7 @@ __device__ __forceinline__ mfma::u32x4 load16(const uint8_t *p, int left, int ha
     return v;
 }
 
-// Where group e of `rows` begins, its used rows and its room, kept inside the matrix whatever the arrays hold.
+// Where a group of `rows` begins, its used rows and its room, kept inside the matrix whatever the arrays hold.
 struct Group {
     int first, count, room;
 };
@@ -99,19 +99,17 @@ __device__ __forceinline__ Group group_of(const int32_t *offsets, const int32_t 
 }
 
 // The group that row tile `tile` (of `height` rows; groups begin a tile each) belongs to and the tile's
-// number in it; false past the last. Every lane of the wave gets the same answer: 64 groups are counted
-// at a time.
-__device__ __forceinline__ bool find_tile(const int32_t *offsets, int experts, int rows, int height, int tile, int &expert,
-                                          int &in_group) {
+// number in it; false past the last. Every lane of the wave gets the same answer: 64 groups are loaded and counted
+// at a time, and the one that is wanted comes out of its lane's registers.
+__device__ __forceinline__ bool find_tile(const int32_t *offsets, const int32_t *counts, int experts, int rows, int height, int tile,
+                                          int &expert, int &in_group, Group &group) {
     const int lane = __lane_id();
     int before = 0;
     for (int e0 = 0; e0 < experts; e0 += 64) {
         const int e = e0 + lane;
-        int n = 0;
-        if (e < experts) {
-            const int first = min(max(offsets[e], 0), rows);
-            n = (min(max(offsets[e + 1], first), rows) - first + height - 1) / height;
-        }
+        Group g = {0, 0, 0};
+        if (e < experts) g = group_of(offsets, counts, e, rows);
+        const int n = (g.room + height - 1) / height;
         int upto = n;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
@@ -121,11 +119,13 @@ __device__ __forceinline__ bool find_tile(const int32_t *offsets, int experts, i
         const uint64_t past = __ballot(before + upto > tile);
         if (past != 0) {
             const int l = __ffsll((unsigned long long)past) - 1;
+            auto of = [&](int x) { return __builtin_amdgcn_readlane(x, l); };
             expert = __builtin_amdgcn_readfirstlane(e0 + l);
-            in_group = __builtin_amdgcn_readfirstlane(tile - before - (__shfl(upto, l) - __shfl(n, l)));
+            in_group = __builtin_amdgcn_readfirstlane(tile - before - of(upto - n));
+            group = Group{of(g.first), of(g.count), of(g.room)};
             return true;
         }
-        before += __shfl(upto, 63);
+        before += __builtin_amdgcn_readlane(upto, 63);
     }
     return false;
 }
@@ -145,8 +145,8 @@ __device__ __forceinline__ bool work_of(const F8Problem &p, int height, int tile
     w.K = p.K;
     if (p.mode == F8Problem::ROWS) {
         int e, in_group;
-        if (!find_tile(p.offsets, p.experts, p.M, height, tile, e, in_group)) return false;
-        const Group g = group_of(p.offsets, p.counts, e, p.M);
+        Group g;
+        if (!find_tile(p.offsets, p.counts, p.experts, p.M, height, tile, e, in_group, g)) return false;
         const int at = in_group * height;
         w.row0 = g.first + at;
         w.rows = min(height, g.room - at);

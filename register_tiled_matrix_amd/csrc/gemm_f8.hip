@@ -96,7 +96,7 @@ bool tile_takes(const F8Problem &p) {
 }
 
 struct Plan {
-    enum { ANY, TILE_128, TILE_WIDE, TILE_256, TOKEN, TILE_DEEP } kernel;
+    enum { ANY, TILE_128, TILE_256, TOKEN, TILE_DEEP } kernel;
     int shape;
     bool exact;
     int parts;     // of k, through the workspace
@@ -129,12 +129,15 @@ Plan plan_of(const F8Problem &p) {
         plan.kernel = Plan::TILE_256;
         return plan;
     }
-    // two 128 x 128 tiles run on a CU: fewer than 512 of them go in parts of at least 1024 k (1024 x 1024 x 8192, 64
-    // tiles: 63.9 us whole, 27.4 in 4 parts, 27.2 in 8; 2048 x 2048 x 2048: 20.9 whole, 28.7 in 2)
+    // Fewer tiles than the chip holds go in parts of at least 1024 k: one workgroup of the 8-bit instructions to a CU with
+    // four stages (1024 x 1024 x 8192, 64 tiles: 48 us whole, 22.4 in 4 parts; 23.8 with two stages; 2048 x 2048 x 2048,
+    // 256 tiles: 15.6, with two stages 17.4), two of the bf16 ones with two (2048 x 1504 x 8096: 80 us whole, 70 in 2;
+    // with four stages 78).
     if (dense) {
-        const int64_t blocks = ((int64_t)p.K + BLOCK - 1) / BLOCK, fill = 512 / tiles128;
+        const int64_t blocks = ((int64_t)p.K + BLOCK - 1) / BLOCK, fill = (plan.exact ? 512 : 256) / tiles128;
         plan.parts = (int)(fill < blocks / 8 ? fill : blocks / 8);
-        if (plan.parts < 1 || (tiles128 >= 256 && blocks < 32)) plan.parts = 1;
+        if (plan.parts < 1) plan.parts = 1;
+        if (!plan.exact && tiles128 <= 256) plan.kernel = Plan::TILE_DEEP;
     }
     return plan;
 }
@@ -175,14 +178,11 @@ hipError_t launch_f8(const F8Problem &given, hipStream_t s, const char **name) {
     p.work = work;
     p.work_bytes -= plan.copy_bytes;
     while (plan.parts > 1 && (int64_t)plan.parts * p.M * p.N * 4 > p.work_bytes) --plan.parts;
-    static const char *const wide[2] = {"f8_tile_256x128", "f8_tile_256x128_exact"};
     static const char *const small[2] = {"f8_tile_128x128", "f8_tile_128x128_exact"};
-    static const char *const deep[2] = {"f8_tile_128x128_deep", "f8_tile_128x128_deep_exact"};
     switch (plan.kernel) {
         case Plan::TILE_256: *name = "f8_tile_256x256"; return launch_f8_tile_256(p, s);
-        case Plan::TILE_WIDE: *name = wide[plan.exact]; return launch_f8_tile_wide(p, plan.exact, s, plan.parts);
         case Plan::TILE_128: *name = small[plan.exact]; return launch_f8_tile_128(p, plan.exact, s, plan.parts);
-        case Plan::TILE_DEEP: *name = deep[plan.exact]; return launch_f8_tile_deep(p, plan.exact, s, plan.parts);
+        case Plan::TILE_DEEP: *name = "f8_tile_128x128_deep"; return launch_f8_tile_deep(p, s, plan.parts);
         case Plan::TOKEN: *name = "f8_token"; return launch_f8_token(p, plan.shape, s);
         default: return launch_f8_any(p, s, name);
     }

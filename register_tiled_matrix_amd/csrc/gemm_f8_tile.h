@@ -58,8 +58,8 @@ __device__ __forceinline__ void apart(const uint8_t *__restrict__ cur, uint8_t *
 // WM x WN waves of MI x NI fragments of 16 x 16. TA: A's type (B is e4m3). NN: B stored K x N. SB: B has a scale
 // for each column, else one for 128.
 template <int WM, int WN, int MI, int NI, int STAGES, bool EXACT, int TA, bool NN, bool SB>
-__global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, int tiles_m, int tiles_n, int per_split,
-                                                                                      bool wide) {
+__global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, int tiles_m, int tiles_n, int group_m,
+                                                                      int per_split, bool wide) {
     constexpr int WAVES = WM * WN, NT = 64 * WAVES, BM = WM * MI * 16, BN = WN * NI * 16;
     constexpr int JA = BM / 8 / WAVES, JB = BN / 8 / WAVES;       // DMA instructions of a wave
     constexpr int SC = (BM + BN) / 64;                            // waves' worth of scales
@@ -73,7 +73,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
     int tm, tn;
     const int id = xcd_contiguous_id(blockIdx.x, gridDim.x), tiles = tiles_m * tiles_n;
     const int split = id / tiles;  // part of k, per_split blocks
-    grouped_tile<8>(id - split * tiles, tiles_m, tiles_n, tm, tn);
+    {  // group_m tile rows at a time, column by column
+        const int at = id - split * tiles, group = at / (group_m * tiles_n), row = group * group_m;
+        const int rows = min(tiles_m - row, group_m), in_group = at - group * group_m * tiles_n;
+        tm = row + in_group % rows;
+        tn = in_group / rows;
+    }
     Work w;
     if (!work_of(p, BM, tm, blockIdx.y, w)) return;
     // (the same in every lane; where it comes from memory or a division it would stay in vector registers, and an offset
@@ -315,6 +320,12 @@ hipError_t launch_tile(const F8Problem &p, hipStream_t s, int splits) {
     const int64_t tiles_m = most_row_tiles(p, BM), tiles_n = ((int64_t)p.N + BN - 1) / BN, grid = tiles_m * tiles_n * splits;
     if (grid * NT > 0xFFFFFFFFll || p.experts > 65535) return hipErrorInvalidConfiguration;
     const int blocks = (p.K + BLOCK - 1) / BLOCK, per = blocks > 0 ? (blocks + splits - 1) / splits : 1;
+    // tile rows that share B's panels: 8, in groups as many as a group has on the average (the others have another B)
+    int group_m = 8;
+    if (p.mode == F8Problem::ROWS) {
+        const int64_t mean = ((int64_t)p.M / p.experts + BM - 1) / BM;
+        group_m = (int)(mean < 1 ? 1 : mean < 8 ? mean : 8);
+    }
     F8Problem q = p;
     if (splits > 1) {  // parts of M x N fp32, joined by f8_join
         q.out.C = p.work;
@@ -326,7 +337,7 @@ hipError_t launch_tile(const F8Problem &p, hipStream_t s, int splits) {
     auto f = f8_tile_kernel<WM, WN, MI, NI, STAGES, EXACT, TA, NN, SB>;
     note_launch(reinterpret_cast<const void *>(f), NT);
     hipLaunchKernelGGL(f, dim3((unsigned)grid, p.mode == F8Problem::DEPTH ? p.experts : 1), dim3(NT), 0, s, q, (int)tiles_m, (int)tiles_n,
-                       per, c_wide(q));
+                       group_m, per, c_wide(q));
     const hipError_t e = hipGetLastError();
     return e == hipSuccess && splits > 1 ? launch_f8_join(p, s, splits) : e;
 }
