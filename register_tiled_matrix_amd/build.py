@@ -29,7 +29,7 @@ SOURCES = ["regtile_api.hip", "gemm_simple.hip", "gemm_f32_regtile.hip", "gemm_f
            "mx_convert.hip", "gemm_mx_mfma.hip", "gemm_mx_token.hip",
            "gemm_mx_dma.hip", "gemm_mx_splitk.hip", "gemm_mx_codes.hip",
            "regtile_f8_api.hip", "f8_convert.hip", "gemm_f8.hip", "gemm_f8_any.hip",
-           "gemm_f8_tile_256.hip", "gemm_f8_tile_128.hip", "gemm_f8_tile_deep.hip",
+           "gemm_f8_tile_256.hip", "gemm_f8_tile_128.hip", "gemm_f8_tile_deep.hip", "gemm_f8_tile_64.hip",
            "gemm_f8_token.hip", "experts.hip"]
 
 COMMON_FLAGS = [

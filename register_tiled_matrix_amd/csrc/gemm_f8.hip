@@ -83,6 +83,42 @@ hipError_t align_rows(const Copy &a, const Copy &b, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Scales of 1 x 128 blocks whose rows are apart: a block's load by DMA then touches a line for each row, as many as the
+// codes' loads together. Products of 2^37 operations or more have them turned in the workspace first (8192^3: 497 us
+// against 449 with turned scales, 4096^3 with both operands' so 94 against 83; turning takes about 5).
+bool scales_apart(const F8Problem &p, const F8Operand &o, int64_t rows) {
+    const double work = 2.0 * p.M * p.N * p.K;
+    const int64_t turned = rows * (((int64_t)p.K + BLOCK - 1) / BLOCK) * 4;
+    return o.shift == 0 && o.s_row != 1 && work >= (double)(int64_t(1) << 37) && turned < int64_t(1) << 31;
+}
+struct Turn {
+    const float *from;
+    float *to;
+    int64_t s_row, s_col, rows, blocks;
+};
+int64_t turned_bytes(int64_t rows, int64_t blocks) { return (rows * blocks * 4 + 15) / 16 * 16; }
+// 64 rows x 64 blocks at a time, through LDS
+__global__ __launch_bounds__(256) void f8_turn_scales_kernel(Turn a, Turn b, int ya) {
+    __shared__ float tile[64][65];
+    const bool second = (int)blockIdx.y >= ya;
+    const Turn t = second ? b : a;
+    const int y = second ? blockIdx.y - ya : blockIdx.y, ny = second ? gridDim.y - ya : ya;
+    const int x = threadIdx.x & 63, z = threadIdx.x >> 6;
+    for (int64_t k0 = (int64_t)y * 64; k0 < t.blocks; k0 += (int64_t)ny * 64)
+        for (int64_t r0 = (int64_t)blockIdx.x * 64; r0 < t.rows; r0 += (int64_t)gridDim.x * 64) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int64_t r = min(r0 + z * 16 + i, t.rows - 1), k = min(k0 + x, t.blocks - 1);
+                tile[z * 16 + i][x] = t.from[r * t.s_row + k * t.s_col];
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (k0 + z * 16 + i < t.blocks && r0 + x < t.rows) t.to[(k0 + z * 16 + i) * t.rows + r0 + x] = tile[x][z * 16 + i];
+            __syncthreads();
+        }
+}
+
 // What the tiles take: K-contiguous A, e4m3 B, and operands within the reach of a tile's 32-bit offsets
 bool tile_takes(const F8Problem &p) {
     const F8Operand &a = p.a, &b = p.b;
@@ -96,45 +132,70 @@ bool tile_takes(const F8Problem &p) {
 }
 
 struct Plan {
-    enum { ANY, TILE_128, TILE_256, TOKEN, TILE_DEEP } kernel;
+    enum { ANY, TILE_128, TILE_256, TOKEN, TILE_DEEP, TILE_64 } kernel;
     int shape;
     bool exact;
     int parts;     // of k, through the workspace
-    bool copy_a, copy_b;  // operands that it needs copies of
+    bool copy_a, copy_b;  // operands that it needs copies of,
+    bool turn_a, turn_b;  // and whose scales it wants turned
     int64_t copy_bytes;
 };
 
 Plan plan_of(const F8Problem &p) {
-    Plan plan = {Plan::ANY, 0, p.out.dtype == 0, 1, false, false, 0};
-    if (!tile_takes(p)) return plan;
+    Plan plan = {Plan::ANY, 0, p.out.dtype == 0, 1, false, false, false, false, 0};
+    if (p.K == 0 || !tile_takes(p)) return plan;
     const bool dense = p.mode == F8Problem::DENSE, rows = p.mode == F8Problem::ROWS;
-    // Few rows (in a group, on the average): codes straight to registers
-    const int64_t weights = (int64_t)p.N * p.K, group = rows ? p.M / p.experts : p.M;
+    // Few rows (in a group, on the average): codes straight to registers. us on 128 x 128 tiles (64 x 64 for the last):
+    // 16x4096x4096 13.0, here 6.8; 32 tokens x 6 of 64 experts 114, here 107; 256 x 4 of 32 34.5, here 70.6, which unaligned
+    // rows of B still beat (50 us to copy them)
+    const int64_t weights = (int64_t)p.N * p.K, group = rows ? p.mean_rows : p.M;
     if (p.b.step == 1 && (dense || rows)) {
         plan.kernel = Plan::TOKEN;
         if (dense && p.M <= 16) return plan.shape = 11, plan;
-        if (dense && p.M <= 32 && weights <= 1 << 25) return plan.shape = 21, plan;
-        if (dense && p.M <= 64 && weights <= 1 << 25) return plan.shape = 22, plan;
+        // (32x4096x4096 9.0, on 64 x 64 tiles 10.0; 32x4096x8192 14.4, 11.7; 48x1024x4096 8.4, 9.3; 64x4096x4096 12.0, 11.1,
+        // and 10 more to copy unaligned rows)
+        const bool aligned = a_aligned(p) && b_aligned(p);
+        if (dense && p.M <= 32 && weights <= 1 << (aligned ? 24 : 27)) return plan.shape = 21, plan;
+        if (dense && p.M <= 64 && weights <= 1 << 22) return plan.shape = 21, plan;
+        if (dense && p.M <= 64 && !aligned && weights <= 1 << 27) return plan.shape = 22, plan;
         if (rows && group <= (b_aligned(p) ? 12 : 48)) return plan.shape = 12, plan;
     }
     plan.copy_a = !a_aligned(p);
     plan.copy_b = !b_aligned(p);
-    plan.copy_bytes = (plan.copy_a ? stored_a(p).bytes() : 0) + (plan.copy_b ? stored_b(p).bytes() : 0);
-    const int64_t tiles256 = most_row_tiles(p, 256) * (((int64_t)p.N + 255) / 256);
-    const int64_t tiles128 = most_row_tiles(p, 128) * (((int64_t)p.N + 127) / 128);
-    plan.kernel = Plan::TILE_128;
-    // 256 x 256 tiles run one to a CU: with fewer than 192 too many of the 256 CUs are idle (2048^3, 64 tiles: 35.3
-    // us against 20.9; 4096 x 4096 x 8192, 256 tiles: 130 against 161)
-    if (!plan.exact && p.b.shift != 0 && tiles256 >= 192 && (!rows || group >= 256)) {
+    plan.turn_a = scales_apart(p, p.a, stored_a(p).rows);
+    plan.turn_b = !rows && scales_apart(p, p.b, p.N);
+    const int64_t blocks = ((int64_t)p.K + BLOCK - 1) / BLOCK;
+    plan.copy_bytes = (plan.copy_a ? stored_a(p).bytes() : 0) + (plan.copy_b ? stored_b(p).bytes() : 0) +
+                      (plan.turn_a ? turned_bytes(stored_a(p).rows, blocks) : 0) + (plan.turn_b ? turned_bytes(p.N, blocks) : 0);
+    auto tiles = [&](int64_t side) {
+        return most_row_tiles(p, (int)side) * (((int64_t)p.N + side - 1) / side) * (p.mode == F8Problem::DEPTH ? p.experts : 1);
+    };
+    // 64 x 64 tiles while there are at most 512 of them, or few rows in a group. us on 128 x 128 (best of two and four stages
+    // and parts of k), here: 1024^3 10.5, 5.5 (fp32 C 14.2, 7.1); 1024x1024x4096 21.6, 12.3 (25.6, 19.7); 296x2984x1056 11.2,
+    // 7.5; 2048^3, 1024 tiles, 16.5, 18.8 (25.3, 27.7); 256 tokens x 4 of 32 experts 43.5, 34.5; 512 x 8 of 64 82.7, 99.4.
+    // They go in parts of at least 2048 k (fp32 C: 1024), two (one) workgroups to a CU: 64x8192x8192 27.9 whole, 19.8 in 4.
+    const int64_t tiles64 = tiles(64);
+    if (rows ? group <= 48 : tiles64 <= 512) {
+        plan.kernel = Plan::TILE_64;
+        if (dense) {
+            const int64_t fill = (plan.exact ? 256 : 512) / tiles64, most = blocks / (plan.exact ? 8 : 16);
+            plan.parts = (int)(fill < most ? fill : most);
+            if (plan.parts < 1) plan.parts = 1;
+        }
+        return plan;
+    }
+    // 256 x 256 tiles run one to a CU: with fewer than 192 too many of the 256 CUs are idle (2048^3, 64 tiles: 31.7
+    // us against 16.5; 4096 x 4096 x 8192, 256 tiles: 115 against 133)
+    if (!plan.exact && p.b.shift != 0 && p.mode != F8Problem::DEPTH && tiles(256) >= 192 && (!rows || group >= 256)) {
         plan.kernel = Plan::TILE_256;
         return plan;
     }
-    // Fewer tiles than the chip holds go in parts of at least 1024 k: one workgroup of the 8-bit instructions to a CU with
-    // four stages (1024 x 1024 x 8192, 64 tiles: 48 us whole, 22.4 in 4 parts; 23.8 with two stages; 2048 x 2048 x 2048,
-    // 256 tiles: 15.6, with two stages 17.4), two of the bf16 ones with two (2048 x 1504 x 8096: 80 us whole, 70 in 2;
-    // with four stages 78).
+    // 128 x 128 tiles: fewer than the chip holds go in parts of at least 1024 k. One workgroup of the 8-bit instructions to
+    // a CU with four stages (2048^3, 256 tiles: 16.5, with two stages 17.5), two of the bf16 ones with two (2048 x 1504 x
+    // 8096: 80 us whole, 70 in 2 parts; with four stages 78).
+    plan.kernel = Plan::TILE_128;
     if (dense) {
-        const int64_t blocks = ((int64_t)p.K + BLOCK - 1) / BLOCK, fill = (plan.exact ? 512 : 256) / tiles128;
+        const int64_t tiles128 = tiles(128), fill = (plan.exact ? 512 : 256) / tiles128;
         plan.parts = (int)(fill < blocks / 8 ? fill : blocks / 8);
         if (plan.parts < 1) plan.parts = 1;
         if (!plan.exact && tiles128 <= 256) plan.kernel = Plan::TILE_DEEP;
@@ -152,7 +213,11 @@ int64_t f8_work_bytes(const F8Problem &p) {
 hipError_t launch_f8(const F8Problem &given, hipStream_t s, const char **name) {
     Plan plan = plan_of(given);
     F8Problem p = given;
-    if (plan.copy_bytes > p.work_bytes) return launch_f8_any(p, s, name);  // no room for them
+    if (plan.copy_bytes > p.work_bytes) {  // no room for them: scales can stay as they are, rows cannot
+        if (plan.copy_a || plan.copy_b) return launch_f8_any(p, s, name);
+        plan.turn_a = plan.turn_b = false;
+        plan.copy_bytes = 0;
+    }
     uint8_t *work = static_cast<uint8_t *>(p.work);
     Copy copies[2] = {};
     if (plan.copy_a) {
@@ -171,17 +236,45 @@ hipError_t launch_f8(const F8Problem &given, hipStream_t s, const char **name) {
         ld = m.ld();
         work += m.bytes();
     }
-    if (plan.copy_bytes > 0) {
+    if (plan.copy_a || plan.copy_b) {
         const hipError_t e = align_rows(copies[0], copies[1], s);
+        if (e != hipSuccess) return e;
+    }
+    Turn turns[2] = {};
+    if (plan.turn_a) {
+        const int64_t rows = stored_a(p).rows, blocks = ((int64_t)p.K + BLOCK - 1) / BLOCK;
+        turns[0] = {p.a.s, reinterpret_cast<float *>(work), p.a.s_row, p.a.s_col, rows, blocks};
+        p.a.s = turns[0].to;
+        p.a.s_row = 1;
+        p.a.s_col = rows;
+        work += turned_bytes(rows, blocks);
+    }
+    if (plan.turn_b) {
+        const int64_t rows = p.N, blocks = ((int64_t)p.K + BLOCK - 1) / BLOCK;
+        turns[1] = {p.b.s, reinterpret_cast<float *>(work), p.b.s_row, p.b.s_col, rows, blocks};
+        p.b.s = turns[1].to;
+        p.b.s_row = 1;
+        p.b.s_col = rows;
+        work += turned_bytes(rows, blocks);
+    }
+    if (plan.turn_a || plan.turn_b) {
+        const int64_t rows = turns[0].rows > turns[1].rows ? turns[0].rows : turns[1].rows, gx = (rows + 63) / 64;
+        auto tiles = [](const Turn &t) { return (int)((t.blocks + 63) / 64 < 1024 ? (t.blocks + 63) / 64 : 1024); };
+        const int ya = tiles(turns[0]), yb = tiles(turns[1]);
+        hipLaunchKernelGGL(f8_turn_scales_kernel, dim3((unsigned)(gx < (1 << 16) ? gx : 1 << 16), (unsigned)(ya + yb)), dim3(256), 0, s,
+                           turns[0], turns[1], ya);
+        const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     p.work = work;
     p.work_bytes -= plan.copy_bytes;
     while (plan.parts > 1 && (int64_t)plan.parts * p.M * p.N * 4 > p.work_bytes) --plan.parts;
     static const char *const small[2] = {"f8_tile_128x128", "f8_tile_128x128_exact"};
+    static const char *const tiny[2] = {"f8_tile_64x64", "f8_tile_64x64_exact"};
     switch (plan.kernel) {
         case Plan::TILE_256: *name = "f8_tile_256x256"; return launch_f8_tile_256(p, s);
         case Plan::TILE_128: *name = small[plan.exact]; return launch_f8_tile_128(p, plan.exact, s, plan.parts);
+        case Plan::TILE_64: *name = tiny[plan.exact]; return launch_f8_tile_64(p, plan.exact, s, plan.parts);
         case Plan::TILE_DEEP: *name = "f8_tile_128x128_deep"; return launch_f8_tile_deep(p, s, plan.parts);
         case Plan::TOKEN: *name = "f8_token"; return launch_f8_token(p, plan.shape, s);
         default: return launch_f8_any(p, s, name);

@@ -33,6 +33,8 @@ typedef float __attribute__((may_alias)) f32_any;  // as lds_read16: no wait for
 
 template <int BN>
 __device__ __forceinline__ int nn_key(int row) {
+    static_assert(BN == 64 || BN == 128 || BN == 256, "4, 8 or 16 chunks a row");
+    if (BN == 64) return ((row >> 2) & 1) | ((row >> 4) & 1) << 1;
     return BN == 256 ? (row & 7) | ((row >> 4) & 1) << 3 : ((row >> 1) & 3) | ((row >> 4) & 1) << 2;
 }
 
@@ -177,12 +179,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
         // accumulator LAG tiles later, when its sum has left the matrix pipe. The sums of the last tiles of a
         // block are added in the next one's time, with that block's factors.
         constexpr int LAG = EXACT ? 1 : 2, RING = EXACT ? 2 : 4, TILES = MI * NI;
-        static_assert(TILES % RING == 0 && MI % 2 == 0 && NI > LAG, "a tile has one slot of the ring, a row one of two factors");
-        f32x4 d[RING];
+        static_assert(TILES % RING == 0 && MI % 2 == 0 && NI >= LAG, "a tile has one slot of the ring, a row one of two factors");
+        f32x4 d[RING] = {};
         i32x8 qa[2], qb[NI];  // codes that have been read: of the next two rows (row i in qa[i % 2]), of the next block's columns
         Frag a, b[NI];
-        float fa[2], sb_all; // row i's factor in fa[i % 2]; sb_all: of the block that is read, sb: of the one that is added
-        f32x4 sb[SB ? NI : 1];
+        float fa[2] = {0.0f, 0.0f}, sb_all;  // row i's factor in fa[i % 2]; sb_all: of the block that is read, sb: of the one that is added
+        // (with two rows of fragments a block's rows are all multiplied in the next one's time, when its stage is gone: its
+        // columns' factors wait in sb_in)
+        constexpr bool TWO = MI == 2;
+        f32x4 sb[SB ? NI : 1] = {}, sb_in[SB && TWO ? NI : 1];
         float sa_next[2];
         auto read_a = [&](const uint8_t *s, int i) {
             qa[i & 1] = whole(lds_read16(s + a_at + lo + i * 16 * BLOCK), lds_read16(s + a_at + hi + i * 16 * BLOCK));
@@ -197,7 +202,23 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
         };
         auto read_sb = [&](const uint8_t *s) {
 #pragma unroll
-            for (int j = 0; j < (SB ? NI : 0); ++j) sb[j] = __builtin_bit_cast(f32x4, lds_read16(s + sb_at + fg * 16 + j * 64));
+            for (int j = 0; j < (SB ? NI : 0); ++j)
+                (TWO ? sb_in : sb)[j] = __builtin_bit_cast(f32x4, lds_read16(s + sb_at + fg * 16 + j * 64));
+        };
+        // Tile t of a block is multiplied: its column's fragment and factor are the block's from the first row on
+        auto next_columns = [&](int t) {
+            if (t < NI) b[t] = frag(qb[t], type_b);
+        };
+        auto next_factors = [&](int t, const uint8_t *s) {  // behind the last sum of the block before
+            if constexpr (SB) {
+                if (t != LAG - 1) return;
+                if constexpr (TWO) {
+#pragma unroll
+                    for (int j = 0; j < NI; ++j) sb[j] = sb_in[j];
+                } else {
+                    read_sb(s);
+                }
+            }
         };
         auto add = [&](int t) {  // tile t of a block's
             const int i = t / NI, j = t % NI;
@@ -232,19 +253,25 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
                 for (int j = 0; j < NI; ++j) read_b(cur, j);
                 read_a(cur, 0);
                 read_a(cur, 1);
+                if constexpr (SB && TWO) read_sb(cur);
+                if constexpr (START == TILES) {
+#pragma unroll
+                    for (int m = 0; m < PIECES; ++m) dma(m, t + STAGES - 1, next);
+                }
             }
 #pragma unroll
             for (int n = START; n < TILES; ++n) {
                 const int i = n / NI - 2, j = n % NI;  // rows -2 and -1: the last of block t - 1
                 const int id = ((i + MI) % MI) * NI + j;
                 if (j == 0) begin_row(id / NI);
-                if (i == 0) b[j] = frag(qb[j], type_b);
+                next_columns(id);
                 tile(id);
                 if constexpr (!EXACT) __builtin_amdgcn_sched_barrier(0);  // (the sum that is added next needs time)
                 if (!FIRST || n - LAG >= START) add((id + TILES - LAG) % TILES);
-                if (SB && i == 0 && j == LAG - 1) read_sb(cur);  // (the block before has been added)
+                next_factors(id, cur);
                 if (j == 0) read_a(cur, i + 2);
                 if (i == -1) read_b(cur, j);
+                if (SB && TWO && i == -1 && j == NI - 1) read_sb(cur);
 #pragma unroll
                 for (int m = 0; m < PIECES; ++m)
                     if (m * (TILES - START) / PIECES + START == n) dma(m, t + STAGES - 1, next);
@@ -292,8 +319,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
         for (int n = 0; n < 2 * NI + LAG; ++n) {
             const int id = (MI - 2) * NI + n;
             if (n < 2 * NI && n % NI == 0) begin_row(id / NI);
-            if (n < 2 * NI) tile(id);
-            add(id - LAG);
+            if (n < 2 * NI) {
+                if (TWO) next_columns(id);
+                tile(id);
+            }
+            add((id + TILES - LAG) % TILES);
+            if (TWO && n < 2 * NI) next_factors(id, smem);
         }
         wait_vmcnt<0>();  // no LDS DMA may still be in flight when the workgroup retires
     }
@@ -323,7 +354,7 @@ hipError_t launch_tile(const F8Problem &p, hipStream_t s, int splits) {
     // tile rows that share B's panels: 8, in groups as many as a group has on the average (the others have another B)
     int group_m = 8;
     if (p.mode == F8Problem::ROWS) {
-        const int64_t mean = ((int64_t)p.M / p.experts + BM - 1) / BM;
+        const int64_t mean = ((int64_t)p.mean_rows + BM - 1) / BM;
         group_m = (int)(mean < 1 ? 1 : mean < 8 ? mean : 8);
     }
     F8Problem q = p;

@@ -84,6 +84,7 @@ struct F8Problem {
     const int32_t *offsets, *counts;
     const int32_t *slots;  // row r of A is token slots[r] / top_k (of a_rows), or null: row r
     int top_k, a_rows;
+    int mean_rows;  // ROWS: a group's, on the average
     void *work;
     int64_t work_bytes;
 };
@@ -188,6 +189,7 @@ int64_t f8_work_bytes(const F8Problem &p);
 // tiles fed by DMA, what f8_tile_takes; `exact` as in gemm_f8_tile.h; 128-wide ones in parts of k through the workspace
 hipError_t launch_f8_tile_256(const F8Problem &p, hipStream_t s);
 hipError_t launch_f8_tile_128(const F8Problem &p, bool exact, hipStream_t s, int splits);
+hipError_t launch_f8_tile_64(const F8Problem &p, bool exact, hipStream_t s, int splits);
 hipError_t launch_f8_tile_deep(const F8Problem &p, hipStream_t s, int splits);
 hipError_t launch_f8_join(const F8Problem &p, hipStream_t s, int splits);
 // few rows of A (in each group), B stored N x K

@@ -272,9 +272,13 @@ def test_beta_zero_never_reads_C_and_alpha_zero_never_reads_the_operands():
     C = torch.ones(40, 200, device="cuda")
     assert bool((rt.gemm_f8(bad, B, C, alpha=0.0, beta=2.0) == 2.0).all())
     assert bool((rt.gemm_f8(bad, B, alpha=0.0) == 0.0).all())
+    a, b, _, _ = products(rng, 700, 300, 257, f8.E4M3, f8.E4M3, "nt")  # more rows than go straight to registers, unaligned
+    C = torch.ones(700, 300, device="cuda", dtype=torch.bfloat16)
+    rt.gemm_f8(on_device(*a, f8.E4M3, 1, False, "tight"), on_device(*b, f8.E4M3, 128, True, "tight"), C, alpha=0.0, beta=-3.0)
+    assert bool((C == -3.0).all())
 
 
-@pytest.mark.parametrize("M,N,K", [(0, 5, 128), (5, 0, 128), (5, 7, 0), (0, 0, 0)])
+@pytest.mark.parametrize("M,N,K", [(0, 5, 128), (5, 0, 128), (5, 7, 0), (0, 0, 0), (300, 513, 0), (0, 300, 1024)])
 def test_empty(M, N, K):
     e = torch.float8_e4m3fn
 
