@@ -31,7 +31,7 @@ __global__ __launch_bounds__(JOIN_NT) void f8_join_kernel(F8Problem p, int split
     }
 }
 
-constexpr int64_t SPAN = int64_t(1) << 31;  // bytes that a descriptor's offsets may reach
+constexpr int64_t SPAN = int64_t(1) << 31;  // bytes that the offsets of scales may reach
 
 // Rows that DMA reads begin at multiples of 16 bytes; operands that lie otherwise are copied into a workspace first.
 bool a_aligned(const F8Problem &p) { return aligned16(p.a.q) && p.a.row % 16 == 0; }
@@ -125,8 +125,7 @@ bool tile_takes(const F8Problem &p) {
     const bool nn = b.step != 1;
     const int64_t ldb = nn ? b.step : b.row, kb = ((int64_t)p.K + BLOCK - 1) / BLOCK;
     if (a.step != 1 || b.type != REGTILE_F8_E4M3) return false;
-    const int64_t rows_a = p.slots != nullptr ? p.a_rows : 256;
-    if (rows_a * a.row + p.K + BLOCK >= SPAN || (nn ? ((int64_t)p.K + BLOCK) * ldb + 256 : 256 * ldb + p.K + BLOCK) >= SPAN) return false;
+    if (!addr::f8_reach(false, p.slots != nullptr ? p.a_rows : 256, p.K, a.row) || !addr::f8_reach(nn, 256, p.K, ldb)) return false;
     const int64_t all_a = p.slots != nullptr ? p.a_rows : p.M;
     return ((all_a >> a.shift) * a.s_row + kb * a.s_col) * 4 < SPAN && (((int64_t)p.N >> b.shift) * b.s_row + kb * b.s_col) * 4 < SPAN;
 }

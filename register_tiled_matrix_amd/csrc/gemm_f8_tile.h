@@ -3,7 +3,7 @@
 //
 // A stage in LDS is one block of 128 k: BM + BN rows of 128 codes and as many scales. While one is
 // multiplied the next STAGES - 1 are on their way, and one barrier a block hands over. Two stages let two workgroups of
-// 128 x 128 share a CU; with too few tiles for that, four hide the latency of memory better (DESIGN_FIGURE). A block's products are summed from
+// 128 x 128 share a CU; with too few tiles for that, three and four hide the latency of memory better. A block's products are summed from
 // zero by the matrix instructions and enter the fp32 accumulators as c += (sa sb) sum, so the scales cost a
 // vector instruction for each of a lane's sums (two where B has a scale for each column), and the other wave
 // of the SIMD keeps the matrix pipe busy meanwhile. B's fragment is the first operand: a lane holds 4
@@ -12,10 +12,9 @@
 // EXACT: sums of exact products, four 16x16x32 bf16 MFMAs on codes expanded in registers; else one
 // 16x16x128 8-bit MFMA at twice the rate (f8_common.h has what that loses).
 //
-// LDS: K-contiguous rows of 8 chunks of 16 codes, chunk c of row r at slot c ^ slab_key<8, 16>(r); a lane reads
-// chunks g and 4 + g (g = lane / 16), for both operands the same k. A K x N operand keeps its storage: rows
-// of BN codes at one k, read by transposing reads (8 k of 16 columns for 16 lanes), chunk c of row r at slot
-// c ^ nn_key(r), which spreads the 16 rows that 32 lanes read over all banks.
+// LDS (tile_addressing.h has the layouts): K-contiguous rows of 128 codes, of which a lane reads chunks g and 4 + g (g =
+// lane / 16), for both operands the same k. A K x N operand keeps its storage: rows of BN codes at one k, read by
+// transposing reads (8 k of 16 columns for 16 lanes).
 //
 // Edges: rows past the last are loaded from the last, chunks past N from the last one that holds an element. What
 // lies past K in the last block (bytes between rows, or zeros from behind the descriptor) is overwritten with
@@ -30,13 +29,6 @@ namespace regtile {
 namespace f8 {
 using namespace mfma;
 typedef float __attribute__((may_alias)) f32_any;  // as lds_read16: no wait for DMA
-
-template <int BN>
-__device__ __forceinline__ int nn_key(int row) {
-    static_assert(BN == 64 || BN == 128 || BN == 256, "4, 8 or 16 chunks a row");
-    if (BN == 64) return ((row >> 2) & 1) | ((row >> 4) & 1) << 1;
-    return BN == 256 ? (row & 7) | ((row >> 4) & 1) << 3 : ((row >> 1) & 3) | ((row >> 4) & 1) << 2;
-}
 
 // Transposing LDS read of 8-bit elements (ds_read_b64_tr_b8): in each group of 16 lanes, lane 2 j + h gives the
 // address of 8 bytes at columns 8 h .. 8 h + 7 of row j, and lane i receives column i of rows 0 .. 7 (measured).
@@ -99,28 +91,21 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
         // Descriptors begin at the tile's first row (where rows are gathered: at A) and end behind the last chunk
         // that holds an element; chunks past it arrive as zeros. Lanes hold offsets, the block's is uniform.
         const bool gather = p.slots != nullptr;
-        auto span = [](int64_t rows, int64_t ld, int width) { return (uint32_t)((rows - 1) * ld + ((width + 15) & ~15)); };
         const int n_rows = min(BN, p.N - n0);
         const rsrc_t a_rsrc = make_rsrc(gather ? w.a.q : w.a.q + (int64_t)w.row0 * w.a.row,
-                                        span(gather ? p.a_rows : w.used, w.a.row, K));
-        const rsrc_t b_rsrc = NN ? make_rsrc(w.b.q + n0, span(K, w.b.step, p.N - n0))
-                                 : make_rsrc(w.b.q + (int64_t)n0 * w.b.row, span(n_rows, w.b.row, K));
+                                        addr::f8_span(gather ? p.a_rows : w.used, w.a.row, K));
+        const rsrc_t b_rsrc = NN ? make_rsrc(w.b.q + n0, addr::f8_span(K, w.b.step, p.N - n0))
+                                 : make_rsrc(w.b.q + (int64_t)n0 * w.b.row, addr::f8_span(n_rows, w.b.row, K));
         uint32_t av[JA], bv[JB];
 #pragma unroll
         for (int j = 0; j < JA; ++j) {
-            const int r = (wave * JA + j) * 8 + (lane >> 3), c = (lane & 7) ^ addr::slab_key<8, 16>(r), at = min(r, w.used - 1);
-            av[j] = (uint32_t)((gather ? a_row(p, w, at) : at) * w.a.row) + c * 16;
+            const int q = wave * JA + j, at = min(addr::f8_row(q, lane), w.used - 1);
+            av[j] = addr::f8_lane(q, lane, gather ? a_row(p, w, at) : at, w.a.row);
         }
 #pragma unroll
         for (int j = 0; j < JB; ++j) {
-            if constexpr (NN) {
-                constexpr int CH = BN / 16;
-                const int slot = (wave * JB + j) * 64 + lane, r = slot / CH, c = (slot % CH) ^ nn_key<BN>(r);
-                bv[j] = (uint32_t)(r * w.b.step) + min(c * 16, (n_rows - 1) & ~15);
-            } else {
-                const int r = (wave * JB + j) * 8 + (lane >> 3), c = (lane & 7) ^ addr::slab_key<8, 16>(r);
-                bv[j] = (uint32_t)(min(r, n_rows - 1) * w.b.row) + c * 16;
-            }
+            const int q = wave * JB + j;
+            bv[j] = NN ? addr::f8_nn_lane<BN>(q, lane, n_rows, w.b.step) : addr::f8_lane(q, lane, min(addr::f8_row(q, lane), n_rows - 1), w.b.row);
         }
         // scales: a wave brings 64 rows' of A or 64 columns' of B
         static_assert(BM % 64 == 0, "a wave's scales are all of one operand");
@@ -135,9 +120,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
         auto dma = [&](int n, int block, uint8_t *to) {
             const int kb = first + min(block, blocks - 1);
             if (n < JA)
-                dma16_buf(a_rsrc, av[n], kb * BLOCK, to + (wave * JA + n) * 1024);
+                dma16_buf(a_rsrc, av[n], addr::f8_block(false, kb, 0), to + (wave * JA + n) * 1024);
             else if (n < JA + JB)
-                dma16_buf(b_rsrc, bv[n - JA], NN ? (uint32_t)(kb * BLOCK * w.b.step) : kb * BLOCK, to + BM * BLOCK + (wave * JB + n - JA) * 1024);
+                dma16_buf(b_rsrc, bv[n - JA], addr::f8_block(NN, kb, w.b.step), to + BM * BLOCK + (wave * JB + n - JA) * 1024);
             else
                 dma4_buf(s_rsrc, sv, kb * s_step, to + (BM + BN) * BLOCK + wave * 256);
         };
@@ -148,7 +133,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
         const int key = addr::slab_key<8, 16>(fr), lo = (fg ^ key) * 16, hi = ((fg + 4) ^ key) * 16;
         const int a_at = (wm * MI * 16 + fr) * BLOCK, b_at = BM * BLOCK + (wn * NI * 16 + fr) * BLOCK;
         const int sa_at = (BM + BN) * BLOCK + (wm * MI * 16 + fr) * 4, sb_at = (BM + BN) * BLOCK + (BM + wn * NI * 16) * 4;
-        const int tr_row = fg * 16 + (fr >> 1), tr_at = BM * BLOCK + tr_row * BN + (fr & 1) * 8, tr_key = nn_key<BN>(tr_row);
+        const int tr_row = fg * 16 + (fr >> 1), tr_at = BM * BLOCK + tr_row * BN + (fr & 1) * 8, tr_key = addr::f8_nn_key<BN>(tr_row);
         auto whole = [](u32x4 l, u32x4 h) {
             return i32x8{(int)l[0], (int)l[1], (int)l[2], (int)l[3], (int)h[0], (int)h[1], (int)h[2], (int)h[3]};
         };

@@ -203,6 +203,39 @@ REGTILE_HD int mx_wide_parts(bool ta, int M, int N, int K, int64_t lda) {
 // bits: cols goes up to 2^31 - 1. Argument checks, launches and kernels all count with these.
 REGTILE_HD int64_t mx_row_bytes(bool fp4, int64_t cols) { return fp4 ? (cols + 1) / 2 : cols; }
 REGTILE_HD int64_t mx_units(int64_t cols) { return (cols + 7) / 8; }
+// The 8-bit float tiles (gemm_f8_tile.h). LDS row r of a K-contiguous operand holds the 8 chunks of 16 codes of a block
+// of 128 k, chunk c at slot c ^ slab_key<8, 16>(r); of a K x N operand, the BN codes of one k, chunk c at slot
+// c ^ f8_nn_key<BN>(r), which spreads the 16 rows that 32 lanes of a transposing read touch over all banks. DMA instruction q
+// of a block brings slots 64 q .. 64 q + 63, one to a lane. Descriptors span `rows` rows and end behind the last chunk of
+// 16 that holds an element of the last one; leading dimensions are multiples of 16, so that no chunk straddles an end.
+REGTILE_HD uint32_t f8_span(int64_t rows, int64_t ld, int width) { return (uint32_t)((rows - 1) * ld + ((width + 15) & ~15)); }
+REGTILE_HD int f8_row(int q, int lane) { return q * 8 + (lane >> 3); }
+REGTILE_HD int f8_chunk(int q, int lane) { return (lane & 7) ^ slab_key<8, 16>(f8_row(q, lane)); }
+// `row`: the operand's row (from the descriptor's base) that LDS row f8_row(q, lane) is loaded from
+REGTILE_HD uint32_t f8_lane(int q, int lane, int64_t row, int64_t ld) { return (uint32_t)(row * ld) + f8_chunk(q, lane) * 16; }
+template <int BN>
+REGTILE_HD int f8_nn_key(int row) {
+    static_assert(BN == 64 || BN == 128 || BN == 256, "4, 8 or 16 chunks a row");
+    if (BN == 64) return ((row >> 2) & 1) | ((row >> 4) & 1) << 1;
+    return BN == 256 ? (row & 7) | ((row >> 4) & 1) << 3 : ((row >> 1) & 3) | ((row >> 4) & 1) << 2;
+}
+template <int BN>
+REGTILE_HD int f8_nn_row(int q, int lane) { return (q * 64 + lane) / (BN / 16); }
+template <int BN>
+REGTILE_HD int f8_nn_chunk(int q, int lane) { return ((q * 64 + lane) % (BN / 16)) ^ f8_nn_key<BN>(f8_nn_row<BN>(q, lane)); }
+// columns: of the operand in this tile; chunks behind the last that holds one are loaded from it
+template <int BN>
+REGTILE_HD uint32_t f8_nn_lane(int q, int lane, int columns, int64_t ld) {
+    const int c = f8_nn_chunk<BN>(q, lane) * 16, last = (columns - 1) & ~15;
+    return (uint32_t)(f8_nn_row<BN>(q, lane) * ld) + (uint32_t)(c < last ? c : last);
+}
+// Uniform part of block kb: k0 codes, or k0 rows
+REGTILE_HD uint32_t f8_block(bool nn, int kb, int64_t ld) { return nn ? (uint32_t)(kb * (int64_t)128 * ld) : (uint32_t)kb * 128u; }
+// Operands whose tiles stay within reach of 32-bit offsets: K-contiguous rows (256 of them, or all where they are
+// gathered), or K rows of a K x N operand
+REGTILE_HD bool f8_reach(bool nn, int64_t rows, int64_t K, int64_t ld) {
+    return (nn ? (K + 128) * ld + 256 : rows * ld + K + 128) < (int64_t(1) << 31);
+}
 // The register-staged kernel's gather of an M/N-contiguous operand with `cols` columns goes
 // through a per-slab descriptor (8-byte runs) when this holds, else through predicated loads.
 REGTILE_HD bool gather_desc_takes(int64_t cols, int64_t ld) { return runs_fit(cols, ld, 4); }
