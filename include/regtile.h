@@ -270,10 +270,10 @@ int64_t regtile_gemm_mx_workspace_ex(int format, int trans_a, int trans_b, int M
  *                           bytes and in floats
  *   rows, cols, stack       sizes; stack is 1 for a single matrix
  *   type, block_rows        regtile_f8_type; 1 or 128
- * No alignment is needed; products of more than a few rows want codes, ld and codes_stack to be multiples of 16, and
- * copy operands that are not into their workspace first (without one they are slow). Products read
- * aligned rows in aligned chunks of 16 bytes: bytes behind a row's end that share a chunk with its last element may
- * be read, whatever they hold, and have no influence.
+ * No alignment is needed. Products of more than a few rows want codes, ld and codes_stack to be multiples of 16,
+ * and copy operands that are not into their workspace first (without one they are slow). They read aligned rows
+ * in aligned chunks of 16 bytes: bytes behind a row's end that share a chunk with its last element may be read,
+ * whatever they hold, and have no influence.
  */
 enum regtile_f8_type { REGTILE_F8_E4M3 = 0, REGTILE_F8_E5M2 = 1 };
 typedef struct regtile_f8_matrix {
@@ -289,8 +289,8 @@ typedef struct regtile_f8_matrix {
 /*
  * regtile_quantize_f8 -- X (rows x cols, row-major, of a regtile_mx_dtype) to such a matrix. With a the largest
  * magnitude of a block and top the type's largest value (448, 57344): s = max(a * (1 / top), 2^-126), 1 / top and
- * the product rounded to fp32, and each code is the nearest value of the type to x / s, ties to even. A block with a NaN or an infinity gets a NaN
- * scale and zero codes.
+ * the product rounded to fp32, and each code is the nearest value of the type to x / s, ties to even. A block with a
+ * NaN or an infinity gets a NaN scale and zero codes.
  *   dtype (arg 1), transpose (2) 0, or 1: Q is the transpose of X, its blocks along X's rows (block_rows 1 only),
  *   rows, cols (3-4), X, ldx (5-6)
  *   index (7)  NULL, or one row number of X for each row that is taken (each of Q's rows, or with transpose
@@ -353,12 +353,14 @@ int64_t regtile_order_experts_workspace(int tokens, int k, int experts);
  * regtile_route_experts -- a router: for each token the k experts with the largest values v, the lowest number among
  * equals, and their weights. Scores s = softmax(logits) or sigmoid(logits); v = s + bias (or s). With `groups` > 1
  * the experts fall into groups of equal size, and only the top_groups best are chosen from: a group counts as much
- * as its best v (group_best 1) or the sum of its two best (2). Weights: s, divided by the sum of the chosen s if
+ * as its best v (group_best 1) or the sum of its two best (2; its one v, where no second expert can be chosen). Without
+ * a bias, and with groups by their best, experts are compared by their logits, which scores only grow with: scores that
+ * round to one value, or to 0, still have their order. Weights: s, divided by the sum of the chosen s if
  * `renormalize`, times `scale`; in the order of the choice.
  *   An expert with logit -inf (or bias -inf or NaN) is never chosen; slots for which no expert is left hold -1 and
  *   weight 0 (a token whose logits are all -inf routes nowhere). A row with a NaN or +inf gets experts 0 .. k - 1
  *   and NaN weights. Where the sum of the chosen s is 0 the weights are 0.
- *   score (arg 1), dtype (2, of the logits), tokens (3), experts (4, up to 1024), k (5, up to 64), groups (6, up to
+ *   score (arg 1), dtype (2, of the logits), tokens (3, up to 2^26 - 4), experts (4, up to 1024), k (5, up to 64), groups (6, up to
  *   64, a divisor of experts), top_groups (7), group_best (8), renormalize (9), scale (10), logits, ldl (11-12),
  *   bias (13, experts floats, or NULL), chosen (14, tokens x k), weights (15, the same), stream (16)
  * regtile_route_experts_grad -- the gradient with respect to the logits (of their dtype) from that with respect to

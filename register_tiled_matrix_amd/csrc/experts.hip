@@ -10,7 +10,8 @@
 // computed, by the lane that holds the choice, in 64 bits.
 //
 // order: a stable counting sort. A wave finds the lanes with its own expert by ballots over the index's bits,
-// so that counts and ranks need no atomics and come out the same every time.
+// so that counts and ranks need no atomics and come out the same every time. A workgroup takes a chunk of the slots
+// (from 4 million on several), finds its place by adding up the counts of those before it, and there are at most 1024.
 #include "f8_common.h"
 
 namespace regtile {
@@ -347,27 +348,30 @@ __device__ __forceinline__ void count_chunk(const OrderProblem &p, int *counts, 
     __syncthreads();
 }
 
-__global__ __launch_bounds__(ORDER_NT) void order_count_kernel(OrderProblem p, int bits) {
+__global__ __launch_bounds__(ORDER_NT) void order_count_kernel(OrderProblem p, int bits, int chunks) {
     __shared__ int counts[ORDER_WAVES * MOST_EXPERTS];
-    const int64_t n = (int64_t)p.tokens * p.k, first = (int64_t)blockIdx.x * CHUNK;
-    int e_of[MOST];
-    count_chunk(p, counts, first, min(n, first + CHUNK), CHUNK / ORDER_WAVES, bits, e_of);
+    const int64_t n = (int64_t)p.tokens * p.k, span = (int64_t)chunks * CHUNK, end = min(n, (blockIdx.x + 1) * span);
     const int e = threadIdx.x;
-    if (e < p.experts) {
-        int sum = 0;
-        for (int w = 0; w < ORDER_WAVES; ++w) sum += counts[w * p.experts + e];
-        p.work[(int64_t)blockIdx.x * p.experts + e] = sum;
+    int e_of[MOST], sum = 0;
+    for (int64_t first = blockIdx.x * span; first < end; first += CHUNK) {
+        count_chunk(p, counts, first, min(end, first + CHUNK), CHUNK / ORDER_WAVES, bits, e_of);
+        if (e < p.experts)
+            for (int w = 0; w < ORDER_WAVES; ++w) sum += counts[w * p.experts + e];
+        __syncthreads();
     }
+    if (e < p.experts) p.work[(int64_t)blockIdx.x * p.experts + e] = sum;
 }
 
-__global__ __launch_bounds__(ORDER_NT) void order_place_kernel(OrderProblem p, int bits) {
+__global__ __launch_bounds__(ORDER_NT) void order_place_kernel(OrderProblem p, int bits, int chunks) {
     __shared__ int counts[ORDER_WAVES * MOST_EXPERTS];
     __shared__ int wave_room[ORDER_WAVES];
     __shared__ int2 ends[MOST_EXPERTS];  // of a group's rows and of its room
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, groups = gridDim.x;
-    const int64_t n = (int64_t)p.tokens * p.k, first = (int64_t)blockIdx.x * CHUNK, end = min(n, first + CHUNK);
+    const int64_t n = (int64_t)p.tokens * p.k, span = (int64_t)chunks * CHUNK;
+    int64_t first = blockIdx.x * span, end = min(n, first + CHUNK);
+    const int64_t last = min(n, first + span);
     // a wave's part of the chunk, in whole 64s
-    const int per = ((int)((end - first + ORDER_WAVES - 1) / ORDER_WAVES) + 63) / 64 * 64;
+    int per = ((int)((end - first + ORDER_WAVES - 1) / ORDER_WAVES) + 63) / 64 * 64;
     int e_of[MOST];
     count_chunk(p, counts, first, end, per, bits, e_of);
     int before = 0, all = 0;
@@ -396,13 +400,17 @@ __global__ __launch_bounds__(ORDER_NT) void order_place_kernel(OrderProblem p, i
         if (w < wave) start += wave_room[w];
         used += wave_room[w];
     }
+    int at_expert = start + before;  // the next row of this thread's expert
+    auto begin_waves = [&]() {       // counts to first rows
+        if (tid < p.experts)
+            for (int w = 0; w < ORDER_WAVES; ++w) {
+                const int c = counts[w * p.experts + tid];
+                counts[w * p.experts + tid] = at_expert;
+                at_expert += c;
+            }
+    };
+    begin_waves();
     if (tid < p.experts) {
-        int at = start + before;
-        for (int w = 0; w < ORDER_WAVES; ++w) {
-            const int c = counts[w * p.experts + tid];
-            counts[w * p.experts + tid] = at;
-            at += c;
-        }
         if (blockIdx.x == 0) {
             p.offsets[tid] = start;
             p.counts[tid] = all;
@@ -416,21 +424,31 @@ __global__ __launch_bounds__(ORDER_NT) void order_place_kernel(OrderProblem p, i
     for (int e = (int)blockIdx.x * ORDER_WAVES + wave; e < p.experts; e += groups * ORDER_WAVES)
         for (int r = ends[e].x + lane; r < ends[e].y; r += 64) p.slots[r] = -1;
     int *mine = counts + wave * p.experts;
+    while (true) {
 #pragma unroll
-    for (int i = 0; i < MOST; ++i) {
-        if (i * 64 >= per) break;
-        const int64_t slot = first + wave * per + i * 64 + lane;
-        const int e = e_of[i];
-        const u64 m = same(e, bits);
-        int at = -1;
-        if (e < p.experts) at = mine[e] + __popcll(m & ((1ull << lane) - 1));
-        __builtin_amdgcn_wave_barrier();
-        if (e < p.experts && 63 - __clzll((long long)m) == lane) mine[e] = at + 1;
-        __builtin_amdgcn_wave_barrier();
-        if (slot < end) {
-            p.position[slot] = at;
-            if (at >= 0) p.slots[at] = (int32_t)slot;
+        for (int i = 0; i < MOST; ++i) {
+            if (i * 64 >= per) break;
+            const int64_t slot = first + wave * per + i * 64 + lane;
+            const int e = e_of[i];
+            const u64 m = same(e, bits);
+            int at = -1;
+            if (e < p.experts) at = mine[e] + __popcll(m & ((1ull << lane) - 1));
+            __builtin_amdgcn_wave_barrier();
+            if (e < p.experts && 63 - __clzll((long long)m) == lane) mine[e] = at + 1;
+            __builtin_amdgcn_wave_barrier();
+            if (slot < end) {
+                p.position[slot] = at;
+                if (at >= 0) p.slots[at] = (int32_t)slot;
+            }
         }
+        first += CHUNK;
+        if (first >= last) return;
+        end = min(last, first + CHUNK);
+        per = CHUNK / ORDER_WAVES;
+        __syncthreads();
+        count_chunk(p, counts, first, end, per, bits, e_of);
+        begin_waves();
+        __syncthreads();
     }
 }
 
@@ -551,12 +569,16 @@ hipError_t go(F f, dim3 grid, unsigned threads, hipStream_t s, void **args) {
 
 }  // namespace
 
+// What a launch of 4 tokens to 256 threads counts in 32 bits
+constexpr int MOST_TOKENS = (1 << 26) - 4;
+
 hipError_t launch_route(const RouteProblem &p, hipStream_t s, const char **name) {
     // by the logits where the scores grow with them and nothing is added to them
     const bool wide = p.bias != nullptr || (p.groups > 1 && p.group_best == 2);
     *name = wide ? "route_scores" : "route_logits";
     RouteProblem q = p;
     void *args[] = {&q};
+    if (p.tokens > MOST_TOKENS) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)(((int64_t)p.tokens + 3) / 4));
     auto pick = [&](auto narrow_f, auto wide_f) { return go(wide ? wide_f : narrow_f, grid, NT, s, args); };
     if (p.experts <= 64) return pick(route_kernel<1, false>, route_kernel<1, true>);
@@ -570,6 +592,7 @@ hipError_t launch_route_grad(const RouteProblem &p, hipStream_t s, const char **
     *name = "route_grad";
     RouteProblem q = p;
     void *args[] = {&q};
+    if (p.tokens > MOST_TOKENS) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)(((int64_t)p.tokens + 3) / 4));
     if (p.experts <= 64) return go(route_grad_kernel<1>, grid, NT, s, args);
     if (p.experts <= 128) return go(route_grad_kernel<2>, grid, NT, s, args);
@@ -579,18 +602,26 @@ hipError_t launch_route_grad(const RouteProblem &p, hipStream_t s, const char **
 }
 
 // One workgroup orders a chunk by itself; more of them count first, through the workspace.
+namespace {
+constexpr int64_t MOST_GROUPS = 1024;
+int order_chunks(int64_t slots) { return (int)((slots + MOST_GROUPS * CHUNK - 1) / (MOST_GROUPS * CHUNK)); }  // to a workgroup
+int64_t order_groups(int64_t slots) {
+    const int64_t span = (int64_t)order_chunks(slots) * CHUNK;
+    return slots > 0 ? (slots + span - 1) / span : 1;
+}
+}  // namespace
 int64_t order_work_bytes(int64_t slots, int experts) {
-    const int64_t groups = (slots + CHUNK - 1) / CHUNK;
+    const int64_t groups = order_groups(slots);
     return groups > 1 ? groups * experts * 4 : 0;
 }
 
 hipError_t launch_order(const OrderProblem &p, hipStream_t s, const char **name) {
     const int64_t n = (int64_t)p.tokens * p.k;
-    const unsigned groups = (unsigned)(n > CHUNK ? (n + CHUNK - 1) / CHUNK : 1);
-    int bits = 1;
+    const unsigned groups = (unsigned)order_groups(n);
+    int bits = 1, chunks = order_chunks(n);
     while ((p.experts >> bits) != 0) ++bits;  // 0 .. experts
     OrderProblem q = p;
-    void *args[] = {&q, &bits};
+    void *args[] = {&q, &bits, &chunks};
     *name = "order_experts";
     if (groups > 1) {
         const hipError_t e = go(order_count_kernel, dim3(groups), ORDER_NT, s, args);

@@ -123,9 +123,10 @@ __global__ __launch_bounds__(256) void f8_turn_scales_kernel(Turn a, Turn b, int
 bool tile_takes(const F8Problem &p) {
     const F8Operand &a = p.a, &b = p.b;
     const bool nn = b.step != 1;
-    const int64_t ldb = nn ? b.step : b.row, kb = ((int64_t)p.K + BLOCK - 1) / BLOCK;
+    auto whole = [](int64_t ld) { return (ld + 15) / 16 * 16; };  // (a copy's rows may be that far apart)
+    const int64_t lda = whole(a.row), ldb = whole(nn ? b.step : b.row), kb = ((int64_t)p.K + BLOCK - 1) / BLOCK;
     if (a.step != 1 || b.type != REGTILE_F8_E4M3) return false;
-    if (!addr::f8_reach(false, p.slots != nullptr ? p.a_rows : 256, p.K, a.row) || !addr::f8_reach(nn, 256, p.K, ldb)) return false;
+    if (!addr::f8_reach(false, p.slots != nullptr ? p.a_rows : 256, p.K, lda) || !addr::f8_reach(nn, 256, p.K, ldb)) return false;
     const int64_t all_a = p.slots != nullptr ? p.a_rows : p.M;
     return ((all_a >> a.shift) * a.s_row + kb * a.s_col) * 4 < SPAN && (((int64_t)p.N >> b.shift) * b.s_row + kb * b.s_col) * 4 < SPAN;
 }

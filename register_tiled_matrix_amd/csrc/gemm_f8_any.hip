@@ -18,10 +18,10 @@ using namespace mfma;
 constexpr int T = 64, NT = 256, LD = BLOCK + 16;
 
 // Chunk c (0 .. 511) of an operand's 64 x 128 block from `k0` on; src[0]: a K-contiguous chunk's row
-__device__ __forceinline__ void stage(uint8_t *lds, const F8Operand &o, const uint8_t *row_of_chunk, int c, int row0, int rows, int k0,
+__device__ __forceinline__ void stage(uint8_t *lds, const F8Operand &o, const uint8_t *row_of_chunk, int c, int row0, int rows, int64_t k0,
                                       int K) {
     if (o.step == 1) {
-        const int r = c >> 3, kk = (c & 7) * 16, left = r < rows ? K - k0 - kk : 0;
+        const int r = c >> 3, kk = (c & 7) * 16, left = r < rows ? (int)(K - k0) - kk : 0;
         uint32_t d[4] = {0, 0, 0, 0};
         const uint8_t *p = row_of_chunk + k0 + kk;
         if (left >= 16) {
@@ -35,7 +35,7 @@ __device__ __forceinline__ void stage(uint8_t *lds, const F8Operand &o, const ui
         *reinterpret_cast<u32x4 *>(lds + r * LD + kk) = v;
     } else {
         const int kk = c >> 2, r = (c & 3) * 16;
-        const uint8_t *p = o.q + (int64_t)(k0 + kk) * o.step + row0 + r;
+        const uint8_t *p = o.q + (k0 + kk) * o.step + row0 + r;
         const int left = k0 + kk < K ? rows - r : 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) lds[(r + i) * LD + kk] = i < left ? p[i] : (uint8_t)0;
@@ -70,7 +70,7 @@ __global__ __launch_bounds__(NT) void f8_any_kernel(F8Problem p, int tiles_n, bo
     }
     f32x4 acc[2][2] = {};
     const int K = w.used > 0 ? w.K : 0;
-    for (int k0 = 0; k0 < K; k0 += BLOCK) {
+    for (int64_t k0 = 0; k0 < K; k0 += BLOCK) {  // (K may be the largest int)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             stage(la, w.a, arow[j], tid + NT * j, w.row0, w.used, k0, K);

@@ -207,3 +207,50 @@ def test_graphs_replayed_in_turn():
         torch.cuda.synchronize()
         for A, B, C in held:
             assert torch.equal(C, rt.gemm_f8(A, B))
+
+
+def test_millions_of_slots():
+    """More slots than 1024 chunks hold: workgroups then take several, and the order is still the stable sort's."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    tokens, k, E = 1_400_001, 3, 37
+    chosen = torch.randint(-1, E + 1, (tokens, k), device="cuda", generator=gen).int()
+    for align in (1, 128):
+        rows = rt.expert_rows(chosen, E, align=align)
+        flat = chosen.flatten().long()
+        valid = (flat >= 0) & (flat < E)
+        key, order = torch.sort(torch.where(valid, flat, E), stable=True)
+        counts = torch.bincount(key, minlength=E + 1)[:E]
+        room = (counts + align - 1) // align * align
+        offsets = torch.cat([torch.zeros(1, device="cuda", dtype=torch.int64), room.cumsum(0)])
+        assert torch.equal(rows.counts.long(), counts) and torch.equal(rows.offsets.long(), offsets)
+        n = int(counts.sum())
+        begin = counts.cumsum(0) - counts
+        at = torch.arange(n, device="cuda") - begin[key[:n]] + offsets[key[:n]]
+        slots = torch.full((rows.rows,), -1, device="cuda", dtype=torch.int64)
+        slots[at] = order[:n]
+        position = torch.full((tokens * k,), -1, device="cuda", dtype=torch.int64)
+        position[order[:n]] = at
+        assert torch.equal(rows.slots.long(), slots) and torch.equal(rows.position.flatten().long(), position)
+
+
+def test_gathered_rows_of_a_large_unaligned_matrix():
+    """Rows whose aligned copy would reach 2^31 bytes, where the matrix itself does not."""
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GB of free memory")
+    gen = torch.Generator(device="cuda").manual_seed(10)
+    tokens, K, N, E = 2**20, 2047, 64, 4
+    codes = torch.randint(0, 100, (tokens, K), dtype=torch.uint8, device="cuda", generator=gen).view(E4)
+    A = rt.F8Matrix(codes, torch.rand(f8.blocks(K), tokens, device="cuda", generator=gen).t())
+    W = rt.F8Matrix(torch.randint(0, 100, (E, N, K), dtype=torch.uint8, device="cuda", generator=gen).view(E4),
+                    torch.rand(E, 1, f8.blocks(K), device="cuda", generator=gen), 128)
+    chosen = torch.full((tokens, 1), -1, device="cuda", dtype=torch.int32)
+    taken = torch.cat([torch.arange(300, device="cuda"), torch.arange(tokens - 300, tokens, device="cuda")])
+    chosen[taken, 0] = torch.randint(0, E, (600,), device="cuda", generator=gen).int()
+    rows = rt.expert_rows(chosen, E)
+    C = torch.zeros(rows.rows, N, device="cuda", dtype=torch.bfloat16)
+    rt.gemm_f8_experts(A, W.t(), rows, C, gather=True)
+    for e in range(E):
+        first, n = int(rows.offsets[e]), int(rows.counts[e])
+        at = rows.slots[first:first + n].long()
+        m = rt.F8Matrix(codes[at], A.scales[at])
+        assert_close(C[first:first + n], values(m), values(rt.F8Matrix(W.codes[e], W.scales[e], 128).t()), f"expert {e}")
