@@ -29,6 +29,7 @@ namespace regtile {
 namespace f8 {
 using namespace mfma;
 typedef float __attribute__((may_alias)) f32_any;  // as lds_read16: no wait for DMA
+typedef uint32_t __attribute__((ext_vector_type(2), may_alias)) u32x2_any;
 
 // Transposing LDS read of 8-bit elements (ds_read_b64_tr_b8): in each group of 16 lanes, lane 2 j + h gives the
 // address of 8 bytes at columns 8 h .. 8 h + 7 of row j, and lane i receives column i of rows 0 .. 7 (measured).
@@ -53,7 +54,7 @@ __device__ __forceinline__ void apart(const uint8_t *__restrict__ cur, uint8_t *
 // for each column, else one for 128.
 template <int WM, int WN, int MI, int NI, int STAGES, bool EXACT, int TA, bool NN, bool SB>
 __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, int tiles_m, int tiles_n, int group_m,
-                                                                      int per_split, bool wide) {
+                                                                      int per_split, bool wide, bool lines) {
     constexpr int WAVES = WM * WN, NT = 64 * WAVES, BM = WM * MI * 16, BN = WN * NI * 16;
     constexpr int JA = BM / 8 / WAVES, JB = BN / 8 / WAVES;       // DMA instructions of a wave
     constexpr int SC = (BM + BN) / 64;                            // waves' worth of scales
@@ -292,29 +293,77 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
             const int left = K - (first + t) * BLOCK;
             if (left < BLOCK) clear(cur, left);
         };
-        arrive(0, smem);
-        apart(smem, smem + (STAGES - 1) * STAGE, [&](const uint8_t *c, uint8_t *n) { period(0, c, n, std::true_type{}); });
-        for (int t = 1; t < blocks; ++t) {
-            uint8_t *cur = smem + (t % STAGES) * STAGE, *next = smem + ((t - 1) % STAGES) * STAGE;
-            arrive(t, cur);
-            apart(cur, next, [&](const uint8_t *c, uint8_t *n) { period(t, c, n, std::false_type{}); });
-        }
-        // the last two rows of the last block
+        // A wave whose rows or columns are all past the tile's last only brings its part of each block: its SIMD's matrix
+        // pipe is then the other wave's alone, and a half-filled tile takes little more than half the time.
+        const bool idle = uniform(wm * MI * 16 >= w.used || n0 + wn * NI * 16 >= p.N);
+        if (idle) {
+            for (int t = 0; t < blocks; ++t) {
+                arrive(t, smem + (t % STAGES) * STAGE);
 #pragma unroll
-        for (int n = 0; n < 2 * NI + LAG; ++n) {
-            const int id = (MI - 2) * NI + n;
-            if (n < 2 * NI && n % NI == 0) begin_row(id / NI);
-            if (n < 2 * NI) {
-                if (TWO) next_columns(id);
-                tile(id);
+                for (int n = 0; n < PIECES; ++n) dma(n, t + STAGES - 1, smem + ((t + STAGES - 1) % STAGES) * STAGE);
             }
-            add((id + TILES - LAG) % TILES);
-            if (TWO && n < 2 * NI) next_factors(id, smem);
+        } else {
+            arrive(0, smem);
+            apart(smem, smem + (STAGES - 1) * STAGE, [&](const uint8_t *c, uint8_t *n) { period(0, c, n, std::true_type{}); });
+            for (int t = 1; t < blocks; ++t) {
+                uint8_t *cur = smem + (t % STAGES) * STAGE, *next = smem + ((t - 1) % STAGES) * STAGE;
+                arrive(t, cur);
+                apart(cur, next, [&](const uint8_t *c, uint8_t *n) { period(t, c, n, std::false_type{}); });
+            }
+            // the last two rows of the last block
+#pragma unroll
+            for (int n = 0; n < 2 * NI + LAG; ++n) {
+                const int id = (MI - 2) * NI + n;
+                if (n < 2 * NI && n % NI == 0) begin_row(id / NI);
+                if (n < 2 * NI) {
+                    if (TWO) next_columns(id);
+                    tile(id);
+                }
+                add((id + TILES - LAG) % TILES);
+                if (TWO && n < 2 * NI) next_factors(id, smem);
+            }
         }
         wait_vmcnt<0>();  // no LDS DMA may still be in flight when the workgroup retires
     }
 
     // ---- epilogue ----
+    // `lines`: each wave turns its part of C through LDS and stores 128 bytes of a row at a time
+    if constexpr (!EXACT && NI == 4) {
+        if (lines) {
+            lds_barrier();  // every wave's DMA has landed and every wave has read its last fragments
+            uint8_t *mine = smem + wave * (MI * 16 * 128);
+            const bool bf = w.out.dtype == 1;
+            auto bits = [&](float x) { return bf ? __builtin_bit_cast(uint16_t, (__bf16)x) : __builtin_bit_cast(uint16_t, (_Float16)x); };
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                const int r = i * 16 + (lane & 15);
+#pragma unroll
+                for (int j = 0; j < NI; ++j) {
+                    f32x4 v = acc[i][j] * p.alpha;
+                    if (wm * MI * 16 + r >= w.used) v = f32x4{};
+                    *reinterpret_cast<u32x2_any *>(mine + r * 128 + ((j * 2 + (lane >> 5)) ^ (r & 7)) * 16 + (lane >> 4 & 1) * 8) =
+                        u32x2_any{bits(v[0]) | (uint32_t)bits(v[1]) << 16, bits(v[2]) | (uint32_t)bits(v[3]) << 16};
+                }
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            const int chunk = lane & 7, c = n0 + wn * 64 + chunk * 8;
+#pragma unroll
+            for (int i = 0; i < MI * 2; ++i) {
+                const int at = i * 8 + (lane >> 3), r = wm * MI * 16 + at;
+                const u32x4 v = lds_read16(mine + at * 128 + (chunk ^ (at & 7)) * 16);
+                if (r >= w.rows) continue;
+                uint16_t *to = static_cast<uint16_t *>(w.out.C) + (w.row0 + r) * w.out.ldc + c;
+                if (c + 8 <= p.N) {
+                    *reinterpret_cast<u32x4 *>(to) = v;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (c + e < p.N) to[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+                }
+            }
+            return;
+        }
+    }
     const int row0 = wm * MI * 16 + (lane & 15), col0 = wn * NI * 16 + (lane >> 4) * 4;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
@@ -350,10 +399,11 @@ hipError_t launch_tile(const F8Problem &p, hipStream_t s, int splits) {
         q.alpha = 1.0f;
         q.beta = 0.0f;
     }
+    const bool lines = q.out.dtype != 0 && q.beta == 0.0f && aligned16(q.out.C) && q.out.ldc % 8 == 0 && q.c_stack % 8 == 0;
     auto f = f8_tile_kernel<WM, WN, MI, NI, STAGES, EXACT, TA, NN, SB>;
     note_launch(reinterpret_cast<const void *>(f), NT);
     hipLaunchKernelGGL(f, dim3((unsigned)grid, p.mode == F8Problem::DEPTH ? p.experts : 1), dim3(NT), 0, s, q, (int)tiles_m, (int)tiles_n,
-                       group_m, per, c_wide(q));
+                       group_m, per, c_wide(q), lines);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess && splits > 1 ? launch_f8_join(p, s, splits) : e;
 }
