@@ -98,6 +98,21 @@ __device__ __forceinline__ Group group_of(const int32_t *offsets, const int32_t 
     return g;
 }
 
+// Workgroups take the XCDs in turn: each XCD's get consecutive tiles, of any `count`
+__device__ __forceinline__ int contiguous_id(int block, int count) {
+    const int xcd = block & 7, each = count >> 3, more = count & 7;
+    return xcd * each + min(xcd, more) + (block >> 3);
+}
+
+// How many row tiles of `height` rows the groups have (each begins one)
+__device__ __forceinline__ int row_tiles(const int32_t *offsets, const int32_t *counts, int experts, int rows, int height) {
+    int n = 0;
+    for (int e = __lane_id(); e < experts; e += 64) n += (group_of(offsets, counts, e, rows).room + height - 1) / height;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) n += __shfl_xor(n, d);
+    return __builtin_amdgcn_readfirstlane(n);
+}
+
 // The group that row tile `tile` (of `height` rows; groups begin a tile each) belongs to and the tile's
 // number in it; false past the last. Every lane of the wave gets the same answer: 64 groups are loaded and counted
 // at a time, and the one that is wanted comes out of its lane's registers.

@@ -145,9 +145,10 @@ Plan plan_of(const F8Problem &p) {
     Plan plan = {Plan::ANY, 0, p.out.dtype == 0, 1, false, false, false, false, 0};
     if (p.K == 0 || !tile_takes(p)) return plan;
     const bool dense = p.mode == F8Problem::DENSE, rows = p.mode == F8Problem::ROWS;
-    // Few rows (in a group, on the average): codes straight to registers. us on 128 x 128 tiles (64 x 64 for the last):
-    // 16x4096x4096 13.0, here 6.8; 32 tokens x 6 of 64 experts 114, here 107; 256 x 4 of 32 34.5, here 70.6, which unaligned
-    // rows of B still beat (50 us to copy them)
+    // Few rows: codes straight to registers. us on 128 x 128 tiles: 16x4096x4096 13.0, here 6.8. Of rows in groups that pays up to
+    // 16 in all, and where B's rows would have to be copied first (50 us for 32 x 2048 x 4096, and 70.6 here). 64 x 64 tiles,
+    // here: 1 token x 2 of 8 experts (4096 x 4096) 13.0, 9.3; x 6 of 64 (4096 x 2048) 12.7, 12.2; 4 x 6 of 64 27.7, 32.0;
+    // 8 x 2 of 8 21.1, 30.4; 32 x 6 of 64 96.6, 106.
     const int64_t weights = (int64_t)p.N * p.K, group = rows ? p.mean_rows : p.M;
     if (p.b.step == 1 && (dense || rows)) {
         plan.kernel = Plan::TOKEN;
@@ -158,7 +159,7 @@ Plan plan_of(const F8Problem &p) {
         if (dense && p.M <= 32 && weights <= 1 << (aligned ? 24 : 27)) return plan.shape = 21, plan;
         if (dense && p.M <= 64 && weights <= 1 << 22) return plan.shape = 21, plan;
         if (dense && p.M <= 64 && !aligned && weights <= 1 << 27) return plan.shape = 22, plan;
-        if (rows && group <= (b_aligned(p) ? 12 : 48)) return plan.shape = 12, plan;
+        if (rows && (p.n_slots <= 16 || (!b_aligned(p) && group <= 48))) return plan.shape = 12, plan;
     }
     plan.copy_a = !a_aligned(p);
     plan.copy_b = !b_aligned(p);
@@ -172,7 +173,8 @@ Plan plan_of(const F8Problem &p) {
     };
     // 64 x 64 tiles while there are at most 512 of them, or few rows in a group. us on 128 x 128 (best of two and four stages
     // and parts of k), here: 1024^3 10.5, 5.5 (fp32 C 14.2, 7.1); 1024x1024x4096 21.6, 12.3 (25.6, 19.7); 296x2984x1056 11.2,
-    // 7.5; 2048^3, 1024 tiles, 16.5, 18.8 (25.3, 27.7); 256 tokens x 4 of 32 experts 43.5, 34.5; 512 x 8 of 64 82.7, 99.4.
+    // 7.5; 2048^3, 1024 tiles, 16.5, 18.8 (25.3, 27.7); 32 tokens x 6 of 64 experts 107, 97.7; 256 x 8 of 128 190, 160;
+    // 256 x 6 of 64 114, 117; 1024 x 6 of 64 145, 210.
     // They go in parts of at least 2048 k (fp32 C: 1024), two (one) workgroups to a CU: 64x8192x8192 27.9 whole, 19.8 in 4.
     const int64_t tiles64 = tiles(64);
     if (rows ? group <= 48 : tiles64 <= 512) {
@@ -185,8 +187,9 @@ Plan plan_of(const F8Problem &p) {
         return plan;
     }
     // 256 x 256 tiles run one to a CU: with fewer than 192 too many of the 256 CUs are idle (2048^3, 64 tiles: 31.7
-    // us against 16.5; 4096 x 4096 x 8192, 256 tiles: 115 against 133)
-    if (!plan.exact && p.b.shift != 0 && p.mode != F8Problem::DEPTH && tiles(256) >= 192 && (!rows || group >= 256)) {
+    // us against 16.5; 4096 x 4096 x 8192, 256 tiles: 107 against 128). Groups of fewer than 128 rows leave them too empty (64
+    // experts of 4096 x 2048 with 96 rows on the average: 171 us against 145; 141 rows: 176 against 182)
+    if (!plan.exact && p.b.shift != 0 && p.mode != F8Problem::DEPTH && tiles(256) >= 192 && (!rows || group >= 128)) {
         plan.kernel = Plan::TILE_256;
         return plan;
     }

@@ -66,7 +66,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int wm = wave / WN, wn = wave % WN;
     int tm, tn;
-    const int id = xcd_contiguous_id(blockIdx.x, gridDim.x), tiles = tiles_m * tiles_n;
+    // (of rows in groups only the device knows how many tiles there are; without the count the last XCDs would get all
+    // the workgroups that have none)
+    if (p.mode == F8Problem::ROWS) tiles_m = min(tiles_m, row_tiles(p.offsets, p.counts, p.experts, p.M, BM));
+    const int tiles = tiles_m * tiles_n, count = p.mode == F8Problem::ROWS ? tiles : gridDim.x;
+    if ((int)blockIdx.x >= count) return;
+    const int id = contiguous_id(blockIdx.x, count);
     const int split = id / tiles;  // part of k, per_split blocks
     {  // group_m tile rows at a time, column by column
         const int at = id - split * tiles, group = at / (group_m * tiles_n), row = group * group_m;
@@ -84,7 +89,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
     const int n0 = uniform(tn * BN);
     const int K = uniform(w.used > 0 ? w.K : 0), all = (K + BLOCK - 1) / BLOCK;
     const int first = uniform(split * per_split), blocks = min(per_split, all - first);
-    if ((int)gridDim.x > tiles) w.out.C = static_cast<float *>(w.out.C) + (int64_t)split * p.M * p.N;
+    if (count > tiles) w.out.C = static_cast<float *>(w.out.C) + (int64_t)split * p.M * p.N;
 
     f32x4 acc[MI][NI] = {};
     if (blocks > 0) {
@@ -117,6 +122,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
         const rsrc_t s_rsrc = make_rsrc(sa_wave ? w.a.s : w.b.s, 0x7FFFFFFFu);
 
         constexpr int PIECES = JA + JB + 1;
+        constexpr int SPREAD = 2;
         // instruction n of a block's DMA; past the last block the last again, into the stage that is free then
         auto dma = [&](int n, int block, uint8_t *to) {
             const int kb = first + min(block, blocks - 1);
@@ -260,7 +266,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
                 if (SB && TWO && i == -1 && j == NI - 1) read_sb(cur);
 #pragma unroll
                 for (int m = 0; m < PIECES; ++m)
-                    if (m * (TILES - START) / PIECES + START == n) dma(m, t + STAGES - 1, next);
+                    if (m * (TILES - START) / (SPREAD * PIECES) + START == n) dma(m, t + STAGES - 1, next);
                 __builtin_amdgcn_sched_barrier(0);
             }
         };

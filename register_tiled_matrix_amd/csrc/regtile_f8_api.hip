@@ -107,7 +107,8 @@ void in_rows(const regtile_expert_rows *rows, int gather, const regtile_f8_matri
     p->slots = gather ? rows->slots : nullptr;
     p->top_k = rows->k;
     p->a_rows = A->rows;
-    p->mean_rows = (int)(((int64_t)rows->tokens * rows->k + rows->experts - 1) / rows->experts);
+    p->n_slots = rows->tokens * rows->k;
+    p->mean_rows = (int)(((int64_t)p->n_slots + rows->experts - 1) / rows->experts);
 }
 void in_depth(const regtile_expert_rows *rows, F8Problem *p) {
     p->mode = F8Problem::DEPTH;

@@ -84,7 +84,7 @@ struct F8Problem {
     const int32_t *offsets, *counts;
     const int32_t *slots;  // row r of A is token slots[r] / top_k (of a_rows), or null: row r
     int top_k, a_rows;
-    int mean_rows;  // ROWS: a group's, on the average
+    int n_slots, mean_rows;  // ROWS: how many rows have a slot at most, and a group's on the average
     void *work;
     int64_t work_bytes;
 };
