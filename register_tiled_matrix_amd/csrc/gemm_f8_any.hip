@@ -6,6 +6,9 @@
 // accumulator times the two scales: c += (sa sb) sum. B's fragment is the first operand, so that a lane holds
 // 4 consecutive columns of one row of C, and one scale of A.
 //
+// Bound by the latency of a block's loads, which nothing overlaps: 8192^3 takes 3.3 ms, where tiles take 0.43. What comes here
+// is an e5m2 B, a transposed A, rows too far apart for 32-bit offsets, unaligned rows without a workspace, and K = 0.
+//
 // A K-contiguous chunk of 16 codes is one load at any address; a chunk across K's end, and operands contiguous
 // the other way (16 rows at one k, scattered into LDS), take bytes.
 #include "f8_common.h"

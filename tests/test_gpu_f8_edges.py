@@ -254,3 +254,40 @@ def test_gathered_rows_of_a_large_unaligned_matrix():
         at = rows.slots[first:first + n].long()
         m = rt.F8Matrix(codes[at], A.scales[at])
         assert_close(C[first:first + n], values(m), values(rt.F8Matrix(W.codes[e], W.scales[e], 128).t()), f"expert {e}")
+
+
+@pytest.mark.parametrize("M,N,K,name", [(3501, 3603, 400, "f8_tile_256x256"), (2601, 2307, 400, "f8_tile_128x128"), (1800, 1701, 1100, "f8_tile_128x128_deep")])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_ragged_columns_of_an_aligned_C(M, N, K, name, dtype):
+    """C's rows are aligned for whole stores and N is not: what lies beside C stays."""
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    wide_b = name == "f8_tile_128x128"  # (a scale for each column keeps it off the larger tiles)
+    A, B = make(gen, M, K), make(gen, N, K, 1 if wide_b else 128).t()
+    whole = torch.full((M + 2, (N + 15) // 8 * 8), 7.0, device="cuda", dtype=dtype)
+    C = whole[1:-1, :N]
+    rt.gemm_f8(A, B, C, alpha=0.5)
+    assert rt.last_kernel() == name
+    assert_close(C, values(A) * 0.5, values(B), name)
+    assert bool((whole[0] == 7).all()) and bool((whole[-1] == 7).all()) and bool((whole[:, N:] == 7).all())
+
+
+@pytest.mark.parametrize("tokens,k,E,align", [(1500, 2, 8, 1), (3000, 2, 16, 64), (1000, 2, 16, 128)])
+def test_ragged_groups_of_an_aligned_C(tokens, k, E, align):
+    """Tiles that groups fill in part: rows between groups become 0, rows behind the last and columns beside C stay."""
+    gen = torch.Generator(device="cuda").manual_seed(tokens)
+    N, K = 2051, 300
+    x = make(gen, tokens, K)
+    W = [make(gen, N, K, 128) for _ in range(E)]
+    stack = rt.F8Matrix(torch.stack([w.codes.view(torch.uint8) for w in W]).view(E4), torch.stack([w.scales for w in W]), 128)
+    chosen = (torch.randn(tokens, E, device="cuda", generator=gen) + torch.arange(E, device="cuda") * 0.2).topk(k).indices.int()
+    chosen[:7] = -1
+    rows = rt.expert_rows(chosen, E, align=align)
+    whole = torch.full((rows.rows, 2064), 7.0, device="cuda", dtype=torch.bfloat16)
+    C = whole[:, :N]
+    rt.gemm_f8_experts(x, stack.t(), rows, C, gather=True)
+    offsets, counts, X = rows.offsets.tolist(), rows.counts.tolist(), values(x)
+    for e in range(E):
+        first, n = offsets[e], counts[e]
+        assert_close(C[first:first + n], X[rows.slots[first:first + n].long() // k], values(W[e].t()), f"expert {e}")
+        assert bool((C[first + n:offsets[e + 1]] == 0).all())
+    assert bool((whole[offsets[E]:] == 7).all()) and bool((whole[:, N:] == 7).all())
