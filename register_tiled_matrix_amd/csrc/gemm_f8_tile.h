@@ -21,7 +21,7 @@
 // LDS reads of fragments and the last store of each round of tiles. With an fp32 C 900-955 us: expanding codes
 // takes as many issue slots as the bf16 MFMAs. Few columns of k a tile (2048) add what a tile costs at its ends, 7 us.
 //
-// Edges: rows past the last are loaded from the last, chunks past N from the last one that holds an element. What
+// Edges: rows past the last are not loaded and are zeros, chunks past N come from the last one that holds an element. What
 // lies past K in the last block (bytes between rows, or zeros from behind the descriptor) is overwritten with
 // zeros in LDS, in both operands: a code there may be a NaN.
 #pragma once
@@ -107,16 +107,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
                                         addr::f8_span(gather ? p.a_rows : w.used, w.a.row, K));
         const rsrc_t b_rsrc = NN ? make_rsrc(w.b.q + n0, addr::f8_span(K, w.b.step, p.N - n0))
                                  : make_rsrc(w.b.q + (int64_t)n0 * w.b.row, addr::f8_span(n_rows, w.b.row, K));
+        constexpr uint32_t NOWHERE = 0x80000000u;  // behind every descriptor: nothing is read, zeros arrive
         uint32_t av[JA], bv[JB];
 #pragma unroll
         for (int j = 0; j < JA; ++j) {
-            const int q = wave * JA + j, at = min(addr::f8_row(q, lane), w.used - 1);
-            av[j] = addr::f8_lane(q, lane, gather ? a_row(p, w, at) : at, w.a.row);
+            const int q = wave * JA + j, row = addr::f8_row(q, lane), at = min(row, w.used - 1);
+            av[j] = row < w.used ? addr::f8_lane(q, lane, gather ? a_row(p, w, at) : at, w.a.row) : NOWHERE;
         }
 #pragma unroll
         for (int j = 0; j < JB; ++j) {
             const int q = wave * JB + j;
-            bv[j] = NN ? addr::f8_nn_lane<BN>(q, lane, n_rows, w.b.step) : addr::f8_lane(q, lane, min(addr::f8_row(q, lane), n_rows - 1), w.b.row);
+            if constexpr (NN)
+                bv[j] = addr::f8_nn_lane<BN>(q, lane, n_rows, w.b.step);
+            else
+                bv[j] = addr::f8_row(q, lane) < n_rows ? addr::f8_lane(q, lane, addr::f8_row(q, lane), w.b.row) : NOWHERE;
         }
         // scales: a wave brings 64 rows' of A or 64 columns' of B
         static_assert(BM % 64 == 0, "a wave's scales are all of one operand");
@@ -341,8 +345,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
     }
 
     // ---- epilogue ----
-    // `lines`: each wave turns its part of C through LDS and stores 128 bytes of a row at a time (from the accumulators 32 bytes
-    // of a row leave in one instruction, and 8192^3 took 450 us instead of 429)
+    // `lines`: each wave turns its part of C through LDS and stores 128 bytes of a row at a time, at any alignment (from the
+    // accumulators 32 bytes of an aligned row leave in one instruction, 2 of another, and 8192^3 took 450 us instead of 429,
+    // 8191 x 8190 x 8192 490 instead of 426)
     if constexpr (!EXACT && NI == 4) {
         if (lines) {
             lds_barrier();  // every wave's DMA has landed and every wave has read its last fragments
@@ -369,7 +374,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
                 if (r >= w.rows) continue;
                 uint16_t *to = static_cast<uint16_t *>(w.out.C) + (w.row0 + r) * w.out.ldc + c;
                 if (c + 8 <= p.N) {
-                    *reinterpret_cast<u32x4 *>(to) = v;
+                    __builtin_memcpy(to, &v, 16);  // (at any address)
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
@@ -414,7 +419,7 @@ hipError_t launch_tile(const F8Problem &p, hipStream_t s, int splits) {
         q.alpha = 1.0f;
         q.beta = 0.0f;
     }
-    const bool lines = q.out.dtype != 0 && q.beta == 0.0f && aligned16(q.out.C) && q.out.ldc % 8 == 0 && q.c_stack % 8 == 0;
+    const bool lines = q.out.dtype != 0 && q.beta == 0.0f;
     auto f = f8_tile_kernel<WM, WN, MI, NI, STAGES, EXACT, TA, NN, SB>;
     note_launch(reinterpret_cast<const void *>(f), NT);
     hipLaunchKernelGGL(f, dim3((unsigned)grid, p.mode == F8Problem::DEPTH ? p.experts : 1), dim3(NT), 0, s, q, (int)tiles_m, (int)tiles_n,
