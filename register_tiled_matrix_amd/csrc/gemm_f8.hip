@@ -56,13 +56,14 @@ struct Copy {
     uint8_t *to;
     int64_t ld, stack, to_ld;
     int64_t rows, cols, count;
+    int across;  // threads to a row
 };
 constexpr int COPY_NT = 256;
-__global__ __launch_bounds__(COPY_NT) void f8_align_kernel(Copy c0, Copy c1, int z1, int across) {
+__global__ __launch_bounds__(COPY_NT) void f8_align_kernel(Copy c0, Copy c1, int z1) {
     const bool second = (int)blockIdx.z >= z1;
     const Copy c = second ? c1 : c0;
     const int z = second ? blockIdx.z - z1 : blockIdx.z, nz = second ? gridDim.z - z1 : z1;
-    const int tx = threadIdx.x % across, ty = threadIdx.x / across;
+    const int across = c.across, tx = threadIdx.x % across, ty = threadIdx.x / across;
     for (int64_t e = z; e < c.count; e += nz)
         for (int64_t r = (int64_t)blockIdx.x * (COPY_NT / across) + ty; r < c.rows; r += (int64_t)gridDim.x * (COPY_NT / across)) {
             const uint8_t *from = c.from + e * c.stack + r * c.ld;
@@ -72,14 +73,19 @@ __global__ __launch_bounds__(COPY_NT) void f8_align_kernel(Copy c0, Copy c1, int
         }
 }
 // Copies of one or two operands (count 0: none), in one launch
-hipError_t align_rows(const Copy &a, const Copy &b, hipStream_t s) {
-    const int64_t cols = a.cols > b.cols ? a.cols : b.cols, rows = a.rows > b.rows ? a.rows : b.rows, units = (cols + 15) / 16;
-    int across = COPY_NT;
-    while (across > 8 && across / 2 >= units) across /= 2;
-    const int64_t gx = (rows * across + COPY_NT - 1) / COPY_NT, gy = (units + across - 1) / across;
+hipError_t align_rows(Copy a, Copy b, hipStream_t s) {
+    int64_t gx = 1, gy = 1;
+    for (Copy *c : {&a, &b}) {
+        const int64_t units = (c->cols + 15) / 16;
+        c->across = COPY_NT;
+        while (c->across > 8 && c->across / 2 >= units) c->across /= 2;
+        const int64_t x = (c->rows * c->across + COPY_NT - 1) / COPY_NT, y = (units + c->across - 1) / c->across;
+        if (c->count > 0 && x > gx) gx = x;
+        if (c->count > 0 && y > gy) gy = y;
+    }
     const int za = (int)(a.count < 1024 ? a.count : 1024), zb = (int)(b.count < 1024 ? b.count : 1024);
     hipLaunchKernelGGL(f8_align_kernel, dim3((unsigned)(gx < (1 << 16) ? gx : 1 << 16), (unsigned)(gy < 64 ? gy : 64), (unsigned)(za + zb)),
-                       dim3(COPY_NT), 0, s, a, b, za, across);
+                       dim3(COPY_NT), 0, s, a, b, za);
     return hipGetLastError();
 }
 
@@ -225,7 +231,7 @@ hipError_t launch_f8(const F8Problem &given, hipStream_t s, const char **name) {
     Copy copies[2] = {};
     if (plan.copy_a) {
         const Stored m = stored_a(p);
-        copies[0] = {p.a.q, work, p.a.row, 0, m.ld(), m.rows, m.cols, 1};
+        copies[0] = {p.a.q, work, p.a.row, 0, m.ld(), m.rows, m.cols, 1, 0};
         p.a.q = work;
         p.a.row = m.ld();
         work += m.bytes();
@@ -233,7 +239,7 @@ hipError_t launch_f8(const F8Problem &given, hipStream_t s, const char **name) {
     if (plan.copy_b) {
         const Stored m = stored_b(p);
         int64_t &ld = p.b.step != 1 ? p.b.step : p.b.row;
-        copies[1] = {p.b.q, work, ld, p.b_stack, m.ld(), m.rows, m.cols, m.count};
+        copies[1] = {p.b.q, work, ld, p.b_stack, m.ld(), m.rows, m.cols, m.count, 0};
         p.b.q = work;
         p.b_stack = m.rows * m.ld();
         ld = m.ld();
