@@ -181,14 +181,16 @@ Plan plan_of(const F8Problem &p) {
     // and parts of k), here: 1024^3 10.5, 5.5 (fp32 C 14.2, 7.1); 1024x1024x4096 21.6, 12.3 (25.6, 19.7); 296x2984x1056 11.2,
     // 7.5; 2048^3, 1024 tiles, 16.5, 18.8 (25.3, 27.7); 32 tokens x 6 of 64 experts 107, 97.7; 256 x 8 of 128 190, 160;
     // 256 x 6 of 64 114, 117; 1024 x 6 of 64 145, 210.
-    // They go in parts of at least 2048 k (fp32 C: 1024), two (one) workgroups to a CU: 64x8192x8192 27.9 whole, 19.8 in 4.
+    // They go in parts of at least 1024 k, one workgroup to a CU (K x N B, whole, 2 and 4 parts: 1216x176x4720 16.3, 13.2, 11.5,
+    // 256x1024x4096 13.6, 11.8, 10.7; two to a CU cost more in the join: 1024x1024x4096 12.3 whole, 16.7 in 2). Two parts
+    // of the 8-bit instructions take at least 2048 (64x2048x2048 7.5 whole, 8.7 in 2; 64x8192x8192 27.0, 20.5).
     const int64_t tiles64 = tiles(64);
     if (rows ? group <= 48 : tiles64 <= 512) {
         plan.kernel = Plan::TILE_64;
         if (dense) {
-            const int64_t fill = (plan.exact ? 256 : 512) / tiles64, most = blocks / (plan.exact ? 8 : 16);
+            const int64_t fill = 256 / tiles64, most = blocks / 8;
             plan.parts = (int)(fill < most ? fill : most);
-            if (plan.parts < 1) plan.parts = 1;
+            if (plan.parts < 1 || (plan.parts == 2 && !plan.exact && blocks < 32)) plan.parts = 1;
         }
         return plan;
     }
