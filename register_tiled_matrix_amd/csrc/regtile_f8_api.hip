@@ -42,7 +42,8 @@ regtile::F8Operand operand(const regtile_f8_matrix *m, bool rows_are_k) {
 
 bool bad_rows(const regtile_expert_rows *r) {
     if (r == nullptr || r->tokens < 0 || r->k < 1 || r->experts < 1 || r->align < 1) return true;
-    if (r->rows != regtile_expert_rows_size(r->tokens, r->k, r->experts, r->align)) return true;
+    // (the size of what passes 2^31 - 1 is -1: a caller may have stored it)
+    if (r->rows < 0 || r->rows != regtile_expert_rows_size(r->tokens, r->k, r->experts, r->align)) return true;
     if (r->offsets == nullptr || r->counts == nullptr) return true;
     return r->rows > 0 && (r->slots == nullptr || r->position == nullptr);
 }
