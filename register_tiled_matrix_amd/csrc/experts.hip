@@ -251,10 +251,23 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteProblem p) {
     }
 }
 
+// x of lane j
+__device__ __forceinline__ double lane_of(double x, int j) {
+    const u64 b = __builtin_bit_cast(u64, x);
+    return __builtin_bit_cast(double, (u64)(uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), j) << 32 |
+                                          (uint32_t)__builtin_amdgcn_readlane((int)b, j));
+}
+
 // The gradient with respect to the logits. With w the weights before `scale` and dot = sum_j dw_j w_j, expert
 // c's is scale times:  softmax, renormalised: w_c (dw_c - dot), and 0 for experts that were not chosen;
 // softmax: p_e (dw_e - dot), dw_e = 0 for those;  sigmoid, renormalised: w_c (1 - s_c) (dw_c - dot);
 // sigmoid: s_c (1 - s_c) dw_c.
+// Where one expert is nearly certain, dw_c - dot is the difference of two numbers that are nearly equal. The weights (the
+// probabilities of all experts) sum to 1, so every dw may be counted from one of them: from the likeliest expert's (0 if it
+// was not chosen), whose own terms, the large ones, are then 0. What was not chosen has dw = 0 too, and counts with the sum of
+// its probabilities, which are fp32 exponentials added in 64 bits; all else is 64 bits. The slots of an expert that was chosen
+// more than once are added before they are rounded, in a loop that other tokens do not run. 8192 tokens of 64 experts, k = 8:
+// 6.2 us renormalised and 9.1 not (with fp32 sums 6.6, and a gradient off by a fifth of itself 16 ahead).
 template <int R>
 __global__ __launch_bounds__(NT) void route_grad_kernel(RouteProblem p) {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -280,32 +293,59 @@ __global__ __launch_bounds__(NT) void route_grad_kernel(RouteProblem p) {
     const double dw = expert >= 0 ? (double)p.dweights[token * p.k + lane] : 0.0;
     const float logit = expert >= 0 ? load_value(p.logits, p.dtype, token * p.ldl + expert) : -INFINITY;
     const double s = expert >= 0 && !poison ? score_of(p.sigmoid, logit, top) : 0.0;
-    double total = 1.0;
+    const uint32_t key = expert >= 0 ? (uint32_t)(key_of(logit) >> 32) : 0u, best = wave_max(key);  // of the chosen
+    const u64 likely = __ballot(key == best && best != 0);
+    auto likeliest = [&](double v) { return likely != 0 ? lane_of(v, __ffsll((unsigned long long)likely) - 1) : 0.0; };
+    double mine;
     if (p.renormalize) {
-        total = wave_sum(s);
-    } else if (!p.sigmoid) {
-        float sum = 0.0f;
+        const double total = wave_sum(s), w = total > 0.0 ? s / total : 0.0, from = likeliest(dw), diff = expert >= 0 ? dw - from : 0.0;
+        mine = w * (diff - wave_sum(w * diff));
+    } else if (p.sigmoid) {
+        mine = s * dw;
+    } else {
+        // every expert's exponential; an expert's first slot stands for all of its slots
+        double all = 0.0, left = 0.0, of_expert = 0.0;
+        uint32_t chosen = 0;  // a bit for each of this lane's experts
+        bool first = true;
+        for (int j = 0; j < p.k; ++j) {
+            const int c = __builtin_amdgcn_readlane(expert, j);
+            const double v = lane_of(dw, j);
+            if (c >= 0 && (c & 63) == lane) chosen |= 1u << (c >> 6);
+            if (c == expert) of_expert += v;
+            first &= c != expert || j >= lane;
+        }
 #pragma unroll
-        for (int i = 0; i < R; ++i) sum += expf(x[i] - top);
-        total = wave_sum((double)sum);
+        for (int i = 0; i < R; ++i) {
+            d[i] = expf(x[i] - top);
+            all += (double)d[i];
+            if (!(chosen >> i & 1)) left += (double)d[i];
+        }
+        const double own = first ? s : 0.0, from = best == top_key ? likeliest(of_expert) : 0.0, diff = of_expert - from;
+        const double total = wave_sum(all), rest = wave_sum(left), shift = wave_sum(own * diff), sum = wave_sum(own * of_expert);
+        const double unit = total > 0.0 ? 1.0 / total : 0.0, dot = sum * unit * unit * (double)p.scale;
+        mine = own * unit * (diff - (shift - rest * from) * unit);
+#pragma unroll
+        for (int i = 0; i < R; ++i) d[i] = (float)(-dot * (double)d[i]);
     }
-    const double w = total > 0.0 ? s / total : 0.0, dot = wave_sum(dw * w);
-    double mine = w * (dw - (p.renormalize || !p.sigmoid ? dot : 0.0)) * (double)p.scale;
     if (p.sigmoid) mine *= 1.0 - s;
-    if (!p.sigmoid && !p.renormalize) {
-        mine = w * dw * (double)p.scale;  // the other part goes to every expert
-        const float all = total > 0.0 ? (float)(dot / total * (double)p.scale) : 0.0f;
+    mine *= (double)p.scale;
+    auto place = [&](double of_slot) {  // slots' values at their experts; whether an expert has several
+        const float v = (float)of_slot;
+        u64 twice = 0;
+        for (int j = 0; j < p.k; ++j) {
+            const int c = __builtin_amdgcn_readlane(expert, j);
+            const u64 same_expert = __ballot(expert == c);
+            if (c >= 0) twice |= same_expert & (same_expert - 1);
+            const float of_j = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), j));
 #pragma unroll
-        for (int i = 0; i < R; ++i) d[i] = -all * expf(x[i] - top);
-    }
-    const float value = (float)mine;
-    for (int j = 0; j < p.k; ++j) {
-        const int e = __builtin_amdgcn_readlane(expert, j);
-        if (e < 0) continue;
-        const float v = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, value), j));
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-            if (e == i * 64 + lane) d[i] += v;
+            for (int i = 0; i < R; ++i) d[i] = c == i * 64 + lane ? of_j : d[i];
+        }
+        return twice != 0;
+    };
+    if (place(mine)) {
+        double sum = 0.0;
+        for (int j = 0; j < p.k; ++j) sum += __builtin_amdgcn_readlane(expert, j) == expert ? lane_of(mine, j) : 0.0;
+        place(sum);
     }
 #pragma unroll
     for (int i = 0; i < R; ++i) {
