@@ -292,7 +292,10 @@ __global__ __launch_bounds__(NT) void route_grad_kernel(RouteProblem p) {
     if (expert >= p.experts || expert < 0) expert = -1;
     const double dw = expert >= 0 ? (double)p.dweights[token * p.k + lane] : 0.0;
     const float logit = expert >= 0 ? load_value(p.logits, p.dtype, token * p.ldl + expert) : -INFINITY;
-    const double s = expert >= 0 && !poison ? score_of(p.sigmoid, logit, top) : 0.0;
+    // the score, and a sigmoid's 1 - s (which is lost in an s near 1), from one exponential
+    const bool some = expert >= 0 && !poison;
+    const double power = exp(p.sigmoid ? -fabs((double)logit) : (double)logit - (double)top), far = p.sigmoid ? 1.0 / (1.0 + power) : 1.0;
+    const double near = power * far, s = !some ? 0.0 : p.sigmoid && logit >= 0.0f ? far : near;
     const uint32_t key = expert >= 0 ? (uint32_t)(key_of(logit) >> 32) : 0u, best = wave_max(key);  // of the chosen
     const u64 likely = __ballot(key == best && best != 0);
     auto likeliest = [&](double v) { return likely != 0 ? lane_of(v, __ffsll((unsigned long long)likely) - 1) : 0.0; };
@@ -327,7 +330,7 @@ __global__ __launch_bounds__(NT) void route_grad_kernel(RouteProblem p) {
 #pragma unroll
         for (int i = 0; i < R; ++i) d[i] = (float)(-dot * (double)d[i]);
     }
-    if (p.sigmoid) mine *= 1.0 - s;
+    if (p.sigmoid) mine *= logit >= 0.0f ? near : far;
     mine *= (double)p.scale;
     auto place = [&](double of_slot) {  // slots' values at their experts; whether an expert has several
         const float v = (float)of_slot;

@@ -68,7 +68,7 @@ def check(x, chosen, dw, dtype, sigmoid, renormalize, scale):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("sigmoid", [False])
+@pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("renormalize", [False, True])
 @pytest.mark.parametrize("experts,k", [(7, 1), (64, 1), (64, 6), (65, 1), (256, 1), (256, 8), (1000, 1), (1024, 64)])
 def test_one_expert_ahead(experts, k, renormalize, sigmoid, dtype):
@@ -84,7 +84,7 @@ def test_one_expert_ahead(experts, k, renormalize, sigmoid, dtype):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("renormalize", [False, True])
-@pytest.mark.parametrize("sigmoid", [False])
+@pytest.mark.parametrize("sigmoid", [False, True])
 def test_repeated_and_missing_choices(sigmoid, renormalize):
     rng = np.random.default_rng(5)
     x = rng.standard_normal((30, 70)).astype(np.float32) * 3
