@@ -144,11 +144,11 @@ struct Plan {
     int parts;     // of k, through the workspace
     bool copy_a, copy_b;  // operands that it needs copies of,
     bool turn_a, turn_b;  // and whose scales it wants turned
-    int64_t copy_bytes;
+    int64_t copy_bytes, turn_bytes;
 };
 
 Plan plan_of(const F8Problem &p) {
-    Plan plan = {Plan::ANY, 0, p.out.dtype == 0, 1, false, false, false, false, 0};
+    Plan plan = {Plan::ANY, 0, p.out.dtype == 0, 1, false, false, false, false, 0, 0};
     if (p.K == 0 || !tile_takes(p)) return plan;
     const bool dense = p.mode == F8Problem::DENSE, rows = p.mode == F8Problem::ROWS;
     // Few rows: codes straight to registers. us on 128 x 128 tiles: 16x4096x4096 13.0, here 6.8. Of rows in groups that pays up to
@@ -172,8 +172,8 @@ Plan plan_of(const F8Problem &p) {
     plan.turn_a = scales_apart(p, p.a, stored_a(p).rows);
     plan.turn_b = !rows && scales_apart(p, p.b, p.N);
     const int64_t blocks = ((int64_t)p.K + BLOCK - 1) / BLOCK;
-    plan.copy_bytes = (plan.copy_a ? stored_a(p).bytes() : 0) + (plan.copy_b ? stored_b(p).bytes() : 0) +
-                      (plan.turn_a ? turned_bytes(stored_a(p).rows, blocks) : 0) + (plan.turn_b ? turned_bytes(p.N, blocks) : 0);
+    plan.copy_bytes = (plan.copy_a ? stored_a(p).bytes() : 0) + (plan.copy_b ? stored_b(p).bytes() : 0);
+    plan.turn_bytes = (plan.turn_a ? turned_bytes(stored_a(p).rows, blocks) : 0) + (plan.turn_b ? turned_bytes(p.N, blocks) : 0);
     auto tiles = [&](int64_t side) {
         return most_row_tiles(p, (int)side) * (((int64_t)p.N + side - 1) / side) * (p.mode == F8Problem::DEPTH ? p.experts : 1);
     };
@@ -218,16 +218,17 @@ Plan plan_of(const F8Problem &p) {
 
 int64_t f8_work_bytes(const F8Problem &p) {
     const Plan plan = plan_of(p);
-    return plan.copy_bytes + (plan.parts > 1 ? (int64_t)plan.parts * p.M * p.N * 4 : 0);
+    return plan.copy_bytes + plan.turn_bytes + (plan.parts > 1 ? (int64_t)plan.parts * p.M * p.N * 4 : 0);
 }
 
 hipError_t launch_f8(const F8Problem &given, hipStream_t s, const char **name) {
     Plan plan = plan_of(given);
     F8Problem p = given;
-    if (plan.copy_bytes > p.work_bytes) {  // no room for them: scales can stay as they are, rows cannot
-        if (plan.copy_a || plan.copy_b) return launch_f8_any(p, s, name);
+    // what there is no room for: scales can stay as they are, rows cannot
+    if (plan.copy_bytes > p.work_bytes) return launch_f8_any(p, s, name);
+    if (plan.copy_bytes + plan.turn_bytes > p.work_bytes) {
         plan.turn_a = plan.turn_b = false;
-        plan.copy_bytes = 0;
+        plan.turn_bytes = 0;
     }
     uint8_t *work = static_cast<uint8_t *>(p.work);
     Copy copies[2] = {};
@@ -278,7 +279,7 @@ hipError_t launch_f8(const F8Problem &given, hipStream_t s, const char **name) {
         if (e != hipSuccess) return e;
     }
     p.work = work;
-    p.work_bytes -= plan.copy_bytes;
+    p.work_bytes -= plan.copy_bytes + plan.turn_bytes;
     while (plan.parts > 1 && (int64_t)plan.parts * p.M * p.N * 4 > p.work_bytes) --plan.parts;
     static const char *const small[2] = {"f8_tile_128x128", "f8_tile_128x128_exact"};
     static const char *const tiny[2] = {"f8_tile_64x64", "f8_tile_64x64_exact"};
