@@ -201,13 +201,14 @@ Plan plan_of(const F8Problem &p) {
         plan.kernel = Plan::TILE_256;
         return plan;
     }
-    // 128 x 128 tiles: fewer than the chip holds go in parts of at least 1024 k. One workgroup of the 8-bit instructions to
-    // a CU with four stages (2048^3, 256 tiles: 16.5, with two stages 17.5), two of the bf16 ones with two (2048 x 1504 x
-    // 8096: 80 us whole, 70 in 2 parts; with four stages 78).
+    // 128 x 128 tiles (129 or more of them: else there are at most 512 of 64 x 64). The bf16 instructions' go in parts of at
+    // least 1024 k while they are fewer than the chip holds, two to a CU with two stages (2048 x 1504 x 8096: 80 us whole, 70 in
+    // 2 parts; with four stages 78). The 8-bit instructions' run one to a CU with four stages while there is one for each (2048^3,
+    // 256 tiles: 16.5, with two stages 17.5).
     plan.kernel = Plan::TILE_128;
     if (dense) {
-        const int64_t tiles128 = tiles(128), fill = (plan.exact ? 512 : 256) / tiles128;
-        plan.parts = (int)(fill < blocks / 8 ? fill : blocks / 8);
+        const int64_t tiles128 = tiles(128), fill = 512 / tiles128;
+        if (plan.exact) plan.parts = (int)(fill < blocks / 8 ? fill : blocks / 8);
         if (plan.parts < 1) plan.parts = 1;
         if (!plan.exact && tiles128 <= 256) plan.kernel = Plan::TILE_DEEP;
     }
@@ -287,7 +288,7 @@ hipError_t launch_f8(const F8Problem &given, hipStream_t s, const char **name) {
         case Plan::TILE_256: *name = "f8_tile_256x256"; return launch_f8_tile_256(p, s);
         case Plan::TILE_128: *name = small[plan.exact]; return launch_f8_tile_128(p, plan.exact, s, plan.parts);
         case Plan::TILE_64: *name = tiny[plan.exact]; return launch_f8_tile_64(p, plan.exact, s, plan.parts);
-        case Plan::TILE_DEEP: *name = "f8_tile_128x128_deep"; return launch_f8_tile_deep(p, s, plan.parts);
+        case Plan::TILE_DEEP: *name = "f8_tile_128x128_deep"; return launch_f8_tile_deep(p, s);
         case Plan::TOKEN: *name = "f8_token"; return launch_f8_token(p, plan.shape, s);
         default: return launch_f8_any(p, s, name);
     }

@@ -3,7 +3,7 @@
 #include "gemm_f8_tile.h"
 
 namespace regtile {
-hipError_t launch_f8_tile_deep(const F8Problem &p, hipStream_t s, int splits) {
-    return f8::launch_tile_of<2, 2, 4, 4, 4, false>(p, s, splits);
+hipError_t launch_f8_tile_deep(const F8Problem &p, hipStream_t s) {
+    return f8::launch_tile_of<2, 2, 4, 4, 4, false>(p, s, 1);
 }
 }  // namespace regtile

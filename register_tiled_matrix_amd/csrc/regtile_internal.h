@@ -186,11 +186,12 @@ hipError_t launch_f8_dequantize(const F8Convert &p, hipStream_t s, const char **
 // Products: the kernel that suits them, and the workspace that it would make use of
 hipError_t launch_f8(const F8Problem &p, hipStream_t s, const char **name);
 int64_t f8_work_bytes(const F8Problem &p);
-// tiles fed by DMA, what f8_tile_takes; `exact` as in gemm_f8_tile.h; 128-wide ones in parts of k through the workspace
+// tiles fed by DMA, for what tile_takes (gemm_f8.hip); `exact` as in gemm_f8_tile.h; 64-wide ones, and exact 128-wide ones, in
+// `splits` parts of k through the workspace
 hipError_t launch_f8_tile_256(const F8Problem &p, hipStream_t s);
 hipError_t launch_f8_tile_128(const F8Problem &p, bool exact, hipStream_t s, int splits);
 hipError_t launch_f8_tile_64(const F8Problem &p, bool exact, hipStream_t s, int splits);
-hipError_t launch_f8_tile_deep(const F8Problem &p, hipStream_t s, int splits);
+hipError_t launch_f8_tile_deep(const F8Problem &p, hipStream_t s);
 hipError_t launch_f8_join(const F8Problem &p, hipStream_t s, int splits);
 // few rows of A (in each group), B stored N x K
 hipError_t launch_f8_token(const F8Problem &p, int shape, hipStream_t s);

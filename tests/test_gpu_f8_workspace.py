@@ -65,3 +65,25 @@ def test_the_size_is_the_sum_of_its_parts():
     assert need(m(n, n, 4112), m(n, n, 4112)) == 2 * turned
     assert need(m(n, n, n, by_rows=False), m(n, n, n, 128)) == 2 * copy
     assert need(m(n, n, n), m(n, n, n)) == 2 * copy + 2 * turned
+
+
+def test_parts_of_k_are_the_exact_products_and_those_of_few_tiles():
+    """Aligned products ask for a workspace for parts of k only: those of up to 512 tiles of 64 x 64, and past that those with
+    an fp32 C of up to 256 tiles of 128 x 128 (half of what the chip holds). M from 65 on: few rows take none."""
+    lib = rt.load()
+
+    def need(M, N, K, dtype):
+        a, b = (MatrixStruct(codes=0x1000, ld=K, scales=0x1000, scale_row=1, scale_col=n, codes_stack=0, scales_stack=0, rows=n, cols=K, stack=1,
+                             type=0, block_rows=1) for n in (M, N))
+        return lib.regtile_gemm_f8_workspace(0, 1, ctypes.byref(a), ctypes.byref(b), dtype, N)
+
+    for M in (65, 100, 128, 300, 1000, 1408, 1500, 2048, 2100, 5000):
+        for N in (64, 129, 700, 1024, 1500, 2000, 2048, 4096):
+            tiles64, tiles128 = f8.blocks(2 * M) * f8.blocks(2 * N), f8.blocks(M) * f8.blocks(N)
+            for K in (128, 1024, 2048, 4096, 8192):
+                part, n = M * N * 4, K // 128
+                for dtype in (0, 1):
+                    parts = (min(256 // tiles64, n // 8) if tiles64 <= 512 else min(512 // tiles128, n // 8) if dtype == 0 else 1)
+                    if tiles64 <= 512 and parts == 2 and dtype == 1 and n < 32:
+                        parts = 1
+                    assert need(M, N, K, dtype) == (parts * part if parts > 1 else 0), (M, N, K, dtype)
