@@ -31,8 +31,6 @@ __global__ __launch_bounds__(JOIN_NT) void f8_join_kernel(F8Problem p, int split
     }
 }
 
-constexpr int64_t SPAN = int64_t(1) << 31;  // bytes that the offsets of scales may reach
-
 // Rows that DMA reads begin at multiples of 16 bytes; operands that lie otherwise are copied into a workspace first.
 bool a_aligned(const F8Problem &p) { return aligned16(p.a.q) && p.a.row % 16 == 0; }
 bool b_aligned(const F8Problem &p) { return aligned16(p.b.q) && (p.b.step != 1 ? p.b.step : p.b.row) % 16 == 0 && p.b_stack % 16 == 0; }
@@ -134,7 +132,7 @@ bool tile_takes(const F8Problem &p) {
     if (a.step != 1 || b.type != REGTILE_F8_E4M3) return false;
     if (!addr::f8_reach(false, p.slots != nullptr ? p.a_rows : 256, p.K, lda) || !addr::f8_reach(nn, 256, p.K, ldb)) return false;
     const int64_t all_a = p.slots != nullptr ? p.a_rows : p.M;
-    return ((all_a >> a.shift) * a.s_row + kb * a.s_col) * 4 < SPAN && (((int64_t)p.N >> b.shift) * b.s_row + kb * b.s_col) * 4 < SPAN;
+    return addr::f8_scales_reach(all_a >> a.shift, a.s_row, kb, a.s_col) && addr::f8_scales_reach((int64_t)p.N >> b.shift, b.s_row, kb, b.s_col);
 }
 
 struct Plan {

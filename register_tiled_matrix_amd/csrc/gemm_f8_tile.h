@@ -107,12 +107,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
                                         addr::f8_span(gather ? p.a_rows : w.used, w.a.row, K));
         const rsrc_t b_rsrc = NN ? make_rsrc(w.b.q + n0, addr::f8_span(K, w.b.step, p.N - n0))
                                  : make_rsrc(w.b.q + (int64_t)n0 * w.b.row, addr::f8_span(n_rows, w.b.row, K));
-        constexpr uint32_t NOWHERE = 0x80000000u;  // behind every descriptor: nothing is read, zeros arrive
         uint32_t av[JA], bv[JB];
 #pragma unroll
         for (int j = 0; j < JA; ++j) {
-            const int q = wave * JA + j, row = addr::f8_row(q, lane), at = min(row, w.used - 1);
-            av[j] = row < w.used ? addr::f8_lane(q, lane, gather ? a_row(p, w, at) : at, w.a.row) : NOWHERE;
+            const int q = wave * JA + j, at = min(addr::f8_row(q, lane), w.used - 1);
+            av[j] = addr::f8_row_lane(q, lane, w.used, gather ? a_row(p, w, at) : at, w.a.row);
         }
 #pragma unroll
         for (int j = 0; j < JB; ++j) {
@@ -120,14 +119,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
             if constexpr (NN)
                 bv[j] = addr::f8_nn_lane<BN>(q, lane, n_rows, w.b.step);
             else
-                bv[j] = addr::f8_row(q, lane) < n_rows ? addr::f8_lane(q, lane, addr::f8_row(q, lane), w.b.row) : NOWHERE;
+                bv[j] = addr::f8_row_lane(q, lane, n_rows, addr::f8_row(q, lane), w.b.row);
         }
         // scales: a wave brings 64 rows' of A or 64 columns' of B
         static_assert(BM % 64 == 0, "a wave's scales are all of one operand");
         const bool sa_wave = wave * 64 < BM || wave >= SC;
         const int si = sa_wave ? min((wave < SC ? wave * 64 : 0) + lane, w.used - 1) : min(n0 + wave * 64 - BM + lane, p.N - 1);
-        const int64_t s_at = sa_wave ? (a_row(p, w, si) >> w.a.shift) * w.a.s_row : (int64_t)(si >> w.b.shift) * w.b.s_row;
-        const uint32_t sv = (uint32_t)(s_at * 4), s_step = uniform((int)((sa_wave ? w.a.s_col : w.b.s_col) * 4));
+        const uint32_t sv = sa_wave ? addr::f8_scale_lane(a_row(p, w, si) >> w.a.shift, w.a.s_row)
+                                    : addr::f8_scale_lane(si >> w.b.shift, w.b.s_row);
+        const int s_step = uniform(addr::f8_scale_step(sa_wave ? w.a.s_col : w.b.s_col));
         const rsrc_t s_rsrc = make_rsrc(sa_wave ? w.a.s : w.b.s, 0x7FFFFFFFu);
 
         constexpr int PIECES = JA + JB + 1;
@@ -143,7 +143,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void f8_tile_kernel(F8Problem p, i
             else if (n < JA + JB)
                 dma16_buf(b_rsrc, bv[n - JA], addr::f8_block(NN, kb, w.b.step), to + BM * BLOCK + (wave * JB + n - JA) * 1024);
             else
-                dma4_buf(s_rsrc, sv, kb * s_step, to + (BM + BN) * BLOCK + wave * 256);
+                dma4_buf(s_rsrc, sv, addr::f8_scale_block(kb, s_step), to + (BM + BN) * BLOCK + wave * 256);
         };
 
         // ---- one block ----

@@ -213,6 +213,12 @@ REGTILE_HD int f8_row(int q, int lane) { return q * 8 + (lane >> 3); }
 REGTILE_HD int f8_chunk(int q, int lane) { return (lane & 7) ^ slab_key<8, 16>(f8_row(q, lane)); }
 // `row`: the operand's row (from the descriptor's base) that LDS row f8_row(q, lane) is loaded from
 REGTILE_HD uint32_t f8_lane(int q, int lane, int64_t row, int64_t ld) { return (uint32_t)(row * ld) + f8_chunk(q, lane) * 16; }
+// ... or, past the operand's last row in the tile, behind every descriptor: nothing is read and zeros arrive. (Blocks' offsets,
+// which are below 2^31 too, do not take it past 2^32.)
+constexpr uint32_t F8_NOWHERE = 0x80000000u;
+REGTILE_HD uint32_t f8_row_lane(int q, int lane, int rows, int64_t row, int64_t ld) {
+    return f8_row(q, lane) < rows ? f8_lane(q, lane, row, ld) : F8_NOWHERE;
+}
 template <int BN>
 REGTILE_HD int f8_nn_key(int row) {
     static_assert(BN == 64 || BN == 128 || BN == 256, "4, 8 or 16 chunks a row");
@@ -235,6 +241,14 @@ REGTILE_HD uint32_t f8_block(bool nn, int kb, int64_t ld) { return nn ? (uint32_
 // gathered), or K rows of a K x N operand
 REGTILE_HD bool f8_reach(bool nn, int64_t rows, int64_t K, int64_t ld) {
     return (nn ? (K + 128) * ld + 256 : rows * ld + K + 128) < (int64_t(1) << 31);
+}
+// Scales, 4 bytes a lane: a row of theirs and a uniform block, and the operands whose offsets stay within reach (`rows`: all the
+// operand's rows of scales, `blocks`: of k)
+REGTILE_HD uint32_t f8_scale_lane(int64_t row, int64_t s_row) { return (uint32_t)(row * s_row * 4); }
+REGTILE_HD int f8_scale_step(int64_t s_col) { return (int)(s_col * 4); }
+REGTILE_HD uint32_t f8_scale_block(int kb, int step) { return (uint32_t)(kb * step); }
+REGTILE_HD bool f8_scales_reach(int64_t rows, int64_t s_row, int64_t blocks, int64_t s_col) {
+    return (rows * s_row + blocks * s_col) * 4 < (int64_t(1) << 31);
 }
 // The register-staged kernel's gather of an M/N-contiguous operand with `cols` columns goes
 // through a per-slab descriptor (8-byte runs) when this holds, else through predicated loads.
