@@ -86,14 +86,21 @@ class F8Matrix:
     ``codes``: rows x cols (or stack x rows x cols) of ``torch.float8_e4m3fn`` or ``torch.float8_e5m2`` with unit
     column stride. ``scales``: float32, ceil(rows / block_rows) x ceil(cols / 128) (in a stack: of each), any
     strides. ``block_rows``: 1 (activations) or 128 (weights). ``t()`` is the transposed view: the same bytes,
-    taken as cols x rows. The tensors are kept, not copied. Products are fastest where rows of codes start at
-    multiples of 16 bytes (``quantize_f8`` lays them out so) and scales of one block of columns are contiguous.
+    taken as cols x rows. The tensors are kept, not copied, and described anew where a call finds that their storage has been
+    replaced. Products are fastest where rows of codes start at multiples of 16 bytes (``quantize_f8`` lays them out so) and
+    scales of one block of columns are contiguous.
     """
 
-    __slots__ = ("codes", "scales", "block_rows", "type", "transposed", "_rows", "_cols", "_stack", "_c", "_at")
+    __slots__ = ("codes", "scales", "block_rows", "type", "transposed", "_rows", "_cols", "_stack", "_c", "_address", "_codes_at", "_scales_at")
 
     def __init__(self, codes, scales, block_rows=1, transposed=False):
+        self.codes, self.scales, self.block_rows, self.transposed = codes, scales, block_rows, bool(transposed)
+        self._rows = None
+        self._describe()
+
+    def _describe(self):
         torch = _torch or _import_torch()
+        codes, scales, block_rows = self.codes, self.scales, self.block_rows
         kind = _types.get(codes.dtype)
         if kind is None:
             raise ValueError("codes must be float8_e4m3fn or float8_e5m2")
@@ -116,12 +123,22 @@ class F8Matrix:
             raise ValueError("codes and scales are on different devices")
         ld = max(strides[-2], cols, 1)
         _rt._ints(rows, cols, ld, stack)
+        now = rows, cols, stack if dim == 3 else 0, kind
+        if self._rows is not None and (self._rows, self._cols, self._stack, self.type) != now:
+            raise ValueError("the matrix's codes were replaced by some of another shape or type")
         s = scales.stride()
-        self.codes, self.scales, self.block_rows, self.type, self.transposed = codes, scales, block_rows, kind, bool(transposed)
-        self._rows, self._cols, self._stack = rows, cols, stack if dim == 3 else 0
-        self._c = MatrixStruct(codes.data_ptr(), ld, scales.data_ptr(), s[-2], s[-1], strides[0] if dim == 3 else 0,
+        self._rows, self._cols, self._stack, self.type = now
+        self._codes_at, self._scales_at = codes.data_ptr(), scales.data_ptr()
+        self._c = MatrixStruct(self._codes_at, ld, self._scales_at, s[-2], s[-1], strides[0] if dim == 3 else 0,
                                s[0] if dim == 3 else 0, rows, cols, stack, kind, block_rows)
-        self._at = ctypes.addressof(self._c)
+        self._address = ctypes.addressof(self._c)
+
+    @property
+    def _at(self):
+        """The address of its regtile_f8_matrix."""
+        if self.codes.data_ptr() != self._codes_at or self.scales.data_ptr() != self._scales_at:
+            self._describe()
+        return self._address
 
     @property
     def shape(self):
@@ -136,7 +153,8 @@ class F8Matrix:
     def t(self):
         v = object.__new__(F8Matrix)
         v.codes, v.scales, v.block_rows, v.type, v.transposed = self.codes, self.scales, self.block_rows, self.type, not self.transposed
-        v._rows, v._cols, v._stack, v._c, v._at = self._rows, self._cols, self._stack, self._c, self._at
+        v._rows, v._cols, v._stack, v._c, v._address = self._rows, self._cols, self._stack, self._c, self._address
+        v._codes_at, v._scales_at = self._codes_at, self._scales_at
         return v
 
     def __repr__(self):
@@ -153,8 +171,9 @@ def _new_matrix(like, dtype, rows, cols, block_rows):
     scales = m.scales = like.new_empty_strided((br, bc), (1, br or 1), dtype=_torch.float32)
     m.block_rows, m.type, m.transposed = block_rows, _types[dtype], False
     m._rows, m._cols, m._stack = rows, cols, 0
-    m._c = MatrixStruct(codes.data_ptr(), ld, scales.data_ptr(), 1, br or 1, 0, 0, rows, cols, 1, m.type, block_rows)
-    m._at = ctypes.addressof(m._c)
+    m._codes_at, m._scales_at = codes.data_ptr(), scales.data_ptr()
+    m._c = MatrixStruct(m._codes_at, ld, m._scales_at, 1, br or 1, 0, 0, rows, cols, 1, m.type, block_rows)
+    m._address = ctypes.addressof(m._c)
     return m
 
 
@@ -299,9 +318,10 @@ def _run_gemm(A, B, C, alpha, beta, dtype, dt, M, N, ldc, handle):
     if C is None:
         C = A.codes.new_empty((M, N), dtype=dtype)
     ta, tb = (1 if A.transposed else 0), (1 if B.transposed else 0)
+    a, b = A._at, B._at
     # (a few rows go without)
-    work, at, size = _workspace(A, 0 if M <= 16 and tb else lib.regtile_gemm_f8_workspace(ta, tb, A._at, B._at, dt, ldc))
-    status = lib.regtile_gemm_f8(ta, tb, alpha, A._at, B._at, beta, dt, C.data_ptr(), ldc, at, size, handle)
+    work, at, size = _workspace(A, 0 if M <= 16 and tb else lib.regtile_gemm_f8_workspace(ta, tb, a, b, dt, ldc))
+    status = lib.regtile_gemm_f8(ta, tb, alpha, a, b, beta, dt, C.data_ptr(), ldc, at, size, handle)
     if status:
         _rt._check(status)
     return C
@@ -385,9 +405,10 @@ def expert_rows_size(tokens, k, experts, align=1):
 class ExpertRows:
     """The rows that experts work on: the slots t * k + j in the order of their experts, each expert's from a multiple of
     ``align`` on (include/regtile.h). ``slots`` (rows), ``position`` (tokens x k), ``offsets`` (experts + 1) and
-    ``counts`` (experts) are contiguous int32 tensors on one device; they are kept, not copied."""
+    ``counts`` (experts) are contiguous int32 tensors on one device; they are kept, not copied, and described anew where a call
+    finds that their storage has been replaced."""
 
-    __slots__ = ("tokens", "k", "experts", "align", "rows", "device", "_parts", "_c", "_at")
+    __slots__ = ("tokens", "k", "experts", "align", "rows", "device", "_parts", "_parts_at", "_c", "_address")
 
     def __init__(self, slots, position, offsets, counts, align=1):
         _torch or _import_torch()
@@ -395,21 +416,30 @@ class ExpertRows:
             raise ValueError("position must be tokens x k, counts one number for each expert, align at least 1")
         tokens, k = position.shape
         experts = counts.shape[0]
-        rows = expert_rows_size(tokens, k, experts, align)
-        device = slots.device
-        _int32(slots, "slots", device, (rows,))
-        _int32(position, "position", device, (tokens, k))
-        _int32(offsets, "offsets", device, (experts + 1,))
-        _int32(counts, "counts", device, (experts,))
-        self._set((slots, position, offsets, counts), [t.data_ptr() for t in (slots, position, offsets, counts)], device, tokens, k, experts,
-                  align, rows)
+        self._parts, self.device = (slots, position, offsets, counts), slots.device
+        self.tokens, self.k, self.experts, self.align, self.rows = tokens, k, experts, align, expert_rows_size(tokens, k, experts, align)
+        self._describe()
 
-    def _set(self, parts, at, device, tokens, k, experts, align, rows):
-        self._parts, self.device = parts, device
-        self.tokens, self.k, self.experts, self.align, self.rows = tokens, k, experts, align, rows
-        self._c = RowsStruct(*at, tokens, k, experts, align, rows)
-        self._at = ctypes.addressof(self._c)
-        return self
+    def _describe(self):
+        for t, name, shape in zip(self._parts, ("slots", "position", "offsets", "counts"),
+                                  ((self.rows,), (self.tokens, self.k), (self.experts + 1,), (self.experts,))):
+            _int32(t, name, self.device, shape)
+        self._set([t.data_ptr() for t in self._parts])
+
+    def _set(self, at):
+        self._parts_at = at
+        self._c = RowsStruct(*at, self.tokens, self.k, self.experts, self.align, self.rows)
+        self._address = ctypes.addressof(self._c)
+
+    @property
+    def _at(self):
+        """The address of its regtile_expert_rows. (Parts that nobody has asked for are as they were made.)"""
+        parts = self._parts
+        if type(parts) is tuple:
+            a, b, c, d = self._parts_at
+            if parts[0].data_ptr() != a or parts[1].data_ptr() != b or parts[2].data_ptr() != c or parts[3].data_ptr() != d:
+                self._describe()
+        return self._address
 
     def _part(self, i):
         """slots, position, offsets or counts; the four lie in one tensor until one of them is asked for."""
@@ -457,9 +487,11 @@ def _run_rows(experts, tokens, k, n_experts, align, rows, handle):
     start = (used + 3) // 4 * 4
     parts = experts.new_empty(start + (size + 3) // 4 if size else used)
     at = parts.data_ptr()
-    r = object.__new__(ExpertRows)._set(parts, (at, at + 4 * rows, at + 4 * (rows + n), at + 4 * (rows + n + n_experts + 1)), experts.device,
-                                        tokens, k, n_experts, align, rows)
-    status = lib.regtile_order_experts(experts.data_ptr(), r._at, at + 4 * start if size else None, size, handle)
+    r = object.__new__(ExpertRows)
+    r._parts, r.device = parts, experts.device
+    r.tokens, r.k, r.experts, r.align, r.rows = tokens, k, n_experts, align, rows
+    r._set((at, at + 4 * rows, at + 4 * (rows + n), at + 4 * (rows + n + n_experts + 1)))
+    status = lib.regtile_order_experts(experts.data_ptr(), r._address, at + 4 * start if size else None, size, handle)
     if status:
         _rt._check(status)
     return r
@@ -493,8 +525,9 @@ def _run_experts(A, B, rows, C, gather, alpha, beta, dtype, dt, N, ldc, handle):
     if C is None:
         C = A.codes.new_empty((rows.rows, N), dtype=dtype)
     lib, tb = _lib(), 1 if B.transposed else 0
-    work, at, size = _workspace(A, lib.regtile_gemm_f8_experts_workspace(rows._at, gather, tb, A._at, B._at, dt))
-    status = lib.regtile_gemm_f8_experts(rows._at, gather, tb, alpha, A._at, B._at, beta, dt, C.data_ptr(), ldc, at, size, handle)
+    r, a, b = rows._at, A._at, B._at
+    work, at, size = _workspace(A, lib.regtile_gemm_f8_experts_workspace(r, gather, tb, a, b, dt))
+    status = lib.regtile_gemm_f8_experts(r, gather, tb, alpha, a, b, beta, dt, C.data_ptr(), ldc, at, size, handle)
     if status:
         _rt._check(status)
     return C
@@ -523,8 +556,9 @@ def _run_experts_dw(A, B, rows, C, alpha, beta, dtype, dt, M, N, ldc, handle):
     if C is None:
         C = A.codes.new_empty((rows.experts, M, N), dtype=dtype)
     lib = _lib()
-    work, at, size = _workspace(A, lib.regtile_gemm_f8_experts_dw_workspace(rows._at, A._at, B._at, dt))
-    status = lib.regtile_gemm_f8_experts_dw(rows._at, alpha, A._at, B._at, beta, dt, C.data_ptr(), ldc, C.stride(0), at, size, handle)
+    r, a, b = rows._at, A._at, B._at
+    work, at, size = _workspace(A, lib.regtile_gemm_f8_experts_dw_workspace(r, a, b, dt))
+    status = lib.regtile_gemm_f8_experts_dw(r, alpha, a, b, beta, dt, C.data_ptr(), ldc, C.stride(0), at, size, handle)
     if status:
         _rt._check(status)
     return C
