@@ -323,7 +323,9 @@ int regtile_dequantize_f8(const regtile_f8_matrix *Q, int dtype, void *X, int ld
  *   trans_a, trans_b (args 1-2), alpha (3), A (4), B (5), beta (6), c_dtype (7), C, ldc (8-9),
  *   work, work_bytes (10-11) a workspace as for regtile_gemm_bf16_mx, of which regtile_gemm_f8_workspace() bytes
  *   are made use of, stream (12)
- * alpha == 0 and beta == 0 as for gemm_f32. Every output is summed in a fixed order.
+ * alpha == 0 and beta == 0 as for gemm_f32. Every output is summed in a fixed order. Products that need the kernel for any
+ * operands (an e5m2 B, a transposed A, rows too far apart for 32-bit offsets, no room for copies) count up to 2^24 - 1 tiles of
+ * 64 x 64 in a launch: more of C is hipErrorInvalidConfiguration, C untouched.
  */
 int regtile_gemm_f8(int trans_a, int trans_b, float alpha, const regtile_f8_matrix *A, const regtile_f8_matrix *B, float beta,
                     int c_dtype, void *C, int ldc, void *work, int64_t work_bytes, void *stream);

@@ -320,7 +320,7 @@ def _run_gemm(A, B, C, alpha, beta, dtype, dt, M, N, ldc, handle):
     ta, tb = (1 if A.transposed else 0), (1 if B.transposed else 0)
     a, b = A._at, B._at
     # (a few rows go without)
-    work, at, size = _workspace(A, 0 if M <= 16 and tb else lib.regtile_gemm_f8_workspace(ta, tb, a, b, dt, ldc))
+    work, at, size = _workspace(A, 0 if M <= 16 and tb and N < 1 << 27 else lib.regtile_gemm_f8_workspace(ta, tb, a, b, dt, ldc))
     status = lib.regtile_gemm_f8(ta, tb, alpha, a, b, beta, dt, C.data_ptr(), ldc, at, size, handle)
     if status:
         _rt._check(status)

@@ -154,7 +154,9 @@ Plan plan_of(const F8Problem &p) {
     // here: 1 token x 2 of 8 experts (4096 x 4096) 13.0, 9.3; x 6 of 64 (4096 x 2048) 12.7, 12.2; 4 x 6 of 64 27.7, 32.0;
     // 8 x 2 of 8 21.1, 30.4; 32 x 6 of 64 96.6, 106.
     const int64_t weights = (int64_t)p.N * p.K, group = rows ? p.mean_rows : p.M;
-    if (p.b.step == 1 && (dense || rows)) {
+    // (a launch counts 2^23 of its workgroups, which take 16 rows and 16 columns or more)
+    const int64_t most_token = most_row_tiles(p, 16) * (((int64_t)p.N + 15) / 16);
+    if (p.b.step == 1 && (dense || rows) && most_token < 1 << 23) {
         plan.kernel = Plan::TOKEN;
         if (dense && p.M <= 16) return plan.shape = 11, plan;
         // (32x4096x4096 9.0, on 64 x 64 tiles 10.0; 32x4096x8192 14.4, 11.7; 48x1024x4096 8.4, 9.3; 64x4096x4096 12.0, 11.1,
