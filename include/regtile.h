@@ -392,8 +392,8 @@ int regtile_route_experts_grad(int score, int dtype, int tokens, int experts, in
  *   work, work_bytes (11-12) as for regtile_gemm_f8, stream (13)
  * regtile_gemm_f8_experts_dw -- the gradient of each expert's matrix: C_e = alpha A[:, group e] B[:, group e]^T +
  * beta C_e, with A (M x rows) and B (N x rows) quantised transposed, blocks along the rows; rows->align has to be a
- * multiple of 128. Columns behind a group's count are left out, whatever their codes (their blocks' scales have to
- * be finite).
+ * multiple of 128, and there are at most 65535 experts. Columns behind a group's count are left out, whatever their
+ * codes (their blocks' scales have to be finite).
  *   rows (arg 1), alpha (2), A (3), B (4), beta (5), c_dtype (6), C, ldc, c_stack (7-9: C_e at C + e * c_stack
  *   elements), work, work_bytes (10-11), stream (12)
  * Accuracy as for regtile_gemm_f8.

@@ -130,7 +130,7 @@ hipError_t launch_f8_any(const F8Problem &p, hipStream_t s, const char **name) {
                                             {"f8_any_64x64x128_e5m2_e4m3", "f8_any_64x64x128_e5m2_e5m2"}};
     *name = names[p.a.type][p.b.type];
     const int64_t tiles_n = ((int64_t)p.N + T - 1) / T, tiles = most_row_tiles(p, T) * tiles_n;
-    if (tiles * NT > 0xFFFFFFFFll || p.experts > 65535) return hipErrorInvalidConfiguration;
+    if (tiles * NT > 0xFFFFFFFFll || (p.mode == F8Problem::DEPTH && p.experts > 65535)) return hipErrorInvalidConfiguration;
     static void (*const kernels[2][2])(F8Problem, int, bool) = {{f8_any_kernel<0, 0>, f8_any_kernel<0, 1>},
                                                                 {f8_any_kernel<1, 0>, f8_any_kernel<1, 1>}};
     const auto f = kernels[p.a.type][p.b.type];

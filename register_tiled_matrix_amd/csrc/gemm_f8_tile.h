@@ -403,7 +403,7 @@ template <int WM, int WN, int MI, int NI, int STAGES, bool EXACT, int TA, bool N
 hipError_t launch_tile(const F8Problem &p, hipStream_t s, int splits) {
     constexpr int BM = WM * MI * 16, BN = WN * NI * 16, NT = 64 * WM * WN;
     const int64_t tiles_m = most_row_tiles(p, BM), tiles_n = ((int64_t)p.N + BN - 1) / BN, grid = tiles_m * tiles_n * splits;
-    if (grid * NT > 0xFFFFFFFFll || p.experts > 65535) return hipErrorInvalidConfiguration;
+    if (grid * NT > 0xFFFFFFFFll || (p.mode == F8Problem::DEPTH && p.experts > 65535)) return hipErrorInvalidConfiguration;
     const int blocks = (p.K + BLOCK - 1) / BLOCK, per = blocks > 0 ? (blocks + splits - 1) / splits : 1;
     // tile rows that share B's panels: 8, in groups as many as a group has on the average (the others have another B)
     int group_m = 8;

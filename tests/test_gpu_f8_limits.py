@@ -1,4 +1,4 @@
-"""8-bit float products of more columns than one kind of launch counts."""
+"""8-bit float products of more columns, and of more experts, than one kind of launch counts."""
 from __future__ import annotations
 
 import numpy as np
@@ -29,3 +29,24 @@ def test_few_rows_times_many_columns(M, K):
     va = f8.decode(x.cpu().numpy(), X.scales.cpu().numpy(), f8.E4M3)
     vb = f8.decode_table(f8.E4M3)[w[at].cpu().numpy()] * W.scales[at // 128].double().cpu().numpy()
     assert_close(C[:, at], va @ vb.T, np.abs(va) @ np.abs(vb).T, rt.last_kernel())
+
+
+@pytest.mark.parametrize("K", [200, 208])
+def test_more_experts_than_a_grid_has_layers(K):
+    """70000 experts that share one matrix (a stack with stride 0), most of them without a row; rows that are aligned or not."""
+    E, T, N = 70000, 40, 130
+    rng = np.random.default_rng(1)
+    experts = np.sort(rng.choice(E, T, replace=False))
+    experts[-1] = E - 1
+    counts = np.zeros(E, np.int32)
+    counts[experts] = 1
+    gpu = lambda a: torch.from_numpy(np.ascontiguousarray(a)).int().cuda()
+    r = rt.ExpertRows(gpu(np.arange(T)), gpu(np.arange(T)[:, None]), gpu(np.r_[0, np.cumsum(counts)]), gpu(counts))
+    w = torch.randint(0, 100, (1, N, K), dtype=torch.uint8, device="cuda").view(E4).expand(E, N, K)
+    s = torch.rand(1, f8.blocks(N), f8.blocks(K), device="cuda").expand(E, -1, -1)
+    x = rt.F8Matrix(torch.randint(0, 100, (T, K), dtype=torch.uint8, device="cuda").view(E4), torch.rand(T, f8.blocks(K), device="cuda"))
+    C = rt.gemm_f8_experts(x, rt.F8Matrix(w, s, 128).t(), r)
+    one = rt.F8Matrix(w[0], s[0], 128)
+    va = f8.decode(x.codes.view(torch.uint8).cpu().numpy(), x.scales.cpu().numpy(), f8.E4M3)
+    vb = f8.decode(one.codes.view(torch.uint8).cpu().numpy(), one.scales.cpu().numpy(), f8.E4M3, 128)
+    assert_close(C, va @ vb.T, np.abs(va) @ np.abs(vb).T, rt.last_kernel())
