@@ -39,6 +39,13 @@ __device__ __forceinline__ void store_value(void *p, int dtype, int64_t at, floa
         static_cast<_Float16 *>(p)[at] = (_Float16)x;
 }
 
+// LDS that lanes of one wave hand to each other: what stands before is done before what stands behind. (A wave's LDS instructions
+// run in order; this keeps the compiler from exchanging them, and costs none.)
+__device__ __forceinline__ void lds_step() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // The largest x of the wave, in every lane
 __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -148,7 +155,7 @@ __global__ __launch_bounds__(NT) void route_kernel(RouteProblem p) {
                 const int e = i * 64 + lane;
                 if (e < p.experts) mine[e + e / per] = key[i];
             }
-            __builtin_amdgcn_wave_barrier();
+            lds_step();
             // the two best of each group: `sub` lanes to a group, then over those
             int sub = 64;
             while (sub * p.groups > 64) sub >>= 1;
@@ -391,7 +398,7 @@ __device__ __forceinline__ void count_chunk(const OrderProblem &p, int *counts, 
         const int e = e_of[i];
         const u64 m = same(e, bits);
         if (e < p.experts && __ffsll((unsigned long long)m) - 1 == lane) mine[e] += __popcll(m);
-        __builtin_amdgcn_wave_barrier();
+        lds_step();
     }
     __syncthreads();
 }
@@ -481,9 +488,9 @@ __global__ __launch_bounds__(ORDER_NT) void order_place_kernel(OrderProblem p, i
             const u64 m = same(e, bits);
             int at = -1;
             if (e < p.experts) at = mine[e] + __popcll(m & ((1ull << lane) - 1));
-            __builtin_amdgcn_wave_barrier();
+            lds_step();
             if (e < p.experts && 63 - __clzll((long long)m) == lane) mine[e] = at + 1;
-            __builtin_amdgcn_wave_barrier();
+            lds_step();
             if (slot < end) {
                 p.position[slot] = at;
                 if (at >= 0) p.slots[at] = (int32_t)slot;
