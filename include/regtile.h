@@ -340,7 +340,7 @@ int64_t regtile_gemm_f8_workspace(int trans_a, int trans_b, const regtile_f8_mat
  *   offsets   [experts + 1] the first row of each group, and the end of the last one's room
  *   counts    [experts]     its slots
  *   rows = regtile_expert_rows_size(tokens, k, experts, align): what any choice fits into (-1 for sizes that pass
- *   2^31 - 1). All arrays on the device.
+ *   2^31 - 1). All arrays on the device. Here and below, arrays of 32-bit numbers begin at multiples of 4 bytes.
  */
 typedef struct regtile_expert_rows {
     const int32_t *slots, *position, *offsets, *counts;

@@ -13,7 +13,7 @@ constexpr int64_t INT_LIMIT = 0x7FFFFFFFll;
 
 bool bad_dtype(int d) { return d != REGTILE_MX_F32 && d != REGTILE_MX_BF16 && d != REGTILE_MX_F16; }
 bool misaligned(const void *p, int dtype) { return (reinterpret_cast<uintptr_t>(p) & (dtype == REGTILE_MX_F32 ? 3u : 1u)) != 0; }
-int64_t blocks(int64_t n) { return (n + regtile::f8::BLOCK - 1) / regtile::f8::BLOCK; }
+bool misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }  // 32-bit numbers
 
 // A described matrix (or stack of at least `stack`) whose elements are used if `used`
 bool bad_matrix(const regtile_f8_matrix *m, bool used, int stack) {
@@ -22,7 +22,7 @@ bool bad_matrix(const regtile_f8_matrix *m, bool used, int stack) {
     if (m->block_rows != 1 && m->block_rows != regtile::f8::BLOCK) return true;
     if (m->ld < m->cols || m->ld > INT_LIMIT) return true;
     if (m->scale_row < 0 || m->scale_col < 0 || m->codes_stack < 0 || m->scales_stack < 0) return true;
-    if ((reinterpret_cast<uintptr_t>(m->scales) & 3u) != 0) return true;
+    if (misaligned(m->scales)) return true;
     return used && m->rows > 0 && m->cols > 0 && (m->codes == nullptr || m->scales == nullptr);
 }
 
@@ -45,6 +45,7 @@ bool bad_rows(const regtile_expert_rows *r) {
     // (the size of what passes 2^31 - 1 is -1: a caller may have stored it)
     if (r->rows < 0 || r->rows != regtile_expert_rows_size(r->tokens, r->k, r->experts, r->align)) return true;
     if (r->offsets == nullptr || r->counts == nullptr) return true;
+    if (misaligned(r->slots) || misaligned(r->position) || misaligned(r->offsets) || misaligned(r->counts)) return true;
     return r->rows > 0 && (r->slots == nullptr || r->position == nullptr);
 }
 
@@ -131,7 +132,7 @@ int regtile_quantize_f8(int dtype, int transpose, int rows, int cols, const void
     const bool some = Q != nullptr && Q->rows > 0 && Q->cols > 0;
     if ((some && rows > 0 && X == nullptr) || misaligned(X, dtype)) return -5;
     if (ldx < (cols > 1 ? cols : 1)) return -6;
-    if ((reinterpret_cast<uintptr_t>(index) & 3u) != 0) return -7;
+    if (misaligned(index)) return -7;
     if (bad_matrix(Q, true, 1) || (transpose && Q->block_rows != 1)) return -8;
     if ((transpose ? Q->rows : Q->cols) != cols || (index == nullptr && (transpose ? Q->cols : Q->rows) != rows)) return -8;
     return convert(true, dtype, transpose, rows, cols, const_cast<void *>(X), ldx, index, Q, stream);
@@ -193,7 +194,7 @@ int64_t regtile_order_experts_workspace(int tokens, int k, int experts) {
 int regtile_order_experts(const int32_t *chosen, const regtile_expert_rows *rows, void *work, int64_t work_bytes, void *stream) {
     if (bad_rows(rows) || rows->experts > 1024) return -2;
     const int64_t n = (int64_t)rows->tokens * rows->k;
-    if (n > 0 && chosen == nullptr) return -1;
+    if ((n > 0 && chosen == nullptr) || misaligned(chosen)) return -1;
     if ((reinterpret_cast<uintptr_t>(work) & 15u) != 0) return -3;
     if (work_bytes < regtile::order_work_bytes(n, rows->experts) || (work == nullptr && work_bytes != 0)) return -4;
     regtile::OrderProblem p;
@@ -302,8 +303,9 @@ int regtile_route_experts(int score, int dtype, int tokens, int experts, int k, 
     if (renormalize != 0 && renormalize != 1) return -9;
     if ((tokens > 0 && logits == nullptr) || misaligned(logits, dtype)) return -11;
     if (ldl < experts) return -12;
-    if (tokens > 0 && chosen == nullptr) return -14;
-    if (tokens > 0 && weights == nullptr) return -15;
+    if (misaligned(bias)) return -13;
+    if ((tokens > 0 && chosen == nullptr) || misaligned(chosen)) return -14;
+    if ((tokens > 0 && weights == nullptr) || misaligned(weights)) return -15;
     if (tokens == 0) return regtile::quick();
     regtile::RouteProblem p = {};
     p.tokens = tokens;
@@ -338,8 +340,8 @@ int regtile_route_experts_grad(int score, int dtype, int tokens, int experts, in
     if (renormalize != 0 && renormalize != 1) return -6;
     if ((tokens > 0 && logits == nullptr) || misaligned(logits, dtype)) return -8;
     if (ldl < experts) return -9;
-    if (tokens > 0 && chosen == nullptr) return -10;
-    if (tokens > 0 && dweights == nullptr) return -11;
+    if ((tokens > 0 && chosen == nullptr) || misaligned(chosen)) return -10;
+    if ((tokens > 0 && dweights == nullptr) || misaligned(dweights)) return -11;
     if ((tokens > 0 && dlogits == nullptr) || misaligned(dlogits, dtype)) return -12;
     if (ldd < experts) return -13;
     if (tokens == 0) return regtile::quick();
@@ -371,6 +373,7 @@ int regtile_combine_experts(const regtile_expert_rows *rows, int dtype, int n, c
     const bool some = n > 0 && rows->tokens > 0;
     if ((some && Y == nullptr) || misaligned(Y, dtype)) return -4;
     if (ldy < (n > 1 ? n : 1)) return -5;
+    if (misaligned(weights)) return -6;
     if ((some && out == nullptr) || misaligned(out, dtype)) return -7;
     if (ldo < (n > 1 ? n : 1)) return -8;
     if (!some) return regtile::quick();
@@ -402,8 +405,10 @@ int regtile_combine_experts_grad(const regtile_expert_rows *rows, int dtype, int
     if (ldd < (n > 1 ? n : 1)) return -5;
     if ((some && dweights != nullptr && Y == nullptr) || misaligned(Y, dtype)) return -6;
     if (dweights != nullptr && ldy < (n > 1 ? n : 1)) return -7;
+    if (misaligned(weights)) return -8;
     if ((some && dY == nullptr) || misaligned(dY, dtype)) return -9;
     if (lddy < (n > 1 ? n : 1)) return -10;
+    if (misaligned(dweights)) return -11;
     if (rows->rows == 0 || (n == 0 && dweights == nullptr)) return regtile::quick();
     regtile::CombineProblem p = {};
     p.tokens = rows->tokens;
