@@ -253,11 +253,13 @@ def _operands(name, A, B, stack=None):
     """Checks what every product checks; (M, K, N)."""
     if not isinstance(A, F8Matrix) or not isinstance(B, F8Matrix):
         raise ValueError(f"{name} takes F8Matrix operands")
-    if A.codes.dim() != 2 or B.codes.dim() != (2 if stack is None else 3):
+    a, b = A.codes, B.codes
+    if a.dim() != 2 or b.dim() != (2 if stack is None else 3):
         raise ValueError(f"{name}: A is a single matrix" + (" and so is B" if stack is None else ", B a stack of them"))
     if stack is not None and B._stack != stack:
         raise ValueError(f"{name}: B must be a stack of {stack} matrices, not {B._stack}")
-    if not A.codes.is_cuda or B.codes.device != A.codes.device:
+    index = a.get_device()  # (a number: -1 on the host)
+    if index < 0 or b.get_device() != index:
         raise ValueError(f"{name} takes device tensors, all on one device")
     if (A.transposed and A.block_rows == 1) or (not B.transposed and B.block_rows == 1):
         raise ValueError(f"{name}: blocks of 1 x {F8_BLOCK} must run along k (a row-major A, a transposed B); "
