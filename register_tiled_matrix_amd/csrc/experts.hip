@@ -15,7 +15,7 @@
 //
 // combine and its gradient move each row once: a token's columns go over a workgroup's threads with 4 rows under way, the
 // gradient takes a wave to a row. 8192 tokens x 8 of 2048 bf16: 73 us forward and 123 back, where a copy of as many bytes takes 56
-// and 106. The router (64 tokens of 256 experts 8.4 us, 8192 of 64 7.5, the gradient 6.2) and the order (512 slots of 256 experts
+// and 106. The router (64 tokens of 256 experts 8.4 us, 8192 of 64 7.5, the gradient 6.5) and the order (512 slots of 256 experts
 // 5.7 us, 65536 of 64 6.2 to count and 12.3 to place) are bound by their chains of latencies, not by bytes.
 #include "f8_common.h"
 

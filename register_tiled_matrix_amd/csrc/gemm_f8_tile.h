@@ -17,9 +17,9 @@
 // transposing reads (8 k of 16 columns for 16 lanes).
 //
 // What bounds it: 8192^3 of e4m3 into bf16 takes 418-429 us (2560-2630 TFLOP/s; the library's product with one scale a matrix
-// 377): at 1.9 GHz the matrix pipes are busy two thirds of the time, and the rest is the sums' 4 vector instructions a tile,
-// LDS reads of fragments and the last store of each round of tiles. With an fp32 C 900-955 us: expanding codes
-// takes as many issue slots as the bf16 MFMAs. Few columns of k a tile (2048) add what a tile costs at its ends, 7 us.
+// 377): the matrix pipes are busy 62% of the time, at 1.85 GHz, and the rest is the sums' 4 vector instructions a tile, LDS reads
+// of fragments and the last store of each round of tiles. With an fp32 C 880-955 us: expanding codes takes as many issue
+// slots as the bf16 MFMAs. Few columns of k a tile (2048) add what a tile costs at its ends, 7 us.
 //
 // Edges: rows past the last are not loaded and are zeros, chunks past N come from the last one that holds an element. What
 // lies past K in the last block (bytes between rows, or zeros from behind the descriptor) is overwritten with

@@ -5,7 +5,8 @@
 // 16 MF rows; wave w takes the blocks w, w + 8, ... of 128 k, U of them under way, so that a workgroup reads
 // 1 KB of each column at a time. Codes are expanded and summed exactly, whatever C's type (the matrix pipes have time).
 // The waves' sums are added through LDS in their order. Bound by the latency of its loads, and by the weights' bytes where
-// they come from memory: 1x4096x4096 5.9 us (16.8 MB, 2.8 TB/s), 16x8192x8192 18.8 (67 MB, 3.6 TB/s).
+// they come from memory: 1x4096x4096 5.9 us (16.8 MB, 2.8 TB/s), 16x8192x8192 18.8 from the cache and
+// 23.7 from memory (67 MB, 2.8 TB/s), each wave's loads and products in turn.
 #include "f8_common.h"
 
 namespace regtile {
